@@ -90,6 +90,10 @@ extern "C" {
 #define MOE_ERR_BAD_IDS           -7  /* device: an expert id outside [0, E) */
 #define MOE_ERR_BAD_SCALE         -8  /* device: an e8m0 scale byte of 255 (NaN) */
 #define MOE_ERR_NO_DEVICE         -9  /* current device is not sm_103 (GB300) */
+#define MOE_ERR_BAD_LENGTHS      -10  /* device: a request's length is negative or does not fit */
+#define MOE_ERR_NO_PAGES         -11  /* device: the list of free pages is too short */
+#define MOE_ERR_BAD_PARENT       -12  /* device: a drafted token's parent is not an earlier one */
+#define MOE_ERR_BAD_PAGE         -13  /* device: a page id or slot outside the cache */
 
 /* moe_shape.flags */
 #define MOE_POST_NORM    1u  /* per-pick RMSNorm of y before the weighted sum */
@@ -306,6 +310,125 @@ int moe_latent_forward(const moe_latent_shape* shape, const void* x, const void*
                        const void* w_sgu, const void* w_sd,
                        int32_t* ids, float* weights, float* out,
                        void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The cache side of the verify step: what stands before the block in a layer.
+ * One call feeds the next: moe_kv_plan (once a step) lays out where the new
+ * tokens of every request go, moe_kv_append (a layer) writes their K and V rows
+ * into the paged cache, moe_tree_attention (a layer) reads the cache.
+ *
+ * A batch holds B requests.  Request b has c_b = ctx_len[b] tokens in the cache
+ * and brings n_b new ones: one token, a prompt or a part of one (a chain), or
+ * a tree of drafted tokens.  The new tokens' rows of all requests stand one
+ * after the other: request b owns rows row_start[b] .. row_start[b+1]-1, and
+ * its row i is token c_b + i of its sequence in the cache.  Either count may be
+ * zero.  The lengths are read on the device only, so no call waits for the GPU
+ * and a captured graph serves any lengths that fit the shape.
+ *
+ * The cache is one K and one V tensor of pages of `page` tokens: element
+ * (p, h, o, e) of either is at p * page_stride + h * head_stride +
+ * o * token_stride + e.  Token a of request b is at offset a % page of page
+ * block_table[b, a / page]; its slot is that page's id * page + a % page.
+ * Entries are bf16, or with MOE_KV_E4M3 e4m3 codes (OCP 8-bit floating point)
+ * that stand for code * scale, one positive fp32 scale a K/V head for K and one for V.
+ */
+#define MOE_KV_E4M3 1u  /* moe_kv_shape.flags: e4m3 cache */
+
+/*
+ * Supported: 1 <= B <= 4096; 1 <= T <= 1<<20; D 64 or 128; Hq a multiple of
+ * Hkv with Hq / Hkv <= 128, Hq <= 4096; page a multiple of 8 up to 1024;
+ * n_pages * page < 1<<31; max_pages * page <= 1<<30; 0 <= W <= 32; scale finite and > 0.
+ * A stride of 0 is the packed one: cache [n_pages][Hkv][page][D], rows Hq * D and Hkv * D;
+ * other strides are positive and cover a row (multiples of 16 bytes).
+ */
+typedef struct moe_kv_shape {
+    int32_t B;             /* requests */
+    int32_t T;             /* rows of new tokens the arrays hold */
+    int32_t Hq, Hkv, D;    /* query heads, K/V heads, head width */
+    int32_t page;          /* tokens a page */
+    int32_t n_pages;       /* pages of the cache */
+    int32_t max_pages;     /* columns of the block table */
+    int32_t W;             /* 32-bit mask words a row; 0: chains, no mask */
+    uint32_t flags;        /* MOE_KV_E4M3 */
+    float scale;           /* factor of q . k before the softmax */
+    int64_t page_stride, head_stride, token_stride;  /* cache, in elements */
+    int64_t q_stride;      /* elements from one row of q to the next */
+    int64_t kv_stride;     /* elements from one row of k_new (v_new) to the next */
+} moe_kv_shape;
+
+/*
+ * Workspace size of the three calls in *bytes (pure host function).  Prepared
+ * once with moe_workspace_init; errors found on the device are reported by
+ * moe_device_status as for the block's calls.
+ */
+int moe_kv_workspace_bytes(const moe_kv_shape* shape, size_t* bytes);
+
+/*
+ * Block tables, slot maps, positions and tree masks from request lengths, in
+ * one launch.  A request's pages are those its block-table row already holds
+ * (the first ceil(c_b / page) entries) and then pages of the free list, taken
+ * in request order.
+ *   ctx_len, n_new [B]       int32
+ *   parents   [T]            int32, or NULL (chains; W must be 0): the row of
+ *                            its request a drafted token follows, an earlier
+ *                            one, or -1 (it follows token c_b - 1)
+ *   free_pages [n_free]      int32 page ids (may be NULL when n_free is 0)
+ *   block_table [B, max_pages]  int32, in and out: entries ceil(c_b / page) ..
+ *                            ceil((c_b + n_b) / page) - 1 are written
+ *   row_start [B + 1]        int32 out
+ *   slots     [T]            int64 out, positions [T] int32 out: c_b + the
+ *                            depth in the tree (the row number in a chain);
+ *                            both -1 in rows that no request owns
+ *   mask      [T, W]         uint32 out (NULL when parents is): bit j % 32 of
+ *                            word j / 32 of a row is set when row j of its
+ *                            request is the row itself or an ancestor
+ *   used      [2]            int32 out: rows owned, free pages taken
+ * Device errors: MOE_ERR_BAD_LENGTHS (detail: the request; a negative length,
+ * more tokens than the block table or, in a tree, the mask holds: the request
+ * gets no rows; detail B: more than T rows, the last are cut off),
+ * MOE_ERR_NO_PAGES (detail: pages missing; entries and slots are -1),
+ * MOE_ERR_BAD_PARENT (detail: the row; its walk ends there), MOE_ERR_BAD_PAGE (detail:
+ * the id; slots in that page are -1).
+ */
+int moe_kv_plan(const moe_kv_shape* shape, const int32_t* ctx_len, const int32_t* n_new,
+                const int32_t* parents, const int32_t* free_pages, int32_t n_free,
+                int32_t* block_table, int32_t* row_start, int64_t* slots, int32_t* positions,
+                uint32_t* mask, int32_t* used, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The new tokens' K and V rows into the cache: k_new, v_new [T, Hkv, D] bf16
+ * (rows kv_stride apart) to slots [T] (distinct; a negative slot's row is
+ * skipped, one past the cache is skipped and latches MOE_ERR_BAD_PAGE).
+ * k_scale, v_scale [Hkv] fp32 with MOE_KV_E4M3 (else NULL): a code is
+ * x / scale, rounded to nearest even and saturated at +-448.
+ */
+int moe_kv_append(const moe_kv_shape* shape, const void* k_new, const void* v_new, const int64_t* slots,
+                  const float* k_scale, const float* v_scale, void* k_cache, void* v_cache,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their own K and V
+ * already).  Row i of request b sees the c_b cached tokens and those of its
+ * request's new ones its mask row names (W = 0: rows 0..i).  For query head h
+ * over K/V head h / (Hq / Hkv), with x_j = scale * q . k_j over the keys seen:
+ *   lse = ln sum_j exp(x_j),   out = sum_j exp(x_j - lse) v_j
+ * A row that sees nothing (a score of -inf counts as not seen) gets out 0 and
+ * lse -inf; rows that no request owns are not written.  What a row does not
+ * see does not reach it, whatever it holds (NaN included).  Sums and the softmax's maximum and
+ * sum are fp32; the weights enter the second product as bf16 (e4m3 cache: as
+ * two e4m3 terms, as q does, like bf16).
+ *   q [T, Hq, D] bf16 (rows q_stride apart); block_table [B, max_pages],
+ *   ctx_len [B], row_start [B + 1], mask [T, W] (NULL when W is 0) as
+ *   moe_kv_plan leaves them; k_scale, v_scale [Hkv] with MOE_KV_E4M3 (else
+ *   NULL); out [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL.
+ * Device errors: MOE_ERR_BAD_LENGTHS (detail: the request, which gets no
+ * output), MOE_ERR_BAD_PAGE (detail: the id; that request's output is
+ * unspecified), MOE_ERR_TIMEOUT.
+ */
+int moe_tree_attention(const moe_kv_shape* shape, const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_table, const int32_t* ctx_len, const int32_t* row_start,
+                       const uint32_t* mask, const float* k_scale, const float* v_scale,
+                       void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, returns the status latched in the workspace by the

@@ -24,15 +24,21 @@ MOE_ERR_TIMEOUT = -6
 MOE_ERR_BAD_IDS = -7
 MOE_ERR_BAD_SCALE = -8
 MOE_ERR_NO_DEVICE = -9
+MOE_ERR_BAD_LENGTHS = -10
+MOE_ERR_NO_PAGES = -11
+MOE_ERR_BAD_PARENT = -12
+MOE_ERR_BAD_PAGE = -13
 
 MOE_POST_NORM = 1
 MOE_LOGIT_OFFSET = 2
+MOE_KV_E4M3 = 1
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_abi_version", "moe_strerror", "moe_workspace_bytes", "moe_workspace_init",
            "moe_route", "moe_experts", "moe_forward", "moe_forward_host", "moe_device_status",
            "moe_timing_enable", "moe_timing_collect", "moe_kernel_name", "moe_forward_noalloc",
-           "moe_workspace_region", "moe_latent_workspace_bytes", "moe_latent_forward")
+           "moe_workspace_region", "moe_latent_workspace_bytes", "moe_latent_forward",
+           "moe_kv_workspace_bytes", "moe_kv_plan", "moe_kv_append", "moe_tree_attention")
 
 # workspace regions (moe_workspace_region)
 MOE_WS_STATUS, MOE_WS_POS, MOE_WS_TILES, MOE_WS_XQ, MOE_WS_XS, MOE_WS_HQ, MOE_WS_HS, MOE_WS_Y, MOE_WS_LOGITS = range(9)
@@ -58,6 +64,22 @@ class LatentShape(ctypes.Structure):
     @classmethod
     def of(cls, S, H, LAT, E, k, I, SI, logit_offset=False, norm_eps=1e-6):
         return cls(S, H, LAT, E, k, I, SI, MOE_LOGIT_OFFSET if logit_offset else 0, norm_eps)
+
+
+class KVShape(ctypes.Structure):
+    """moe_kv_shape: a batch of requests over a paged K/V cache.  Strides are in
+    elements, 0 the packed layout (cache [n_pages, Hkv, page, D])."""
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("W", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("kv_stride", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, B, T, Hq, Hkv, D, page, n_pages, max_pages, mask_words=0, e4m3=False, scale=None, page_stride=0,
+           head_stride=0, token_stride=0, q_stride=0, kv_stride=0):
+        return cls(B, T, Hq, Hkv, D, page, n_pages, max_pages, mask_words, MOE_KV_E4M3 if e4m3 else 0,
+                   D ** -0.5 if scale is None else scale, page_stride, head_stride, token_stride, q_stride, kv_stride)
 
 
 class MoEError(RuntimeError):
@@ -106,6 +128,11 @@ def load_library(path: str) -> ctypes.CDLL:
     _LSP = ctypes.POINTER(LatentShape)
     L.moe_latent_workspace_bytes.argtypes = [_LSP, ctypes.POINTER(ctypes.c_size_t)]
     L.moe_latent_forward.argtypes = [_LSP] + [_P] * 17 + [ctypes.c_size_t, _P]
+    _KSP = ctypes.POINTER(KVShape)
+    L.moe_kv_workspace_bytes.argtypes = [_KSP, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_kv_plan.argtypes = [_KSP] + [_P] * 4 + [ctypes.c_int32] + [_P] * 7 + [ctypes.c_size_t, _P]
+    L.moe_kv_append.argtypes = [_KSP] + [_P] * 8 + [ctypes.c_size_t, _P]
+    L.moe_tree_attention.argtypes = [_KSP] + [_P] * 12 + [ctypes.c_size_t, _P]
     L.moe_timing_enable.argtypes = [ctypes.c_int]
     L.moe_timing_collect.argtypes = [_P, _P, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     L.moe_kernel_name.argtypes = [ctypes.c_int]
@@ -166,8 +193,11 @@ def read_region(shape: MoEShape, ws, region: int, dtype=None):
 
 def new_workspace(shape: MoEShape, device="cuda", stream=None):
     """A device workspace (uint8 tensor, 256-byte aligned) prepared by moe_workspace_init."""
+    return _workspace(workspace_bytes(shape), device, stream)
+
+
+def _workspace(nbytes, device, stream):
     import torch
-    nbytes = workspace_bytes(shape)
     buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % 256
     ws = buf[off:off + nbytes]
@@ -215,6 +245,40 @@ def latent_forward(shape, x, w_gate, bias, logit_off, w_ld, w13, w13s, w2, w2s, 
                                     _ptr(w_ld), _ptr(w13), _ptr(w13s), _ptr(w2), _ptr(w2s), _ptr(ln_w),
                                     _ptr(w_up), _ptr(w_sgu), _ptr(w_sd), _ptr(ids), _ptr(weights), _ptr(out),
                                     _ptr(ws), ws.numel(), _stream(stream)), "moe_latent_forward")
+
+
+def kv_workspace_bytes(shape: KVShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_kv_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "moe_kv_workspace_bytes")
+    return n.value
+
+
+def new_kv_workspace(shape: KVShape, device="cuda", stream=None):
+    """A device workspace (uint8 tensor, 256-byte aligned) of the cache calls, prepared by moe_workspace_init."""
+    return _workspace(kv_workspace_bytes(shape), device, stream)
+
+
+def kv_plan(shape, ctx_len, n_new, parents, free_pages, block_table, row_start, slots, positions, mask, used, ws,
+            stream=None) -> None:
+    _check(lib().moe_kv_plan(ctypes.byref(shape), _ptr(ctx_len), _ptr(n_new), _ptr(parents), _ptr(free_pages),
+                             0 if free_pages is None else free_pages.numel(), _ptr(block_table), _ptr(row_start),
+                             _ptr(slots), _ptr(positions), _ptr(mask), _ptr(used), _ptr(ws), ws.numel(),
+                             _stream(stream)), "moe_kv_plan")
+
+
+def kv_append(shape, k_new, v_new, slots, k_scale, v_scale, k_cache, v_cache, ws, stream=None) -> None:
+    _check(lib().moe_kv_append(ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(k_scale),
+                               _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_kv_append")
+
+
+def tree_attention(shape, q, k_cache, v_cache, block_table, ctx_len, row_start, mask, k_scale, v_scale, out, lse, ws,
+                   stream=None) -> None:
+    """Attention of the new tokens over the cache; lse may be None."""
+    _check(lib().moe_tree_attention(ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                    _ptr(ctx_len), _ptr(row_start), _ptr(mask), _ptr(k_scale), _ptr(v_scale),
+                                    _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_tree_attention")
 
 
 def device_status(ws, stream=None) -> tuple[int, int]:

@@ -86,7 +86,7 @@ static int check_ws(const moe_shape* s, void* ws, size_t ws_bytes) {
     return MOE_OK;
 }
 
-static int check_device() {
+int check_device() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return MOE_ERR_NO_DEVICE; }
     int major = 0, minor = 0;
@@ -98,7 +98,7 @@ static int check_device() {
     return (major == 10 && minor == 3) ? MOE_OK : MOE_ERR_NO_DEVICE;
 }
 
-static int cuda_rc(cudaError_t e) {
+int cuda_rc(cudaError_t e) {
     if (e == cudaSuccess) return MOE_OK;
     fprintf(stderr, "libmoe: CUDA error %d (%s)\n", (int)e, cudaGetErrorString(e));
     return MOE_ERR_CUDA;
@@ -217,6 +217,10 @@ const char* moe_strerror(int code) {
         case MOE_ERR_BAD_IDS: return "expert id out of range or repeated within a token";
         case MOE_ERR_BAD_SCALE: return "e8m0 scale byte 255 (NaN)";
         case MOE_ERR_NO_DEVICE: return "no sm_103 device";
+        case MOE_ERR_BAD_LENGTHS: return "request length negative or too long";
+        case MOE_ERR_NO_PAGES: return "free page list too short";
+        case MOE_ERR_BAD_PARENT: return "drafted token's parent is not an earlier token";
+        case MOE_ERR_BAD_PAGE: return "page id or slot outside the cache";
         default: return "unknown status";
     }
 }
