@@ -117,6 +117,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
     }
 }
 
+// The same with a short spin before the clock is read and the warp suspended
+// (for waits on a critical path, or that mostly find the phase complete).
+__device__ __forceinline__ bool mbar_wait_warp_fast(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                                    uint64_t limit_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, abort, limit_ns);
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tiled, 2-D) and L2 policies
 // ---------------------------------------------------------------------------
@@ -384,20 +394,27 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Shared-memory matrix descriptor with a swizzle of SW = 128 or 64 bytes.
+// Shared-memory matrix descriptors with a swizzle of SW = 128 or 64 bytes,
+// version 1: the upper 32 bits are a constant of the layout; the lower hold the
+// address and lbo, both in 16-byte units, so that a step along K is one 32-bit add.
 // K-major: rows of SW bytes, 8-row groups SW * 8 bytes apart (lbo unused).
 // MN-major: SW bytes of consecutive MN elements a K index, 8-K groups SW * 8
 // bytes apart, the next SW bytes of MN elements lbo bytes further.
 template <int SW>
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo) {
+__device__ __forceinline__ uint64_t smem_desc(uint32_t lo) {
     static_assert(SW == 128 || SW == 64, "swizzle width");
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((SW * 8) >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)(SW == 128 ? 2u : 4u) << 61;
+    constexpr uint32_t hi = (uint32_t)((SW * 8) >> 4) | 1u << 14 | (SW == 128 ? 2u : 4u) << 29;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
     return d;
+}
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | lbo >> 4 << 16; }
+
+// One lane of a warp that is whole (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Instruction descriptor, fp32 accumulator, A K-major, B K-major or MN-major:
@@ -489,6 +506,58 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// 32 lanes x 16 columns, all set to v
+__device__ __forceinline__ void tmem_st16_rep(uint32_t taddr, uint32_t v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr),
+        "r"(v)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8_rep(uint32_t taddr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr), "r"(v)
+                 : "memory");
+}
+
+// pairs of fp32 in a 64-bit register
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two fp32 as two e4m3 pairs: hi (the leading 4 significant bits) and lo (the
+// next 4 of what hi leaves), by way of f16, which holds 11.
+__device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    uint32_t h, g;
+    uint16_t p, q;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(h));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(g) : "h"(p));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(g));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(q) : "r"(h));
+    hi = p;
+    lo = q;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -21,8 +21,9 @@
 // K/V tile serves both; with one, the streams take alternate key tiles and are
 // added at the segment's end.
 //
-// Warps: 0 TMA producer (K, V by page boxes; Q), 1 MMA issuer, 2 cleans V
-// tiles that hold keys some row does not see, 4-7 and 8-11 the softmax.
+// Warps: 0 TMA producer (K, V by page boxes; Q), 1 and 3 MMA issuers (one a
+// stream), 2 cleans V tiles that hold keys some row does not see, 4-7 and 8-11
+// the softmax.
 #include "kv.cuh"
 #include "tc_ptx.cuh"
 
@@ -56,7 +57,7 @@ struct ACfg {
 
 // shared-memory tables behind the tiles
 struct AMisc {
-    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_full[2], p_full[2], o_full, o_free, san[16], ml_full, qs_full;
+    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_full[2], p_full[2], o_full, o_free, san[16], ml_full, qs_full, drain[2];
     uint32_t tmem;
     int abort;
     int first_b;
@@ -168,6 +169,96 @@ __device__ __forceinline__ bool row_sees(const KvDims& d, const AttnArgs& a, int
     return (ld_dep(a.mask + (int64_t)row * d.W + (j >> 5)) >> (j & 31)) & 1;
 }
 
+// The weights are relative to a maximum m (kept as mc = m c) that follows the
+// true one only when that is LAZY ahead, so that O is rescaled rarely; P stays
+// below 2^(base + LAZY).  An e4m3 P is held above that format's smallest steps
+// (2^-9): 2^5 at the maximum, at most 2^8 of 448.
+template <bool E4M3>
+__host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
+
+// One thread's row of a tile: its 128 scores at t_s become weights in their
+// place, o (the row of O at t_o) is rescaled when the maximum moves.  Sums and
+// maxima run in four chains of pairs, so that no chain of dependent
+// operations is longer than 16.
+template <int D, bool E4M3>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, bool part, const uint32_t* vis,
+                                             bool have_o, float& mc, float& l) {
+    constexpr float LAZY = E4M3 ? 3.f : 8.f;
+    float s[4][32];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ptx::tmem_ld32(t_s + 32 * k, s[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ptx::tmem_ld_wait32(s[k]);
+    if (part) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[k][x] = (vis[k] >> x) & 1 ? s[k][x] : -CUDART_INF_F;
+    }
+    float tops[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        tops[k] = fmaxf(s[k][0], s[k][1]);
+#pragma unroll
+        for (int x = 2; x < 32; x += 2) tops[k] = ptx::max3(tops[k], s[k][x], s[k][x + 1]);
+    }
+    const float top = fmaxf(ptx::max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+    const bool first = mc == -CUDART_INF_F;
+    const bool move = first || top > mc + LAZY;
+    // (a first maximum finds nothing but zeros in its row of O)
+    const float f = move && !first ? ptx::ex2(mc - top) : 1.f;
+    if (move) mc = top;
+    if (have_o && __any_sync(0xffffffffu, move && !first)) {
+#pragma unroll
+        for (int x = 0; x < D; x += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(t_o + x, o);
+            ptx::tmem_ld_wait16(o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            ptx::tmem_st16(t_o + x, o);
+        }
+    }
+    const float off = mc == -CUDART_INF_F ? 0.f : p_base<E4M3>() - mc;
+    const uint64_t c2 = ptx::pack2(c, c), off2 = ptx::pack2(off, off);
+    uint64_t sum[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t u[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+            float a, b;
+            ptx::unpack2(ptx::fma2(ptx::pack2(s[k][x], s[k][x + 1]), c2, off2), a, b);
+            a = ptx::ex2(a);
+            b = ptx::ex2(b);
+            const uint64_t e = ptx::pack2(a, b);
+            sum[k] = x == 0 ? e : ptx::add2(sum[k], e);
+            s[k][x] = a;
+            s[k][x + 1] = b;
+        }
+        if (E4M3) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                uint32_t h0, h1, l0, l1;
+                ptx::split_e4m3x2(s[k][4 * x], s[k][4 * x + 1], h0, l0);
+                ptx::split_e4m3x2(s[k][4 * x + 2], s[k][4 * x + 3], h1, l1);
+                u[x] = h0 | h1 << 16;
+                u[8 + x] = l0 | l1 << 16;
+            }
+            ptx::tmem_st8(t_s + 8 * k, u);
+            ptx::tmem_st8(t_s + 32 + 8 * k, u + 8);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) u[x] = ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
+            ptx::tmem_st16(t_s + 16 * k, u);
+        }
+    }
+    float a, b;
+    ptx::unpack2(ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3])), a, b);
+    l = l * f + (a + b);
+    ptx::tmem_st_wait();
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(A_THREADS, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
@@ -188,16 +279,17 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
             ptx::mbar_init(&m->full[i], 1);
-            ptx::mbar_init(&m->empty[i], 1);
+            ptx::mbar_init(&m->empty[i], 2);
             ptx::mbar_init(&m->san[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&m->q_full[i], E4M3 ? 8 : 1);
-            ptx::mbar_init(&m->q_empty[i], 1);
+            ptx::mbar_init(&m->q_empty[i], 2);
+            ptx::mbar_init(&m->drain[i], 1);
             ptx::mbar_init(&m->s_full[i], 1);
             ptx::mbar_init(&m->p_full[i], 4);
         }
-        ptx::mbar_init(&m->o_full, 1);
+        ptx::mbar_init(&m->o_full, 2);
         ptx::mbar_init(&m->o_free, 8);
         ptx::mbar_init(&m->ml_full, 8);
         ptx::mbar_init(&m->qs_full, 8);
@@ -289,7 +381,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             auto load = [&](const CUtensorMap* tm, int j, int pg, int off) {
                 const uint32_t s = seq % C::NS;
                 const int key = (w.k0 + j) * KT + bi * t.box;
-                if (!ptx::mbar_wait_warp(&m->empty[s], ((seq / C::NS) & 1) ^ 1, abort_flag, A_WAIT_NS)) return false;
+                if (!ptx::mbar_wait_warp_fast(&m->empty[s], ((seq / C::NS) & 1) ^ 1, abort_flag, A_WAIT_NS)) return false;
                 if (lane == 0) {
                     const int left = total - (w.k0 + j) * KT;
                     const int boxes = left >= KT ? nb : (left + t.box - 1) / t.box;
@@ -311,7 +403,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 const int nt = w.ntok(pt) > t.tpt ? 2 : 1;
                 for (int i = 0; i < nt && ok; ++i, ++nq) {
                     const uint32_t qb = nq & 1;
-                    ok = ptx::mbar_wait_warp(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, abort_flag, A_WAIT_NS);
+                    ok = ptx::mbar_wait_warp_fast(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, abort_flag, A_WAIT_NS);
                     const int ntok = w.ntok(pt) - i * t.tpt;
                     const bool small = ntok <= t.qbox;
                     if (ok && lane == 0) {
@@ -344,93 +436,124 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // copies in flight land before the CTA's memory is given up
             const int none = 0;
             for (uint32_t i = seq > C::NS ? seq - C::NS : 0; i < seq; ++i)
-                ptx::mbar_wait_warp(&m->full[i % C::NS], (i / C::NS) & 1, &none, 10000000ull);
+                ptx::mbar_wait_warp_fast(&m->full[i % C::NS], (i / C::NS) & 1, &none, 10000000ull);
             for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq && !E4M3; ++i)
-                ptx::mbar_wait_warp(&m->q_full[i & 1], (i >> 1) & 1, &none, 10000000ull);
+                ptx::mbar_wait_warp_fast(&m->q_full[i & 1], (i >> 1) & 1, &none, 10000000ull);
         }
-    } else if (warp == 1) {
-        // ---- MMA issuer ---------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
-            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
-            uint32_t base = 0, nq = 0, n_s[2] = {0, 0}, n_seg = 0, san_phase = 0;   // san_phase: a bit a ring slot
-            bool ok = true;
-            const uint32_t sm0 = ptx::smem_u32(sm), ring0 = ptx::smem_u32(ring);
-            for (; more && ok; more = w.next(d, a, pt), ++n_seg) {
-                const int mt = w.k1 - w.k0;
-                const bool two = w.ntok(pt) > t.tpt;
-                const int cnt0 = two ? mt : (mt + 1) / 2, cnt1 = two ? mt : mt / 2;
-                auto tile = [&](int s, int i) { return two ? i : 2 * i + s; };
-                auto qk = [&](int s, int i) {
-                    const int j = tile(s, i);
-                    const uint32_t q = base + seq_k(j), slot = q % C::NS;
-                    if (i == 0 && (two || s == 0)) {
-                        const uint32_t n = nq + s;
-                        if (!ptx::mbar_wait(&m->q_full[n & 1], (n >> 1) & 1, abort_flag, A_WAIT_NS)) return false;
-                    }
-                    if (!ptx::mbar_wait(&m->full[slot], (q / C::NS) & 1, abort_flag, A_WAIT_NS)) return false;
-                    ptx::tc_fence_after();
-                    const uint32_t qa = sm0 + ((nq + (two ? s : 0)) & 1) * C::QT, kb = ring0 + slot * C::SLOT;
-                    const uint32_t dst = tmem + C::T_S + s * 128;
+    } else if (warp == 1 || warp == 3) {
+        // ---- MMA issuers: warp 1 for stream 0, warp 3 for stream 1 ---------
+        // The whole warp walks and waits, one lane issues: descriptors built
+        // from values that are the same in the whole warp stay in uniform
+        // registers, and a product costs a few instructions.  An issuer waits
+        // for, and releases, every tile of the ring, also those that only the
+        // other stream uses, so that neither can be two phases ahead of or
+        // behind a barrier (a parity wait takes two phases for none).
+        constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
+        constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
+        const int s = warp >> 1;
+        uint32_t base = 0, nq = 0, n_p = 0, n_seg = 0, san_phase = 0;   // san_phase: a bit a ring slot
+        bool ok = true;
+        const uint32_t sm0 = ptx::smem_u32(sm), ring0 = ptx::smem_u32(ring);
+        const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
+        auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+        // Waits come before the one for P, which ends a tile's critical path:
+        // after it the products go out one after the other.
+        for (; more && ok; more = w.next(d, a, pt), ++n_seg) {
+            const int mt = w.k1 - w.k0;
+            const bool two = same(w.ntok(pt) > t.tpt);
+            bool first = true;
+            const uint32_t qb = same((nq + (two ? s : 0)) & 1);
+            const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
+            ok = ptx::mbar_wait_warp_fast(&m->q_full[qb], ((nq + (two ? s : 0)) >> 1) & 1, abort_flag, A_WAIT_NS);
+            // the previous segment's O is read before the first product into it
+            auto k_ready = [&](int j, uint32_t& slot) {
+                const uint32_t q = base + seq_k(j);
+                slot = same(q % C::NS);
+                return ptx::mbar_wait_warp_fast(&m->full[slot], (q / C::NS) & 1, abort_flag, A_WAIT_NS);
+            };
+            auto v_ready = [&](int j, uint32_t& slot) {   // landed and clean
+                slot = same((base + seq_v(j, mt)) % C::NS);
+                const bool r =
+                    ptx::mbar_wait_warp_fast(&m->san[slot], (san_phase >> slot) & 1, abort_flag, A_WAIT_NS);
+                san_phase ^= 1u << slot;
+                return r;
+            };
+            // (one lane) S = Q K^T, and the slot's release
+            auto qk = [&](uint32_t slot, bool mine) {
+                if (mine) {
+                    const uint32_t kd = ptx::smem_desc_lo(ring0 + slot * C::SLOT, 16);
 #pragma unroll
                     for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
 #pragma unroll
                         for (int e = 0; e < D / C::KSTEP; ++e) {
-                            const uint32_t o = (e * 32) / C::SW * (128 * C::SW) + (e * 32) % C::SW;
-                            ptx::mma_ss<E4M3>(dst, ptx::smem_desc<C::SW>(qa + part * (C::QT / 2) + o, 16),
-                                              ptx::smem_desc<C::SW>(kb + o, 16), id_s, (part | e) ? 1u : 0u);
+                            const uint32_t o = ((e * 32) / C::SW * (128 * C::SW) + (e * 32) % C::SW) >> 4;
+                            ptx::mma_ss<E4M3>(t_s, ptx::smem_desc<C::SW>(qd + part * (C::QT / 2 >> 4) + o),
+                                              ptx::smem_desc<C::SW>(kd + o), id_s, (part | e) ? 1u : 0u);
                         }
                     }
                     ptx::mma_commit(&m->s_full[s]);
-                    if (!two || s == 1) ptx::mma_commit(&m->empty[slot]);
-                    return true;
-                };
-                auto pv = [&](int s, int i) {
-                    const int j = tile(s, i);
-                    const uint32_t q = base + seq_v(j, mt), slot = q % C::NS;
-                    if (!two || s == 0) {   // the tile has landed and is clean
-                        if (!ptx::mbar_wait(&m->san[slot], (san_phase >> slot) & 1, abort_flag, A_WAIT_NS)) return false;
-                        san_phase ^= 1u << slot;
-                    }
-                    if (!ptx::mbar_wait(&m->p_full[s], n_s[s] & 1, abort_flag, A_WAIT_NS)) return false;
-                    ++n_s[s];
-                    ptx::tc_fence_after();
-                    const uint32_t vb = ring0 + slot * C::SLOT, pa = tmem + C::T_S + s * 128;
-                    const uint32_t dst = tmem + C::T_O + s * 128;
-#pragma unroll
-                    for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
-#pragma unroll
-                        for (int e = 0; e < KT / C::KSTEP; ++e)
-                            ptx::mma_ts<E4M3>(dst, pa + part * 32 + e * 8,
-                                              ptx::smem_desc<C::SW>(vb + e * C::KSTEP * C::SW, KT * C::SW), id_o,
-                                              (i | part | e) ? 1u : 0u);
-                    }
-                    if (!two || s == 1) ptx::mma_commit(&m->empty[slot]);
-                    return true;
-                };
-                ok = qk(0, 0) && (cnt1 == 0 || qk(1, 0));
-                for (int i = 0; i < cnt0 && ok; ++i) {
-                    // the previous segment's O is read before the first product into it
-                    if (i == 0 && n_seg > 0)
-                        ok = ptx::mbar_wait(&m->o_free, (n_seg - 1) & 1, abort_flag, A_WAIT_NS);
-                    ok = ok && pv(0, i) && (i + 1 >= cnt0 || qk(0, i + 1));
-                    if (i < cnt1) ok = ok && pv(1, i) && (i + 1 >= cnt1 || qk(1, i + 1));
+                }
+                ptx::mma_commit(&m->empty[slot]);
+            };
+            // two query tiles: both streams take K0 V0 K1 V1 ...; one: stream j % 2
+            // takes tile j, in the order K0 K1 V0 K2 V1 ...
+            const int ahead = two ? 1 : 2;
+            uint32_t ks = 0, vs = 0;
+            for (int j = 0; j < ahead && j < mt && ok; ++j) {
+                ok = k_ready(j, ks);
+                ptx::tc_fence_after();
+                const bool mine = same(two || (j & 1) == s);
+                if (ok && ptx::elect_one()) qk(ks, mine);
+                __syncwarp();
+            }
+            if (ok && n_seg > 0) ok = ptx::mbar_wait_warp_fast(&m->o_free, (n_seg - 1) & 1, abort_flag, A_WAIT_NS);
+            for (int j = 0; j < mt && ok; ++j) {
+                const bool mine = same(two || (j & 1) == s);
+                const bool nx = same(j + ahead < mt);
+                ok = v_ready(j, vs) && (!nx || k_ready(j + ahead, ks));
+                const uint32_t vd = ptx::smem_desc_lo(ring0 + vs * C::SLOT, KT * C::SW);
+                const uint32_t add = same(!first);
+                if (mine && ok) {
+                    ok = ptx::mbar_wait_warp_fast(&m->p_full[s], n_p & 1, abort_flag, A_WAIT_NS);
+                    ++n_p;
+                    first = false;
                 }
                 if (!ok) break;
+                ptx::tc_fence_after();
+                if (ptx::elect_one()) {
+                    if (mine) {   // O += P V
+#pragma unroll
+                        for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
+#pragma unroll
+                            for (int e = 0; e < KT / C::KSTEP; ++e)
+                                ptx::mma_ts<E4M3>(t_o, t_s + part * 32 + e * 8,
+                                                  ptx::smem_desc<C::SW>(vd + (e * C::KSTEP * C::SW >> 4)), id_o,
+                                                  (part | e) ? 1u : add);
+                        }
+                    }
+                    ptx::mma_commit(&m->empty[vs]);
+                    if (nx) qk(ks, mine);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (ptx::elect_one()) {
                 ptx::mma_commit(&m->o_full);
-                // (every product of the segment is issued, those that read Q among them)
+                // (every product of this stream is issued, those that read Q among them)
                 ptx::mma_commit(&m->q_empty[nq & 1]);
                 if (two) ptx::mma_commit(&m->q_empty[(nq + 1) & 1]);
-                nq += two ? 2 : 1;
-                base += 2 * mt;
             }
-            if (!ok) {
-                fail(2);
-                // products in flight end before TMEM and shared memory are given up
-                const int none = 0;
-                ptx::mma_commit(&m->o_full);
-                ptx::mbar_wait(&m->o_full, n_seg & 1, &none, 10000000ull);
-            }
+            __syncwarp();
+            nq += two ? 2 : 1;
+            base += 2 * mt;
+        }
+        if (!ok) {
+            if (lane == 0) fail(2);
+            // products in flight end before TMEM and shared memory are given up
+            const int none = 0;
+            if (ptx::elect_one()) ptx::mma_commit(&m->drain[s]);
+            __syncwarp();
+            ptx::mbar_wait_warp(&m->drain[s], 0, &none, 10000000ull);
         }
     } else if (warp == 2) {
         // ---- V tiles with keys that some row does not see ------------------
@@ -451,7 +574,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 const int key0 = (w.k0 + j) * KT;
                 const uint32_t q = base + seq_v(j, mt), slot = q % C::NS;
                 for (; seen <= q && ok; ++seen)
-                    ok = ptx::mbar_wait_warp(&m->full[seen % C::NS], (seen / C::NS) & 1, abort_flag, A_WAIT_NS);
+                    ok = ptx::mbar_wait_warp_fast(&m->full[seen % C::NS], (seen / C::NS) & 1, abort_flag, A_WAIT_NS);
                 if (!ok) {
                     if (lane == 0) fail(3);
                     break;
@@ -573,17 +696,12 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_n(&m->q_full[qb], two ? 2 : 1);
                 if (lane == 0) ptx::mbar_arrive(&m->qs_full);
-                if (!ptx::mbar_wait_warp(&m->qs_full, n_seg & 1, abort_flag, A_WAIT_NS)) {   // the row scales are there
+                if (!ptx::mbar_wait_warp_fast(&m->qs_full, n_seg & 1, abort_flag, A_WAIT_NS)) {   // the row scales are there
                     if (lane == 0) fail(6);
                     break;
                 }
                 c *= q_scale[qb * 128 + row];
             }
-            // m: the maximum the weights are relative to, as m * c; it follows
-            // the true one only when that is over LAZY ahead, so that O is
-            // rescaled rarely (P stays below 2^BASE 2^LAZY).  An e4m3 P is held
-            // above that format's smallest steps: 2^BASE at the maximum.
-            constexpr float LAZY = E4M3 ? 3.f : 8.f, BASE = E4M3 ? 5.f : 0.f;
             float mc = -CUDART_INF_F, l = 0.f;
             for (int i = 0; i < cnt && ok; ++i) {
                 const int key0 = (w.k0 + (two ? i : 2 * i + g)) * KT;
@@ -614,92 +732,22 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         for (int k = 0; k < 4; ++k) vis[k] = __funnelshift_r(words[k], words[k + 1], j0 & 31);
                     }
                 }
-                if (!ptx::mbar_wait_warp(&m->s_full[g], n_s & 1, abort_flag, A_WAIT_NS)) {
+                if (!ptx::mbar_wait_warp_fast(&m->s_full[g], n_s & 1, abort_flag, A_WAIT_NS)) {
                     if (lane == 0) fail(4);
                     ok = false;
                     break;
                 }
                 ++n_s;
                 ptx::tc_fence_after();
-                if (live) {
-                    float s[4][32];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ptx::tmem_ld32(t_s + 32 * k, s[k]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ptx::tmem_ld_wait32(s[k]);
-                    if (part) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                s[k][x] = (vis[k] >> x) & 1 ? s[k][x] : -CUDART_INF_F;
-                    }
-                    float top = -CUDART_INF_F;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) top = fmaxf(top, s[k][x]);
-                    top *= c;
-                    const bool first = mc == -CUDART_INF_F;
-                    const bool move = first || top > mc + LAZY;
-                    // (a first maximum finds nothing but zeros in its row of O)
-                    const float f = move && !first ? ptx::ex2(mc - top) : 1.f;
-                    if (move) mc = top;
-                    l *= f;
-                    if (i > 0 && __any_sync(0xffffffffu, move && !first)) {
-                        const uint32_t t_o = tmem + lanes + C::T_O + g * 128;
-#pragma unroll
-                        for (int x = 0; x < D; x += 16) {
-                            uint32_t o[16];
-                            ptx::tmem_ld16(t_o + x, o);
-                            ptx::tmem_ld_wait16(o);
-#pragma unroll
-                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                            ptx::tmem_st16(t_o + x, o);
-                        }
-                    }
-                    const float off = mc == -CUDART_INF_F ? 0.f : BASE - mc;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            s[k][x] = ptx::ex2(fmaf(s[k][x], c, off));
-                            l += s[k][x];
-                        }
-                        uint32_t u[8], v[8];
-                        if (E4M3) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                float z[4];
-                                const float* const y = &s[k][4 * x];
-                                const uint32_t p0 = ptx::cvt_e4m3x2(y[0], y[1]), p1 = ptx::cvt_e4m3x2(y[2], y[3]);
-                                ptx::e4m3x2_to_f32(p0, z[0], z[1]);
-                                ptx::e4m3x2_to_f32(p1, z[2], z[3]);
-                                u[x] = p0 | p1 << 16;
-                                v[x] = ptx::cvt_e4m3x2(y[0] - z[0], y[1] - z[1]) |
-                                       ptx::cvt_e4m3x2(y[2] - z[2], y[3] - z[3]) << 16;
-                            }
-                            ptx::tmem_st8(t_s + 8 * k, u);
-                            ptx::tmem_st8(t_s + 32 + 8 * k, v);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                u[x] = ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
-                                v[x] = ptx::cvt_bf16x2(s[k][16 + 2 * x], s[k][17 + 2 * x]);
-                            }
-                            ptx::tmem_st8(t_s + 16 * k, u);
-                            ptx::tmem_st8(t_s + 16 * k + 8, v);
-                        }
-                    }
-                    ptx::tmem_st_wait();
-                }
+                if (live)
+                    softmax_tile<D, E4M3>(t_s, tmem + lanes + C::T_O + g * 128, c, part, vis, i > 0, mc, l);
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&m->p_full[g]);
             }
             if (!ok) break;
             nq += two ? 2 : 1;
-            if (!ptx::mbar_wait_warp(&m->o_full, n_seg & 1, abort_flag, A_WAIT_NS)) {
+            if (!ptx::mbar_wait_warp_fast(&m->o_full, n_seg & 1, abort_flag, A_WAIT_NS)) {
                 if (lane == 0) fail(5);
                 break;
             }
@@ -711,7 +759,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 m->ml[g][row] = make_float2(mc, l);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&m->ml_full);
-                if (!ptx::mbar_wait_warp(&m->ml_full, n_ml & 1, abort_flag, A_WAIT_NS)) {
+                if (!ptx::mbar_wait_warp_fast(&m->ml_full, n_ml & 1, abort_flag, A_WAIT_NS)) {
                     if (lane == 0) fail(7);
                     break;
                 }
@@ -790,10 +838,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (mine && (two || g == 0)) {
                     // log2 of the sum, without the weights' 2^BASE
                     if (!whole)
-                        t.part_ml[(int64_t)slot * t.rp + prow] = make_float2(top - BASE, sum);
+                        t.part_ml[(int64_t)slot * t.rp + prow] = make_float2(top - p_base<E4M3>(), sum);
                     else if (a.lse)
                         a.lse[(int64_t)grow * d.Hq + head] =
-                            sum == 0.f ? -CUDART_INF_F : (zero - BASE + log2f(sum)) * 0.69314718055994531f;
+                            sum == 0.f ? -CUDART_INF_F : (zero - p_base<E4M3>() + log2f(sum)) * 0.69314718055994531f;
                 }
             }
             if (warp == 4 && lane == 0 && w.k0 == 0 && !whole) {
