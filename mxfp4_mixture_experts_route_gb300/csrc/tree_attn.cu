@@ -21,9 +21,14 @@
 // K/V tile serves both; with one, the streams take alternate key tiles and are
 // added at the segment's end.
 //
-// Warps: 0 TMA producer (K, V by page boxes; Q), 1 and 3 MMA issuers (one a
-// stream), 2 cleans V tiles that hold keys some row does not see, 4-7 and 8-11
-// the softmax.
+// Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q, 1 and 3
+// MMA issuers (one a stream), 2 cleans V tiles that hold keys some row does not
+// see, 14 finds the CTA's segments and hands them to the others, 4-7 and 8-11
+// the softmax; 15 only keeps the register shares whole.
+//
+// Instructions come from a small cache, and a call's first pass through any code
+// waits for it line by line: what runs once a segment is written as loops, and
+// waits and error paths are calls.
 #include "kv.cuh"
 #include "tc_ptx.cuh"
 
@@ -32,12 +37,12 @@
 namespace moe {
 namespace {
 
-constexpr int A_THREADS = 384;
+constexpr int A_THREADS = 512;
 constexpr int A_CTAS = 152;                 // shares (SMs of a GB300)
 constexpr int KT = 128;                     // keys a tile
 constexpr int A_MISC = 3072;                // barriers and small tables
-constexpr uint64_t A_WAIT_NS = 2000000000ull;
-constexpr int SAN_SLOTS = 16;
+constexpr int SEGS = 4;                     // segments handed out ahead
+constexpr int NAN_SLOTS = 16;
 
 template <int D, bool E4M3>
 struct ACfg {
@@ -48,30 +53,43 @@ struct ACfg {
     static constexpr int QT = 128 * D * 2;                   // a query tile: bf16, or e4m3 hi and lo
     static constexpr int QMISC = E4M3 ? 1024 : 0;            // e4m3: row scales of two query tiles
     static constexpr int FIT = (232448 - A_MISC - QMISC - 2 * QT) / SLOT;
-    static constexpr int NS = FIT < 16 ? FIT : 16;           // ring slots
-    static constexpr int SMEM = 2 * QT + NS * SLOT + QMISC + A_MISC;
+    static constexpr int NK = FIT / 2 < 8 ? FIT / 2 : 8;     // slots of the K ring
+    static constexpr int NV = FIT - NK < 8 ? FIT - NK : 8;   // and of the V ring
+    static constexpr int SMEM = 2 * QT + (NK + NV) * SLOT + QMISC + A_MISC;
     static constexpr int KSTEP = E4M3 ? 32 : 16;             // K of one MMA
     // TMEM columns: S (P in its place) and O of each stream
     static constexpr uint32_t T_S = 0, T_O = 256;
 };
 
+// One segment's part in a CTA's share.
+struct Seg {
+    int b, h, c, n;             // request, K/V head, its cached and new tokens
+    int row0, tok0, ntok, kt;   // first row of the batch and token of the request, tokens, key tiles of the whole
+    int k0, k1, flags, last;    // this part's key tiles; SEG_*; last CTA that holds a part
+};
+constexpr int SEG_VALID = 1;    // (0: the share is done)
+constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read once
+
 // shared-memory tables behind the tiles
 struct AMisc {
-    uint64_t full[16], empty[16], q_full[2], q_empty[2], s_full[2], p_full[2], o_full, o_free, san[16], ml_full, qs_full, drain[2];
+    Seg seg[SEGS];
+    uint64_t seg_full[SEGS], seg_empty[SEGS];
+    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], v_clean[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+        o_full, o_free, ml_full, qs_full, wg[2], turn[2], drain[2];
     uint32_t tmem;
     int abort;
     int first_b;
-    int nan_seg[SAN_SLOTS];
+    int nan_seg[NAN_SLOTS];
     long long first_base, total;
-    long long warp_sum[A_THREADS / 32];
+    unsigned warp_sum[A_THREADS / 32];
     float2 ml[2][128];
 };
 static_assert(sizeof(AMisc) <= A_MISC, "misc");
 
 struct ATabs {
     int G, tpt;                 // heads a group, tokens a query tile
+    uint32_t g_inv;             // ceil(2^16 / G): r / G = r g_inv >> 16 for the rows r < 256 of a pair
     int box;                    // keys a TMA box: gcd(page, 128)
-    int qbox;                   // tokens of the small query box
     int rp;                     // rows a partial result holds
     float2* part_ml;            // [2 A_CTAS][rp]: m (log2 units), l
     float* part_o;              // [2 A_CTAS][rp][D]
@@ -91,83 +109,83 @@ struct Joint {
 
 __device__ __forceinline__ long long share_begin(long long total, int c) { return total * c / A_CTAS; }
 
+// ---------------------------------------------------------------------------
+// bounded waits, whole warps
+// ---------------------------------------------------------------------------
+// A try suspends the warp for up to a microsecond or so: some seconds in all.
+// A wait that runs out, or finds that another one did, leaves its number in
+// m->abort, and the kernel's end reports it.
+constexpr int WAIT_TRIES = 1 << 22;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, AMisc* m, int site) {
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i) {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity, 1000u))) return true;
+        if (*(volatile int*)&m->abort) return false;
+    }
+    *(volatile int*)&m->abort = site;
+    return false;
+}
+
+// ---------------------------------------------------------------------------
+// segments
+// ---------------------------------------------------------------------------
 // key tiles of query-tile pair p of a request
 __device__ __forceinline__ int pair_tiles(const KvDims& d, const KvReq& r, int p, int pt) {
     const int upto = d.W || (p + 1) * pt > r.n ? r.n : (p + 1) * pt;
     return (r.c + upto + KT - 1) / KT;
 }
-__device__ __forceinline__ long long request_tiles(const KvDims& d, const KvReq& r, int pt) {
+// key tiles of a request, a K/V head
+__device__ __forceinline__ long long head_tiles(const KvDims& d, const KvReq& r, int pt) {
     if (r.n == 0) return 0;
     const int np = (r.n + pt - 1) / pt;
+    if (d.W) return (long long)np * pair_tiles(d, r, 0, pt);
     long long s = 0;
-    if (d.W) {
-        s = (long long)np * pair_tiles(d, r, 0, pt);
-    } else {
-        for (int p = 0; p < np; ++p) s += pair_tiles(d, r, p, pt);
-    }
-    return s * d.Hkv;
+#pragma unroll 1
+    for (int p = 0; p < np; ++p) s += pair_tiles(d, r, p, pt);
+    return s;
 }
 
-// The walk of one CTA over its share's segments; every role walks by itself.
-struct Walk {
-    long long pos, end;
-    KvReq r;
-    int b, h, p, np, kt;
-    int k0, k1;                 // key tiles of the current segment's part
-    __device__ __forceinline__ bool start(const KvDims& d, const AttnArgs& a, const AMisc* m, int pt) {
-        pos = share_begin(m->total, blockIdx.x);
-        end = share_begin(m->total, blockIdx.x + 1);
-        if (pos >= end) return false;
-        b = m->first_b;
-        r = kv_request(d, a.ctx_len, a.row_start, b);
-        np = (r.n + pt - 1) / pt;
-        long long off = pos - m->first_base;
-        const long long a_head = request_tiles(d, r, pt) / d.Hkv;
-        h = (int)(off / a_head);
-        off -= h * a_head;
-        p = 0;
-        while (off >= (kt = pair_tiles(d, r, p, pt))) {
-            off -= kt;
-            ++p;
-        }
-        k0 = (int)off;
-        k1 = (int)(kt - k0 < end - pos ? kt : k0 + (end - pos));
-        return true;
+// The segments of a share, in order, one after the other from a warp that only
+// does this; every role takes them from the ring.
+struct SegIn {
+    uint32_t i = 0;
+    __device__ __forceinline__ bool next(AMisc* m, Seg& s) {
+        const uint32_t k = i % SEGS;
+        if (!wait(&m->seg_full[k], (i / SEGS) & 1, m, 1)) return false;
+        const int4* const p = reinterpret_cast<const int4*>(&m->seg[k]);
+        const int4 x = p[0], y = p[1], z = p[2];
+        s = Seg{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&m->seg_empty[k]);
+        ++i;
+        return s.flags & SEG_VALID;
     }
-    __device__ __forceinline__ bool next(const KvDims& d, const AttnArgs& a, int pt) {
-        pos += k1 - k0;
-        if (pos >= end) return false;
-        if (++p == np) {
-            p = 0;
-            if (++h == d.Hkv) {
-                h = 0;
-                do {
-                    r = kv_request(d, a.ctx_len, a.row_start, ++b);
-                } while (r.n == 0);
-                np = (r.n + pt - 1) / pt;
-            }
-        }
-        kt = pair_tiles(d, r, p, pt);
-        k0 = 0;
-        k1 = (int)(kt < end - pos ? kt : end - pos);
-        return true;
-    }
-    // the pair's tokens, and whether it has two query tiles
-    __device__ __forceinline__ int tok0(int pt) const { return p * pt; }
-    __device__ __forceinline__ int ntok(int pt) const { return r.n - p * pt < pt ? r.n - p * pt : pt; }
-    // keys below this one are seen by every row of the segment
-    __device__ __forceinline__ int all_see(const KvDims& d, int pt) const { return d.W ? r.c : r.c + p * pt + 1; }
 };
+// keys below this one are seen by every row of the segment
+__device__ __forceinline__ int all_see(const KvDims& d, const Seg& s) { return d.W ? s.c : s.c + s.tok0 + 1; }
 
-// ring position of K tile j and V tile j of a segment of m tiles:
-// K0 K1 V0 K2 V1 ... K(m-1) V(m-2) V(m-1), the order in which they are used
-__device__ __forceinline__ uint32_t seq_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ uint32_t seq_v(int j, int m) { return j == m - 1 ? 2 * m - 1 : 2 * j + 2; }
-
-__device__ __forceinline__ bool row_sees(const KvDims& d, const AttnArgs& a, int row, int i, int j) {
-    if (d.W == 0) return j <= i;
-    return (ld_dep(a.mask + (int64_t)row * d.W + (j >> 5)) >> (j & 31)) & 1;
+// How often a query tile's rows stand in the 128 rows of the product when they
+// are few: with 4 (or 2) copies, each warp of a warpgroup makes the weights of
+// a quarter (half) of the keys of its copy, instead of one warp those of all.
+// The others' weights in its copy are 0; the copies' O are added at the end.
+__device__ __forceinline__ int copies(int ntok, const ATabs& t) {
+    const int rows = ntok * t.G;
+    return ntok > t.tpt || rows > 64 ? 1 : rows > 32 ? 2 : 4;
 }
+
+__device__ __forceinline__ int by_g(int r, const ATabs& t) { return (int)(r * t.g_inv >> 16); }
+
+// A position in a ring of N slots, for whoever goes round it in order.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The weights are relative to a maximum m (kept as mc = m c) that follows the
 // true one only when that is LAZY ahead, so that O is rescaled rarely; P stays
@@ -176,40 +194,46 @@ __device__ __forceinline__ bool row_sees(const KvDims& d, const AttnArgs& a, int
 template <bool E4M3>
 __host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
 
-// One thread's row of a tile: its 128 scores at t_s become weights in their
-// place, o (the row of O at t_o) is rescaled when the maximum moves.  Sums and
-// maxima run in four chains of pairs, so that no chain of dependent
-// operations is longer than 16.
-template <int D, bool E4M3>
-__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, bool part, const uint32_t* vis,
-                                             bool have_o, float& mc, float& l) {
+// One thread's row and COLS keys: the scores at t_s become weights at t_p (bf16,
+// or the e4m3 terms hi at t_p and lo at t_lo), which may lie over them.  When
+// the maximum moves, the row of O at t_o is rescaled (no product into it is
+// under way).  half_done() is called once the first half of the weights has been
+// stored.  Sums and maxima run in chains of 32 columns and of pairs, so that
+// no chain of dependent operations is longer than 16.
+template <int D, bool E4M3, int COLS, class HalfDone>
+__device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_t t_lo, uint32_t t_o, float c, bool part,
+                                             const uint32_t* vis, bool have_o, HalfDone half_done, float& mc, float& l) {
     constexpr float LAZY = E4M3 ? 3.f : 8.f;
-    float s[4][32];
+    constexpr int N = COLS / 32;
+    float s[N][32], tops[2 * N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ptx::tmem_ld32(t_s + 32 * k, s[k]);
+    for (int k = 0; k < N; ++k) ptx::tmem_ld32(t_s + 32 * k, s[k]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) ptx::tmem_ld_wait32(s[k]);
+    for (int k = 0; k < N; ++k) ptx::tmem_ld_wait32(s[k]);
     if (part) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < N; ++k)
 #pragma unroll
             for (int x = 0; x < 32; ++x) s[k][x] = (vis[k] >> x) & 1 ? s[k][x] : -CUDART_INF_F;
     }
-    float tops[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        tops[k] = fmaxf(s[k][0], s[k][1]);
+    for (int k = 0; k < 2 * N; ++k) {
+        const float* const r = s[k / 2] + 16 * (k & 1);
+        tops[k] = fmaxf(r[0], r[1]);
 #pragma unroll
-        for (int x = 2; x < 32; x += 2) tops[k] = ptx::max3(tops[k], s[k][x], s[k][x + 1]);
+        for (int x = 2; x < 16; x += 2) tops[k] = ptx::max3(tops[k], r[x], r[x + 1]);
     }
-    const float top = fmaxf(ptx::max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+    float top = tops[0];
+#pragma unroll
+    for (int k = 1; k < 2 * N - 1; k += 2) top = ptx::max3(top, tops[k], tops[k + 1]);
+    top = fmaxf(top, tops[2 * N - 1]) * c;
     const bool first = mc == -CUDART_INF_F;
     const bool move = first || top > mc + LAZY;
     // (a first maximum finds nothing but zeros in its row of O)
-    const float f = move && !first ? ptx::ex2(mc - top) : 1.f;
-    if (move) mc = top;
     if (have_o && __any_sync(0xffffffffu, move && !first)) {
-#pragma unroll
+        const float f = move && !first ? ptx::ex2(mc - top) : 1.f;
+        l *= f;
+#pragma unroll 1
         for (int x = 0; x < D; x += 16) {
             uint32_t o[16];
             ptx::tmem_ld16(t_o + x, o);
@@ -219,11 +243,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
             ptx::tmem_st16(t_o + x, o);
         }
     }
+    if (move) mc = top;
     const float off = mc == -CUDART_INF_F ? 0.f : p_base<E4M3>() - mc;
     const uint64_t c2 = ptx::pack2(c, c), off2 = ptx::pack2(off, off);
-    uint64_t sum[4];
+    uint64_t sum[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < N; ++k) {
         uint32_t u[16];
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
@@ -245,30 +270,64 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
                 u[x] = h0 | h1 << 16;
                 u[8 + x] = l0 | l1 << 16;
             }
-            ptx::tmem_st8(t_s + 8 * k, u);
-            ptx::tmem_st8(t_s + 32 + 8 * k, u + 8);
+            ptx::tmem_st8(t_p + 8 * k, u);
+            ptx::tmem_st8(t_lo + 8 * k, u + 8);
         } else {
 #pragma unroll
             for (int x = 0; x < 16; ++x) u[x] = ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
-            ptx::tmem_st16(t_s + 16 * k, u);
+            ptx::tmem_st16(t_p + 16 * k, u);
         }
+        if (N == 4 && k == 1) half_done();
     }
+    uint64_t all = sum[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) all = ptx::add2(all, sum[k]);
     float a, b;
-    ptx::unpack2(ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3])), a, b);
-    l = l * f + (a + b);
-    ptx::tmem_st_wait();
+    ptx::unpack2(all, a, b);
+    l += a + b;
+}
+
+// The sum of a V column's infinities and NaN over the keys [k0, k1) that row i
+// (row `row` of the batch) sees: what the products, which meet 0 * NaN there,
+// cannot give.  0 when there are none.
+struct VColumn {                // everything by value: the kernel's parameters stay in constant memory
+    const void* v;              // the K/V head's column in page 0
+    const int32_t* pages;       // the request's row of the block table
+    const uint32_t* mask;       // the row's mask words (chains: null)
+    int64_t page_stride, token_stride;
+    int page, n_pages, c, i;    // cached tokens, the row's number in its request
+};
+template <bool E4M3>
+__device__ __forceinline__ float v_specials(VColumn x, int k0, int k1) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int key = k0; key < k1; ++key) {
+        const int j = key - x.c;
+        if (j >= 0 && !(x.mask ? (ld_dep(x.mask + (j >> 5)) >> (j & 31)) & 1 : j <= x.i)) continue;
+        const int pg = ld_dep(x.pages + key / x.page);
+        if (pg < 0 || pg >= x.n_pages) continue;
+        const int64_t at = pg * x.page_stride + (key % x.page) * x.token_stride;
+        float v;
+        if (E4M3)
+            v = (ld_dep(reinterpret_cast<const unsigned char*>(x.v) + at) & 0x7F) == 0x7F ? CUDART_NAN_F : 0.f;
+        else
+            v = __uint_as_float((uint32_t)ld_dep(reinterpret_cast<const unsigned short*>(x.v) + at) << 16);
+        if (!isfinite(v)) sum += v;
+    }
+    return sum;
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(A_THREADS, 1)
-    k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
-                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const KvDims d,
-                const AttnArgs a, const ATabs t) {
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
+                const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const KvDims d, const AttnArgs a, const ATabs t) {
     using C = ACfg<D, E4M3>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    AMisc* const m = reinterpret_cast<AMisc*>(sm + 2 * C::QT + C::NS * C::SLOT + C::QMISC);
-    uint8_t* const ring = sm + 2 * C::QT;
-    float* const q_scale = reinterpret_cast<float*>(ring + C::NS * C::SLOT);   // e4m3: [2][128]
+    uint8_t* const k_ring = sm + 2 * C::QT;
+    uint8_t* const v_ring = k_ring + C::NK * C::SLOT;
+    float* const q_scale = reinterpret_cast<float*>(v_ring + C::NV * C::SLOT);   // e4m3: [2][128]
+    AMisc* const m = reinterpret_cast<AMisc*>(v_ring + C::NV * C::SLOT + C::QMISC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pt = 2 * t.tpt;
     KT_MARK(K_TREE_ATTN, 0);
@@ -276,66 +335,76 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         if (tid == 0) latch_status(t.sb, MOE_ERR_CUDA, 0);
         return;
     }
-    if (tid == 0) {
-        for (int i = 0; i < C::NS; ++i) {
-            ptx::mbar_init(&m->full[i], 1);
-            ptx::mbar_init(&m->empty[i], 2);
-            ptx::mbar_init(&m->san[i], 1);
+    if (warp == 0) {
+        // the barriers, seg_full .. drain, lie one after the other: 1 arrival each but for these
+        constexpr int N = (offsetof(AMisc, tmem) - offsetof(AMisc, seg_full)) / 8;
+        auto at = [&](const uint64_t* b) { return (int)(b - m->seg_full); };
+#pragma unroll 1
+        for (int i = lane; i < N; i += 32) {
+            uint32_t n = 1;
+            if (i >= at(m->seg_empty) && i < at(m->k_full)) n = E4M3 ? 13 : 14;              // roles
+            if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
+            if (i >= at(m->v_empty) && i < at(m->v_clean)) n = 2;
+            if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
+            if (i >= at(m->q_empty) && i < at(m->s_full)) n = 2;
+            if (i >= at(&m->p_full[0][0]) && i < at(&m->o_full)) n = 4;
+            if (i == at(&m->o_full)) n = 2;
+            if (i >= at(&m->o_free) && i < at(m->wg)) n = 8;
+            if (i >= at(m->wg) && i < at(m->drain)) n = 4;                                   // and turn
+            ptx::mbar_init(&m->seg_full[i], n);
         }
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&m->q_full[i], E4M3 ? 8 : 1);
-            ptx::mbar_init(&m->q_empty[i], 2);
-            ptx::mbar_init(&m->drain[i], 1);
-            ptx::mbar_init(&m->s_full[i], 1);
-            ptx::mbar_init(&m->p_full[i], 4);
+        if (lane < NAN_SLOTS) m->nan_seg[lane] = 0;
+        if (lane == 0) {
+            m->abort = 0;
+            ptx::prefetch_tensormap(&tm_k);
+            ptx::prefetch_tensormap(&tm_v);
+            if (!E4M3) ptx::prefetch_tensormap(&tm_q);
         }
-        ptx::mbar_init(&m->o_full, 2);
-        ptx::mbar_init(&m->o_free, 8);
-        ptx::mbar_init(&m->ml_full, 8);
-        ptx::mbar_init(&m->qs_full, 8);
-        m->abort = 0;
-        for (int i = 0; i < SAN_SLOTS; ++i) m->nan_seg[i] = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 1) ptx::tmem_alloc(&m->tmem, 512);
-    if (warp == 0 && lane == 0) {
-        ptx::prefetch_tensormap(&tm_k);
-        ptx::prefetch_tensormap(&tm_v);
-        if (!E4M3) ptx::prefetch_tensormap(&tm_q);
-    }
     pdl_wait();
     KT_MARK(K_TREE_ATTN, 1);
     pdl_trigger();   // k_tree_join, which waits for this grid before it reads anything
 
-    // this CTA's share: a scan of the requests' key tiles
+    // this CTA's share: a scan of the requests' key tiles (in 32 bits: a thread's
+    // requests' tiles are below 2^30 by the shape's limits unless prompts are
+    // immense, so in units that fit; see the 64-bit total below)
     {
         const int per = (d.B + A_THREADS - 1) / A_THREADS;
         const int b0 = tid * per, b1 = b0 + per < d.B ? b0 + per : d.B;
         long long sum = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const KvReq r = kv_request(d, a.ctx_len, a.row_start, b);
             if (!r.ok && blockIdx.x == 0) latch_status(t.sb, MOE_ERR_BAD_LENGTHS, b);
-            sum += request_tiles(d, r, pt);
+            sum += head_tiles(d, r, pt) * d.Hkv;
         }
         long long s = sum;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const long long u = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += u;
         }
-        if (lane == 31) m->warp_sum[warp] = s;
+        long long* const part = reinterpret_cast<long long*>(m->ml);   // free until the first segment's end
+        if (lane == 31) part[warp] = s;
         __syncthreads();
         long long total = 0, before = 0;
+#pragma unroll 1
         for (int w = 0; w < A_THREADS / 32; ++w) {
             if (w == warp) before = total;
-            total += m->warp_sum[w];
+            total += part[w];
         }
         long long base = before + s - sum;
         const long long pos = share_begin(total, blockIdx.x);
-        if (tid == 0) m->total = total;
+        if (tid == 0) {
+            m->total = total;
+            t.joint[blockIdx.x].rows = 0;
+        }
         if (pos >= base && pos < base + sum) {
+#pragma unroll 1
             for (int b = b0; b < b1; ++b) {
-                const long long n = request_tiles(d, kv_request(d, a.ctx_len, a.row_start, b), pt);
+                const long long n = per == 1 ? sum : head_tiles(d, kv_request(d, a.ctx_len, a.row_start, b), pt) * d.Hkv;
                 if (pos < base + n) {
                     m->first_b = b;
                     m->first_base = base;
@@ -349,313 +418,427 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = m->tmem;
-    volatile int* const abort_flag = &m->abort;
-    auto fail = [&](int site) {
-        latch_status(t.sb, MOE_ERR_TIMEOUT, 200 + site);
-        *abort_flag = 1;
-    };
 
-    if (tid == 0) t.joint[blockIdx.x].rows = 0;
-    if (warp < 4) {
-    ptx::reg_dec<88>();
-    Walk w;
-    bool more = w.start(d, a, m, pt);
-    if (warp == 0) {
-        // ---- producer -----------------------------------------------------
-        uint32_t seq = 0, nq = 0;
-        const int nb = KT / t.box;
-        const int bi = lane / C::HALVES, half = lane % C::HALVES;
-        bool ok = true;
-        for (; more && ok; more = w.next(d, a, pt)) {
-            const int total = w.r.c + w.r.n, mt = w.k1 - w.k0;
-            const int64_t table = (int64_t)w.b * d.max_pages;
-            const uint64_t pol = w.np == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
-            // the page (and offset in it) of this lane's box of key tile j
-            auto page = [&](int j, int& off) {
-                const int key = (w.k0 + j) * KT + bi * t.box;
-                if (j >= mt || bi >= nb || key >= total) return -1;
-                const int pg = key / d.page;
-                off = key - pg * d.page;
-                return ld_dep(a.block_table + table + pg);
-            };
-            auto load = [&](const CUtensorMap* tm, int j, int pg, int off) {
-                const uint32_t s = seq % C::NS;
-                const int key = (w.k0 + j) * KT + bi * t.box;
-                if (!ptx::mbar_wait_warp_fast(&m->empty[s], ((seq / C::NS) & 1) ^ 1, abort_flag, A_WAIT_NS)) return false;
+    if (warp < 4 || warp >= 12) {
+        ptx::reg_dec<72>();
+        SegIn in;
+        Seg w;
+        if (warp == 14) {
+            // ---- the share's segments -----------------------------------------
+            const long long total = m->total;
+            long long pos = share_begin(total, blockIdx.x);
+            const long long end = share_begin(total, blockIdx.x + 1);
+            int b = 0, h = 0, p = 0, np = 1, kt = 0, k0 = 0;
+            KvReq r{0, 0, 0, true};
+            if (pos < end) {
+                b = m->first_b;
+                r = kv_request(d, a.ctx_len, a.row_start, b);
+                np = (r.n + pt - 1) / pt;
+                const long long per_head = head_tiles(d, r, pt);
+                long long off = pos - m->first_base;
+                h = (int)(off / per_head);
+                off -= h * per_head;
+#pragma unroll 1
+                while (off >= (kt = pair_tiles(d, r, p, pt))) {
+                    off -= kt;
+                    ++p;
+                }
+                k0 = (int)off;
+            }
+#pragma unroll 1
+            for (uint32_t i = 0;; ++i) {
+                const bool more = pos < end;
+                if (!wait(&m->seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1, m, 2)) break;
+                const int k1 = (int)(kt - k0 < end - pos ? kt : k0 + (end - pos));
                 if (lane == 0) {
-                    const int left = total - (w.k0 + j) * KT;
-                    const int boxes = left >= KT ? nb : (left + t.box - 1) / t.box;
-                    ptx::mbar_arrive_expect_tx(&m->full[s], boxes * t.box * C::ROWB);
+                    Seg* const s = &m->seg[i % SEGS];
+                    s->b = b;
+                    s->h = h;
+                    s->c = r.c;
+                    s->n = r.n;
+                    s->row0 = r.r0 + p * pt;
+                    s->tok0 = p * pt;
+                    s->ntok = r.n - p * pt < pt ? r.n - p * pt : pt;
+                    s->kt = kt;
+                    s->k0 = k0;
+                    s->k1 = k1;
+                    s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
+                    // a segment that begins here and ends elsewhere: the CTA of its last tile
+                    s->last = more && k0 == 0 && k1 < kt ? (int)(((pos + kt) * A_CTAS - 1) / total) : 0;
+                    ptx::mbar_arrive(&m->seg_full[i % SEGS]);
                 }
                 __syncwarp();
-                if (bi < nb && key < total) {
-                    if (pg < 0 || pg >= d.n_pages) {
-                        latch_status(t.sb, MOE_ERR_BAD_PAGE, pg);
-                        pg = d.n_pages;   // outside: the copy fills zeros
+                if (!more) break;
+                pos += k1 - k0;
+                k0 = 0;
+                if (pos < end) {
+                    if (++p == np) {
+                        p = 0;
+                        if (++h == d.Hkv) {
+                            h = 0;
+                            do {
+                                r = kv_request(d, a.ctx_len, a.row_start, ++b);
+                            } while (r.n == 0);
+                            np = (r.n + pt - 1) / pt;
+                        }
                     }
-                    ptx::tma_load_4d(ring + s * C::SLOT + half * (KT * C::SW) + bi * t.box * C::SW, tm,
-                                     half * (C::SW / (E4M3 ? 1 : 2)), off, w.h, pg, &m->full[s], pol);
+                    kt = pair_tiles(d, r, p, pt);
                 }
-                ++seq;
-                return true;
-            };
-            if (!E4M3) {
-                const int nt = w.ntok(pt) > t.tpt ? 2 : 1;
-                for (int i = 0; i < nt && ok; ++i, ++nq) {
-                    const uint32_t qb = nq & 1;
-                    ok = ptx::mbar_wait_warp_fast(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, abort_flag, A_WAIT_NS);
-                    const int ntok = w.ntok(pt) - i * t.tpt;
-                    const bool small = ntok <= t.qbox;
-                    if (ok && lane == 0) {
-                        ptx::mbar_arrive_expect_tx(&m->q_full[qb],
-                                                   (small ? t.qbox : t.tpt) * t.G * C::SW * C::HALVES);
-                        const int row = w.r.r0 + w.tok0(pt) + i * t.tpt;
+            }
+        } else if (warp == 0 || warp == 12) {
+            // ---- producers: warp 0 for K, warp 12 for V -------------------------
+            // The keys of a part come in boxes of t.box; lane x holds the page of
+            // box 32 r + x, so that pages are looked up once for 32 boxes, one
+            // round ahead.
+            const bool is_v = warp == 12;
+            const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
+            uint64_t* const full = is_v ? m->v_full : m->k_full;
+            uint64_t* const empty = is_v ? m->v_empty : m->k_empty;
+            const uint32_t slots = is_v ? C::NV : C::NK;
+            uint8_t* const ring = is_v ? v_ring : k_ring;
+            uint32_t slot = 0, phase = 0, loads = 0;
+            const int nb = KT / t.box;
+            bool ok = true;
+#pragma unroll 1
+            while (ok && in.next(m, w)) {
+                const int total = w.c + w.n, mt = w.k1 - w.k0;
+                const int32_t* const table = a.block_table + (int64_t)w.b * d.max_pages;
+                const uint64_t pol = w.flags & SEG_ONCE ? ptx::policy_evict_first() : ptx::policy_evict_last();
+                const int key_end = total < w.k1 * KT ? total : w.k1 * KT;
+                int pg = 0, off = 0, pg2 = 0, off2 = 0;
+                int at = 32;                              // first box of the tile in its round; 32: a new round
+                int first = w.k0 * KT;                    // key of the next round's look-up
+#pragma unroll 1
+                for (int j = -1; j < mt; ++j, at += nb) {
+                    if (at == 32 || j < 0) {
+                        pg = pg2;
+                        off = off2;
+                        const int key = first + lane * t.box;
+                        pg2 = 0;
+                        if (key < key_end) {
+                            const int q = key / d.page;
+                            off2 = key - q * d.page;
+                            pg2 = ld_dep(table + q);
+                        }
+                        first += 32 * t.box;
+                        if (j < 0) {                      // the first look-up; the next one follows at once
+                            at = 32 - nb;
+                            continue;
+                        }
+                        at = 0;
+                        if (pg < 0 || pg >= d.n_pages) {
+                            latch_status(t.sb, MOE_ERR_BAD_PAGE, pg);
+                            pg = d.n_pages;               // outside: the copy fills zeros
+                        }
+                    }
+                    const int left = total - (w.k0 + j) * KT;
+                    const int boxes = left >= KT ? nb : (left + t.box - 1) / t.box;
+                    ok = wait(&empty[slot], phase ^ 1, m, 3);
+                    if (!ok) break;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], boxes * t.box * C::ROWB);
+                    __syncwarp();
+                    const int i = lane - at;
+                    if (i >= 0 && i < boxes) {
+                        uint8_t* const to = ring + slot * C::SLOT + i * t.box * C::SW;
+#pragma unroll
                         for (int hf = 0; hf < C::HALVES; ++hf)
-                            ptx::tma_load_3d(sm + qb * C::QT + hf * (128 * C::SW), small ? &tm_q1 : &tm_q, hf * 64,
-                                             w.h * t.G, row, &m->q_full[qb], ptx::policy_evict_last());
+                            ptx::tma_load_4d(to + hf * (KT * C::SW), tm, hf * (C::SW / (E4M3 ? 1 : 2)), off, w.h, pg,
+                                             &full[slot], pol);
+                    }
+                    __syncwarp();
+                    ++loads;
+                    if (++slot == slots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // after a wait ran out, copies in flight land before the CTA's memory is given up
+            const int none = 0;
+            if (!ok) {
+#pragma unroll 1
+                for (uint32_t i = loads > slots ? loads - slots : 0; i < loads; ++i)
+                    ptx::mbar_wait_warp(&full[i % slots], (i / slots) & 1, &none, 10000000ull);
+            }
+        } else if (warp == 13 && !E4M3) {
+            // ---- query tiles ----------------------------------------------------
+            uint32_t nq = 0;
+            bool ok = true;
+#pragma unroll 1
+            while (ok && in.next(m, w)) {
+                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies(w.ntok, t);
+#pragma unroll 1
+                for (int i = 0; i < nt; ++i, ++nq) {
+                    const uint32_t qb = nq & 1;
+                    ok = wait(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, m, 4);
+                    if (!ok) break;
+                    const int ntok = w.ntok - i * t.tpt < t.tpt ? w.ntok - i * t.tpt : t.tpt;
+                    const int row = w.row0 + i * t.tpt, head = w.h * t.G;
+                    uint8_t* const dst = sm + qb * C::QT;
+                    // whole tiles (rows past ntok are not used), or copies 128 / nc
+                    // rows apart, by 8 tokens and by one
+                    const int n8 = ntok / 8, per = nc == 1 ? 1 : n8 + ntok % 8;   // boxes of a copy and half
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(&m->q_full[qb],
+                                                   (nc == 1 ? t.tpt : nc * ntok) * t.G * C::SW * C::HALVES);
+                    __syncwarp();
+#pragma unroll 1
+                    for (int x = lane; x < per * nc * C::HALVES; x += 32) {
+                        const int k = x % per, cp = x / per % nc, hf = x / per / nc;
+                        const int tk = nc == 1 ? 0 : k < n8 ? 8 * k : 8 * n8 + (k - n8);
+                        const CUtensorMap* const tm = nc == 1 ? &tm_q : k < n8 ? &tm_q8 : &tm_q1;
+                        ptx::tma_load_3d(dst + (hf * 128 + cp * (128 / nc) + tk * t.G) * C::SW, tm, hf * 64, head,
+                                         row + tk, &m->q_full[qb], ptx::policy_evict_last());
                     }
                     __syncwarp();
                 }
             }
-            int off0 = 0, off1 = 0, off2 = 0;
-            int pg0 = page(0, off0), pg1 = page(1, off1);
-            ok = ok && load(&tm_k, 0, pg0, off0);
-            for (int j = 0; j < mt && ok; ++j) {
-                const int pg2 = page(j + 2, off2);
-                if (j + 1 < mt) ok = load(&tm_k, j + 1, pg1, off1);
-                ok = ok && load(&tm_v, j, pg0, off0);
-                pg0 = pg1;
-                off0 = off1;
-                pg1 = pg2;
-                off1 = off2;
-            }
-            if (!ok) break;
-        }
-        if (!ok) {
-            if (lane == 0) fail(1);
-            // copies in flight land before the CTA's memory is given up
             const int none = 0;
-            for (uint32_t i = seq > C::NS ? seq - C::NS : 0; i < seq; ++i)
-                ptx::mbar_wait_warp_fast(&m->full[i % C::NS], (i / C::NS) & 1, &none, 10000000ull);
-            for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq && !E4M3; ++i)
-                ptx::mbar_wait_warp_fast(&m->q_full[i & 1], (i >> 1) & 1, &none, 10000000ull);
-        }
-    } else if (warp == 1 || warp == 3) {
-        // ---- MMA issuers: warp 1 for stream 0, warp 3 for stream 1 ---------
-        // The whole warp walks and waits, one lane issues: descriptors built
-        // from values that are the same in the whole warp stay in uniform
-        // registers, and a product costs a few instructions.  An issuer waits
-        // for, and releases, every tile of the ring, also those that only the
-        // other stream uses, so that neither can be two phases ahead of or
-        // behind a barrier (a parity wait takes two phases for none).
-        constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
-        constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
-        const int s = warp >> 1;
-        uint32_t base = 0, nq = 0, n_p = 0, n_seg = 0, san_phase = 0;   // san_phase: a bit a ring slot
-        bool ok = true;
-        const uint32_t sm0 = ptx::smem_u32(sm), ring0 = ptx::smem_u32(ring);
-        const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
-        auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-        // Waits come before the one for P, which ends a tile's critical path:
-        // after it the products go out one after the other.
-        for (; more && ok; more = w.next(d, a, pt), ++n_seg) {
-            const int mt = w.k1 - w.k0;
-            const bool two = same(w.ntok(pt) > t.tpt);
-            bool first = true;
-            const uint32_t qb = same((nq + (two ? s : 0)) & 1);
-            const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
-            ok = ptx::mbar_wait_warp_fast(&m->q_full[qb], ((nq + (two ? s : 0)) >> 1) & 1, abort_flag, A_WAIT_NS);
-            // the previous segment's O is read before the first product into it
-            auto k_ready = [&](int j, uint32_t& slot) {
-                const uint32_t q = base + seq_k(j);
-                slot = same(q % C::NS);
-                return ptx::mbar_wait_warp_fast(&m->full[slot], (q / C::NS) & 1, abort_flag, A_WAIT_NS);
-            };
-            auto v_ready = [&](int j, uint32_t& slot) {   // landed and clean
-                slot = same((base + seq_v(j, mt)) % C::NS);
-                const bool r =
-                    ptx::mbar_wait_warp_fast(&m->san[slot], (san_phase >> slot) & 1, abort_flag, A_WAIT_NS);
-                san_phase ^= 1u << slot;
-                return r;
-            };
-            // (one lane) S = Q K^T, and the slot's release
-            auto qk = [&](uint32_t slot, bool mine) {
-                if (mine) {
-                    const uint32_t kd = ptx::smem_desc_lo(ring0 + slot * C::SLOT, 16);
-#pragma unroll
-                    for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
-#pragma unroll
-                        for (int e = 0; e < D / C::KSTEP; ++e) {
-                            const uint32_t o = ((e * 32) / C::SW * (128 * C::SW) + (e * 32) % C::SW) >> 4;
-                            ptx::mma_ss<E4M3>(t_s, ptx::smem_desc<C::SW>(qd + part * (C::QT / 2 >> 4) + o),
-                                              ptx::smem_desc<C::SW>(kd + o), id_s, (part | e) ? 1u : 0u);
-                        }
+            if (!ok) {
+#pragma unroll 1
+                for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i)
+                    ptx::mbar_wait_warp(&m->q_full[i & 1], (i >> 1) & 1, &none, 10000000ull);
+            }
+        } else if (warp == 1 || warp == 3) {
+            // ---- MMA issuers: warp 1 for stream 0, warp 3 for stream 1 ---------
+            // The whole warp walks and waits, one lane issues: descriptors built
+            // from values that are the same in the whole warp stay in uniform
+            // registers, and a product costs a few instructions.  An issuer waits
+            // for, and releases, every tile of the rings, also those that only the
+            // other stream uses, so that neither can be two phases ahead of or
+            // behind a barrier (a parity wait takes two phases for none).
+            // S of the stream's next tile is begun right after the product with
+            // this one's weights, in whose place it lies; that product in two
+            // halves, the first while the weights of the second are made (one go
+            // where rows are few).  Waits come before the one for P, which ends a
+            // tile's critical path.
+            constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
+            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
+            const int s = warp >> 1;
+            uint32_t nq = 0, n_p0 = 0, n_p1 = 0, n_seg = 0;
+            Ring<C::NK> kr;
+            Ring<C::NV> vr;
+            bool ok = true;
+            const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring), v0 = ptx::smem_u32(v_ring);
+            const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
+            auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+#pragma unroll 1
+            for (; ok && in.next(m, w); ++n_seg) {
+                const int mt = w.k1 - w.k0;
+                const bool two = w.ntok > t.tpt, narrow = copies(w.ntok, t) > 1;
+                const int step = two ? 1 : 2, first = two ? 0 : s;             // own tiles: first, first + step, ...
+                const uint32_t nq_s = nq + (two ? s : 0), qb = same(nq_s & 1);
+                const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
+                ok = wait(&m->q_full[qb], (nq_s >> 1) & 1, m, 5);
+                // the previous segment's O is read before the first product into it
+                bool o_free = n_seg == 0, add = false, have = false;
+                uint32_t ks = 0, vs = 0;
+                // step j: tile j of V, with K of the stream's next tile taken before
+                int jk = 0;
+#pragma unroll 1
+                for (int j = first - step; j < mt && ok; j += step) {
+                    const bool nx = j + step < mt && j + step >= 0;
+                    // past tiles of the other stream, to the own ones
+#pragma unroll 1
+                    for (const int to = nx ? j + step : mt - 1; jk <= to && ok; ++jk) {
+                        ks = same(kr.slot);
+                        ok = wait(&m->k_full[ks], kr.phase, m, 6);
+                        kr.next();
+                        if (!(nx && jk == to) && ok && ptx::elect_one()) ptx::mma_commit(&m->k_empty[ks]);
+                        __syncwarp();
                     }
-                    ptx::mma_commit(&m->s_full[s]);
-                }
-                ptx::mma_commit(&m->empty[slot]);
-            };
-            // two query tiles: both streams take K0 V0 K1 V1 ...; one: stream j % 2
-            // takes tile j, in the order K0 K1 V0 K2 V1 ...
-            const int ahead = two ? 1 : 2;
-            uint32_t ks = 0, vs = 0;
-            for (int j = 0; j < ahead && j < mt && ok; ++j) {
-                ok = k_ready(j, ks);
-                ptx::tc_fence_after();
-                const bool mine = same(two || (j & 1) == s);
-                if (ok && ptx::elect_one()) qk(ks, mine);
-                __syncwarp();
-            }
-            if (ok && n_seg > 0) ok = ptx::mbar_wait_warp_fast(&m->o_free, (n_seg - 1) & 1, abort_flag, A_WAIT_NS);
-            for (int j = 0; j < mt && ok; ++j) {
-                const bool mine = same(two || (j & 1) == s);
-                const bool nx = same(j + ahead < mt);
-                ok = v_ready(j, vs) && (!nx || k_ready(j + ahead, ks));
-                const uint32_t vd = ptx::smem_desc_lo(ring0 + vs * C::SLOT, KT * C::SW);
-                const uint32_t add = same(!first);
-                if (mine && ok) {
-                    ok = ptx::mbar_wait_warp_fast(&m->p_full[s], n_p & 1, abort_flag, A_WAIT_NS);
-                    ++n_p;
-                    first = false;
-                }
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (ptx::elect_one()) {
-                    if (mine) {   // O += P V
-#pragma unroll
-                        for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
-#pragma unroll
-                            for (int e = 0; e < KT / C::KSTEP; ++e)
-                                ptx::mma_ts<E4M3>(t_o, t_s + part * 32 + e * 8,
-                                                  ptx::smem_desc<C::SW>(vd + (e * C::KSTEP * C::SW >> 4)), id_o,
-                                                  (part | e) ? 1u : add);
-                        }
+#pragma unroll 1
+                    for (int jv = have ? j - step + 1 : 0; jv <= j && ok; ++jv) {
+                        vs = same(vr.slot);
+                        ok = wait(&m->v_clean[vs], vr.phase, m, 7);            // landed and clean
+                        vr.next();
+                        if (jv != j && ok && ptx::elect_one()) ptx::mma_commit(&m->v_empty[vs]);
+                        __syncwarp();
                     }
-                    ptx::mma_commit(&m->empty[vs]);
-                    if (nx) qk(ks, mine);
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
-            if (ptx::elect_one()) {
-                ptx::mma_commit(&m->o_full);
-                // (every product of this stream is issued, those that read Q among them)
-                ptx::mma_commit(&m->q_empty[nq & 1]);
-                if (two) ptx::mma_commit(&m->q_empty[(nq + 1) & 1]);
-            }
-            __syncwarp();
-            nq += two ? 2 : 1;
-            base += 2 * mt;
-        }
-        if (!ok) {
-            if (lane == 0) fail(2);
-            // products in flight end before TMEM and shared memory are given up
-            const int none = 0;
-            if (ptx::elect_one()) ptx::mma_commit(&m->drain[s]);
-            __syncwarp();
-            ptx::mbar_wait_warp(&m->drain[s], 0, &none, 10000000ull);
-        }
-    } else if (warp == 2) {
-        // ---- V tiles with keys that some row does not see ------------------
-        // A key past the end, or one that holds NaN or an infinity, must not
-        // reach rows whose weight for it is 0 (0 * NaN).  Rows of V past the end
-        // are zeroed; non-finite entries of new tokens too, and the segment is
-        // flagged, so that its epilogue puts them where they are seen.
-        // Every V tile passes through this warp (it waits for every load in ring
-        // order, the MMA issuer waits for it): a warp that looked only at the tiles
-        // it cleans could be two phases ahead of or behind their barriers, which a
-        // parity wait takes for complete, or waits on for ever.
-        uint32_t base = 0, seen = 0;
-        int seg = 0;
-        bool ok = true;
-        for (; more && ok; more = w.next(d, a, pt), ++seg) {
-            const int mt = w.k1 - w.k0, total = w.r.c + w.r.n, see = w.all_see(d, pt);
-            for (int j = 0; j < mt; ++j) {
-                const int key0 = (w.k0 + j) * KT;
-                const uint32_t q = base + seq_v(j, mt), slot = q % C::NS;
-                for (; seen <= q && ok; ++seen)
-                    ok = ptx::mbar_wait_warp_fast(&m->full[seen % C::NS], (seen / C::NS) & 1, abort_flag, A_WAIT_NS);
-                if (!ok) {
-                    if (lane == 0) fail(3);
-                    break;
-                }
-                if (key0 + KT <= see) {
-                    if (lane == 0) ptx::mbar_arrive(&m->san[slot]);
-                    continue;
-                }
-                const int r0 = see > key0 ? see - key0 : 0, r1 = total - key0 < KT ? total - key0 : KT;
-                uint32_t bad = 0;
-                for (int hf = 0; hf < C::HALVES; ++hf) {
-                    uint8_t* const v = ring + slot * C::SLOT + hf * (KT * C::SW);
-                    for (int o = r1 * C::SW + lane * 16; o < KT * C::SW; o += 512)
-                        *reinterpret_cast<uint4*>(v + o) = make_uint4(0, 0, 0, 0);
-                    for (int o = r0 * C::SW + lane * 16; o < r1 * C::SW; o += 512) {
-                        uint4 x = *reinterpret_cast<uint4*>(v + o);
-                        uint32_t* const u = reinterpret_cast<uint32_t*>(&x);
-                        uint32_t hit = 0;
+                    if (j >= 0) have = true;
+                    if (j >= 0 && !o_free && ok) {
+                        ok = wait(&m->o_free, (n_seg - 1) & 1, m, 8);
+                        o_free = true;
+                    }
+                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::SLOT, KT * C::SW);
+                    const uint32_t kd = ptx::smem_desc_lo(k0 + ks * C::SLOT, 16);
+#pragma unroll 1
+                    for (uint32_t half = j < 0 ? 1 : 0; half < 2 && ok; ++half) {
+                        if (j >= 0 && (half == 0 || !narrow)) {
+                            ok = wait(&m->p_full[s][half], (half ? n_p1 : n_p0) & 1, m, 9);
+                            if (!ok) break;
+                            if (half)
+                                ++n_p1;
+                            else
+                                ++n_p0;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t more_o = same(add);
+                        if (ptx::elect_one()) {
+                            if (j >= 0) {   // O += P V, 64 keys
+                                constexpr int E = KT / 2 / C::KSTEP;
+                                const uint32_t vh = vd + half * (KT / 2 * C::SW >> 4);
+                                const uint32_t pa = t_s + half * (8 * E);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t z;   // all ones in the elements that are not finite
-                            if (E4M3) {
-                                z = __vcmpeq4(u[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                            } else {
-                                z = __vcmpeq2(u[i] & 0x7F807F80u, 0x7F807F80u);
+                                for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
+#pragma unroll
+                                    for (int e = 0; e < E; ++e)
+                                        ptx::mma_ts<E4M3>(t_o, pa + part * 32 + e * 8,
+                                                          ptx::smem_desc<C::SW>(vh + (e * C::KSTEP * C::SW >> 4)), id_o,
+                                                          (part | e) ? 1u : more_o);
+                                }
+                                if (half) ptx::mma_commit(&m->v_empty[vs]);
                             }
-                            u[i] &= ~z;
-                            hit |= z;
+                            if (half && nx) {       // S = Q K^T
+#pragma unroll
+                                for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
+#pragma unroll
+                                    for (int e = 0; e < D / C::KSTEP; ++e) {
+                                        const uint32_t o = ((e * 32) / C::SW * (128 * C::SW) + (e * 32) % C::SW) >> 4;
+                                        ptx::mma_ss<E4M3>(t_s, ptx::smem_desc<C::SW>(qd + part * (C::QT / 2 >> 4) + o),
+                                                          ptx::smem_desc<C::SW>(kd + o), id_s, (part | e) ? 1u : 0u);
+                                    }
+                                }
+                                ptx::mma_commit(&m->s_full[s]);
+                                ptx::mma_commit(&m->k_empty[ks]);
+                            }
                         }
-                        if (hit) *reinterpret_cast<uint4*>(v + o) = x;
-                        bad |= hit;
+                        __syncwarp();
+                        add = j >= 0;
                     }
                 }
-                ptx::fence_proxy_async_shared();
-                bad = __any_sync(0xffffffffu, bad != 0);
-                if (lane == 0) {
-                    if (bad) *(volatile int*)&m->nan_seg[seg % SAN_SLOTS] = seg + 1;
-                    ptx::mbar_arrive(&m->san[slot]);
+                // what is left of the rings is the other stream's
+#pragma unroll 1
+                for (; jk < mt && ok; ++jk) {
+                    ok = wait(&m->k_full[kr.slot], kr.phase, m, 10);
+                    if (ok && ptx::elect_one()) ptx::mma_commit(&m->k_empty[kr.slot]);
+                    __syncwarp();
+                    kr.next();
+                }
+                const int own_last = first < mt ? first + (mt - 1 - first) / step * step : -1;
+#pragma unroll 1
+                for (int jv = own_last + 1; jv < mt && ok; ++jv) {
+                    ok = wait(&m->v_clean[vr.slot], vr.phase, m, 11);
+                    if (ok && ptx::elect_one()) ptx::mma_commit(&m->v_empty[vr.slot]);
+                    __syncwarp();
+                    vr.next();
+                }
+                // (a stream without tiles keeps step with the segments)
+                if (ok && !o_free) ok = wait(&m->o_free, (n_seg - 1) & 1, m, 12);
+                if (!ok) break;
+                if (ptx::elect_one()) {
+                    ptx::mma_commit(&m->o_full);
+                    // every product of this stream is issued, those that read Q among them
+                    // (of few rows, the epilogue uses Q's memory and releases it)
+                    if (!narrow) ptx::mma_commit(&m->q_empty[nq & 1]);
+                    if (two) ptx::mma_commit(&m->q_empty[(nq + 1) & 1]);
                 }
                 __syncwarp();
+                nq += two ? 2 : 1;
             }
-            base += 2 * mt;
+            if (!ok) {
+                // products in flight end before TMEM and shared memory are given up
+                const int none = 0;
+                if (ptx::elect_one()) ptx::mma_commit(&m->drain[s]);
+                __syncwarp();
+                ptx::mbar_wait_warp(&m->drain[s], 0, &none, 10000000ull);
+            }
+        } else if (warp == 2) {
+            // ---- V tiles with keys that some row does not see ------------------
+            // A key past the end, or one that holds NaN or an infinity, must not
+            // reach rows whose weight for it is 0 (0 * NaN).  Rows of V past the end
+            // are zeroed; non-finite entries of new tokens too, and the segment is
+            // flagged, so that its epilogue puts them where they are seen.
+            // Every V tile passes through this warp: one that looked only at the tiles
+            // it cleans could be two phases ahead of or behind their barriers, which a
+            // parity wait takes for complete, or waits on for ever.
+            Ring<C::NV> vr;
+            bool ok = true;
+#pragma unroll 1
+            for (int seg = 0; ok && in.next(m, w); ++seg) {
+                const int mt = w.k1 - w.k0, total = w.c + w.n, see = all_see(d, w);
+#pragma unroll 1
+                for (int j = 0; j < mt; ++j, vr.next()) {
+                    const int key0 = (w.k0 + j) * KT;
+                    ok = wait(&m->v_full[vr.slot], vr.phase, m, 13);
+                    if (!ok) break;
+                    if (key0 + KT > see) {
+                        const int r0 = see > key0 ? see - key0 : 0, r1 = total - key0 < KT ? total - key0 : KT;
+                        uint32_t bad = 0;
+#pragma unroll 1
+                        for (int hf = 0; hf < C::HALVES; ++hf) {
+                            uint8_t* const v = v_ring + vr.slot * C::SLOT + hf * (KT * C::SW);
+#pragma unroll 1
+                            for (int o = r1 * C::SW + lane * 16; o < KT * C::SW; o += 512)
+                                *reinterpret_cast<uint4*>(v + o) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                            for (int o = r0 * C::SW + lane * 16; o < r1 * C::SW; o += 512) {
+                                uint4 x = *reinterpret_cast<uint4*>(v + o);
+                                uint32_t* const u = reinterpret_cast<uint32_t*>(&x);
+                                uint32_t hit = 0;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    // all ones in the elements that are not finite
+                                    const uint32_t z = E4M3 ? __vcmpeq4(u[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                                            : __vcmpeq2(u[i] & 0x7F807F80u, 0x7F807F80u);
+                                    u[i] &= ~z;
+                                    hit |= z;
+                                }
+                                if (hit) *reinterpret_cast<uint4*>(v + o) = x;
+                                bad |= hit;
+                            }
+                        }
+                        ptx::fence_proxy_async_shared();
+                        bad = __any_sync(0xffffffffu, bad != 0);
+                        if (bad && lane == 0) *(volatile int*)&m->nan_seg[seg % NAN_SLOTS] = seg + 1;
+                        __syncwarp();
+                    }
+                    if (lane == 0) ptx::mbar_arrive(&m->v_clean[vr.slot]);
+                }
+            }
         }
-    }
     } else {
-        ptx::reg_inc<208>();
-        Walk w;
-        bool more = w.start(d, a, m, pt);
-        // ---- softmax: warpgroup g, thread = row ---------------------------
+        // ---- softmax: warpgroup g, thread = row -------------------------------
+        ptx::reg_inc<184>();
+        SegIn in;
+        Seg w;
         const int g = (warp - 4) >> 2, wq = warp & 3, row = 32 * wq + lane;
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-        const uint32_t t_s = tmem + lanes + C::T_S + g * 128;
-        uint32_t n_s = 0, nq = 0, n_seg = 0, n_ml = 0;
+        const uint32_t t_s = tmem + lanes + C::T_S + g * 128, t_o = tmem + lanes + C::T_O + g * 128;
+        uint32_t n_s = 0, nq = 0, n_seg = 0, n_ml = 0, n_wg = 0, n_qs = 0, n_turn = 0;
         bool ok = true;
-        for (; more && ok; more = w.next(d, a, pt), ++n_seg) {
-            const int mt = w.k1 - w.k0, total = w.r.c + w.r.n, see = w.all_see(d, pt);
-            const bool two = w.ntok(pt) > t.tpt;
+#pragma unroll 1
+        for (; ok && in.next(m, w); ++n_seg) {
+            const int mt = w.k1 - w.k0, see = all_see(d, w);
+            const bool two = w.ntok > t.tpt;
+            const int nc = copies(w.ntok, t), rs = 128 / nc;             // copies of the rows, lanes each has
+            const int cp = row / rs, rl = row % rs;                      // this thread's copy, and row in it
             const int qs = two ? g : 0;                                  // this stream's query tile
-            const int ntok = w.ntok(pt) - qs * t.tpt < t.tpt ? w.ntok(pt) - qs * t.tpt : t.tpt;
+            const int ntok = w.ntok - qs * t.tpt < t.tpt ? w.ntok - qs * t.tpt : t.tpt;
             const int rows = ntok * t.G;
-            const bool live = 32 * wq < rows;                            // a warp without rows only keeps step
-            const int tok = w.tok0(pt) + qs * t.tpt + row / t.G;         // token of the request (row < rows)
-            const int cnt = two ? mt : (g == 0 ? (mt + 1) / 2 : mt / 2);
+            const bool live = 32 * wq % rs < rows;                       // a warp without rows only keeps step
+            const int tok = qs * t.tpt + by_g(rl, t);                     // token of the segment (rl < rows)
+            const uint32_t qb = (nq + qs) & 1;
             float c = d.scale * 1.4426950408889634f;
             if (E4M3) {
                 // the query tile as e4m3 rows hi and lo (leading and next 4
                 // significant bits) under one power of two a row, into the
                 // swizzled K-major layout: 16 (8) lanes a row, 8 elements a lane
                 c *= ld_dep(a.k_scale + w.h);
+                ok = wait(&m->q_empty[qb], (((nq + qs) >> 1) & 1) ^ 1, m, 14);
+                if (!ok) break;
                 constexpr int LPR = D / 8, RPW = 32 / LPR;
-                const uint32_t qb = (nq + qs) & 1;
                 uint8_t* const hi = sm + qb * C::QT;
                 const int nw = two ? 4 : 8, wi = two ? wq : warp - 4;    // warps that share the tile
                 const int sub = lane % LPR;
+#pragma unroll 1
                 for (int r = wi * RPW + lane / LPR; r < (rows + RPW - 1) / RPW * RPW; r += nw * RPW) {
-                    const int tk = w.tok0(pt) + qs * t.tpt + r / t.G, hh = w.h * t.G + r % t.G;
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (r < rows)
-                        x = ld_dep(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                                  (int64_t)(w.r.r0 + tk) * d.q_stride +
-                                                                  (int64_t)hh * D) + sub);
+                        x = ld_dep(reinterpret_cast<const uint4*>(
+                                       reinterpret_cast<const uint16_t*>(a.q) +
+                                       (int64_t)(w.row0 + qs * t.tpt + by_g(r, t)) * d.q_stride +
+                                       (int64_t)(w.h * t.G + r - by_g(r, t) * t.G) * D) + sub);
                     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                     float f[8], top = 0.f;
 #pragma unroll
@@ -667,8 +850,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll
                     for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     // 2^(134 - e) brings the row's maximum (exponent field e) to [128, 256)
-                    int e = (int)(__float_as_uint(top) >> 23);
                     // (a row below 2^-87 is as good as 0; one with an infinity has NaN scores)
+                    int e = (int)(__float_as_uint(top) >> 23);
                     const bool inf = e == 255;
                     e = e < 40 ? 40 : (e > 250 ? 250 : e);
                     const float up = __uint_as_float((uint32_t)(261 - e) << 23);
@@ -687,42 +870,49 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                 ptx::cvt_e4m3x2(y[2] - z[2], y[3] - z[3]) << 16;
                     }
                     // row r of SW bytes, its 16-byte pieces exchanged by the swizzle
+                    // (copies are a multiple of 32 rows apart: the same exchange)
                     const uint32_t chunk = (uint32_t)(sub >> 1) ^ (C::SW == 128 ? (r & 7) : ((r >> 1) & 3));
-                    uint8_t* const to = hi + r * C::SW + chunk * 16 + (sub & 1) * 8;
-                    *reinterpret_cast<uint2*>(to) = make_uint2(vh[0], vh[1]);
-                    *reinterpret_cast<uint2*>(to + C::QT / 2) = make_uint2(vl[0], vl[1]);
+#pragma unroll 1
+                    for (int k = 0; k < nc; ++k) {
+                        uint8_t* const to = hi + (k * rs + r) * C::SW + chunk * 16 + (sub & 1) * 8;
+                        *reinterpret_cast<uint2*>(to) = make_uint2(vh[0], vh[1]);
+                        *reinterpret_cast<uint2*>(to + C::QT / 2) = make_uint2(vl[0], vl[1]);
+                    }
                 }
                 ptx::fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_n(&m->q_full[qb], two ? 2 : 1);
-                if (lane == 0) ptx::mbar_arrive(&m->qs_full);
-                if (!ptx::mbar_wait_warp_fast(&m->qs_full, n_seg & 1, abort_flag, A_WAIT_NS)) {   // the row scales are there
-                    if (lane == 0) fail(6);
-                    break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_n(&m->q_full[qb], two ? 2 : 1);
+                    ptx::mbar_arrive(&m->qs_full);
                 }
-                c *= q_scale[qb * 128 + row];
+                ok = wait(&m->qs_full, n_qs & 1, m, 15);                 // the row scales are there
+                if (!ok) break;
+                ++n_qs;
+                c *= q_scale[qb * 128 + rl];
             }
             float mc = -CUDART_INF_F, l = 0.f;
-            for (int i = 0; i < cnt && ok; ++i) {
-                const int key0 = (w.k0 + (two ? i : 2 * i + g)) * KT;
+            const int step = two ? 1 : 2;
+#pragma unroll 1
+            for (int j = two ? 0 : g; j < mt; j += step) {
+                const int key0 = (w.k0 + j) * KT;
                 const bool part = key0 + KT > see;
                 uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
                 if (part && live) {
                     if (d.W == 0) {
-                        const int n = w.r.c + tok + 1 - key0;            // keys of the tile the row sees
+                        const int n = w.c + w.tok0 + tok + 1 - key0;     // keys of the tile the row sees
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             vis[k] = n >= 32 * k + 32 ? ~0u : (n <= 32 * k ? 0u : (1u << (n - 32 * k)) - 1u);
                     } else {
                         // bit x of the tile is new token key0 + x - c
                         uint32_t words[5];
-                        const int j0 = key0 - w.r.c, word0 = j0 >> 5;
-                        const uint32_t* const mr = a.mask + (int64_t)(w.r.r0 + tok) * d.W;
+                        const int j0 = key0 - w.c, word0 = j0 >> 5;
+                        const uint32_t* const mr = a.mask + (int64_t)(w.row0 + tok) * d.W;
 #pragma unroll
                         for (int k = 0; k < 5; ++k) {
-                            const int x = word0 + k, n = w.r.n - 32 * x;
+                            const int x = word0 + k, n = w.n - 32 * x;
                             uint32_t v = x < 0 ? ~0u : 0u;
-                            if (x >= 0 && n > 0 && row < rows) {
+                            if (x >= 0 && n > 0 && rl < rows) {
                                 v = ld_dep(mr + x);
                                 if (n < 32) v &= (1u << n) - 1u;
                             }
@@ -732,129 +922,253 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         for (int k = 0; k < 4; ++k) vis[k] = __funnelshift_r(words[k], words[k + 1], j0 & 31);
                     }
                 }
-                if (!ptx::mbar_wait_warp_fast(&m->s_full[g], n_s & 1, abort_flag, A_WAIT_NS)) {
-                    if (lane == 0) fail(4);
-                    ok = false;
-                    break;
-                }
+                ok = wait(&m->s_full[g], n_s & 1, m, 16);
+                if (!ok) break;
                 ++n_s;
                 ptx::tc_fence_after();
-                if (live)
-                    softmax_tile<D, E4M3>(t_s, tmem + lanes + C::T_O + g * 128, c, part, vis, i > 0, mc, l);
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&m->p_full[g]);
+                const bool have_o = j >= step;
+                auto stored = [&](int half) {
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&m->p_full[g][half]);
+                };
+                auto nothing = [] {};
+                int last_half = 0;
+                if (nc == 4) {
+                    // this warp's quarter of the keys; the other quarters' weights are 0 in its rows
+                    const uint32_t v = cp == 0 ? vis[0] : cp == 1 ? vis[1] : cp == 2 ? vis[2] : vis[3];
+                    constexpr int PC = E4M3 ? 8 : 16;                    // columns of 32 keys' weights
+                    softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, &v, have_o,
+                                              nothing, mc, l);
+#pragma unroll 1
+                    for (int k = 1; k < 4; ++k) {
+                        const uint32_t other = t_s + PC * ((cp + k) & 3);
+                        if (E4M3) {
+                            ptx::tmem_st8_rep(other, 0);
+                            ptx::tmem_st8_rep(other + 32, 0);
+                        } else {
+                            ptx::tmem_st16_rep(other, 0);
+                        }
+                    }
+                } else if (nc == 2) {
+                    constexpr int PC = E4M3 ? 16 : 32;
+                    const uint32_t v[2] = {cp ? vis[2] : vis[0], cp ? vis[3] : vis[1]};
+                    softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, v, have_o,
+                                              nothing, mc, l);
+                    const uint32_t other = t_s + PC * (cp ^ 1);
+                    ptx::tmem_st16_rep(other, 0);
+                    ptx::tmem_st16_rep(other + (E4M3 ? 32 : 16), 0);
+                } else {
+                    // The warpgroups take turns: two at once would each take longer, and
+                    // reach the tensor core together, which then waits for both.
+                    last_half = 1;
+                    if (g == 1 || n_turn > 0) ok = wait(&m->turn[g], (n_turn - (g ^ 1)) & 1, m, 20);
+                    if (!ok) break;
+                    ++n_turn;
+                    if (live)
+                        softmax_cols<D, E4M3, 128>(t_s, t_s, t_s + 32, t_o, c, part, vis, have_o, [&] { stored(0); }, mc, l);
+                    else
+                        stored(0);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
+                }
+                stored(last_half);
             }
             if (!ok) break;
-            nq += two ? 2 : 1;
-            if (!ptx::mbar_wait_warp_fast(&m->o_full, n_seg & 1, abort_flag, A_WAIT_NS)) {
-                if (lane == 0) fail(5);
-                break;
+            if (nc == 1 && !two && g == 1 && mt % 2) {                   // the turn of a tile that stream 1 does not have
+                ok = wait(&m->turn[1], n_turn & 1, m, 21);
+                if (!ok) break;
+                ++n_turn;
+                if (lane == 0) ptx::mbar_arrive(&m->turn[0]);
             }
+            nq += two ? 2 : 1;
+            ok = wait(&m->o_full, n_seg & 1, m, 17);
+            if (!ok) break;
             ptx::tc_fence_after();
             // ---- the segment's end ------------------------------------------
-            // one query tile: both streams' O of a row, half its columns a warpgroup
-            float m1 = -CUDART_INF_F, l1 = 0.f;
+            const bool whole = w.k0 == 0 && w.k1 == w.kt;
+            const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);       // of a partial result
+            const bool flagged = *(volatile int*)&m->nan_seg[n_seg % NAN_SLOTS] == (int)n_seg + 1;
+            const float v_scale = E4M3 ? ld_dep(a.v_scale + w.h) : 1.f;
             if (!two) {
                 m->ml[g][row] = make_float2(mc, l);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&m->ml_full);
-                if (!ptx::mbar_wait_warp_fast(&m->ml_full, n_ml & 1, abort_flag, A_WAIT_NS)) {
-                    if (lane == 0) fail(7);
-                    break;
-                }
+                ok = wait(&m->ml_full, n_ml & 1, m, 18);
+                if (!ok) break;
                 ++n_ml;
-                const float2 o = m->ml[g ^ 1][row];
-                m1 = o.x;
-                l1 = o.y;
             }
-            const float top = fmaxf(mc, m1), zero = top == -CUDART_INF_F ? 0.f : top;
-            // a stream that saw nothing adds nothing (its O may never have been written)
-            const float f0 = mc == -CUDART_INF_F && !(l != l) ? 0.f : ptx::ex2(mc - zero);
-            const float f1 = m1 == -CUDART_INF_F && !(l1 != l1) ? 0.f : ptx::ex2(m1 - zero);
-            const float sum = l * f0 + l1 * f1;
-            const bool whole = w.k0 == 0 && w.k1 == w.kt;
-            const bool mine = row < rows;
-            const int grow = w.r.r0 + tok;                               // row of the batch
-            const int head = w.h * t.G + row % t.G;
-            const int slot = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
-            const int prow = qs * t.tpt * t.G + row;                     // row of the partial result
-            const bool flagged = *(volatile int*)&m->nan_seg[n_seg % SAN_SLOTS] == (int)n_seg + 1;
-            if (live) {
-                const int x0 = two ? 0 : g * (D / 2), x1 = two ? D : x0 + D / 2;
-                const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) * (E4M3 ? ld_dep(a.v_scale + w.h) : 1.f) : 1.f;
-                const bool have0 = f0 != 0.f, have1 = f1 != 0.f;
-                for (int x = x0; x < x1; x += 16) {
-                    uint32_t u[16], v[16];
-                    ptx::tmem_ld16(tmem + lanes + C::T_O + g * 128 + x, u);
-                    if (!two) ptx::tmem_ld16(tmem + lanes + C::T_O + (g ^ 1) * 128 + x, v);
-                    ptx::tmem_ld_wait16(u);
-                    if (!two) ptx::tmem_ld_wait16(v);
-                    float o[16];
+            // a part that saw nothing adds nothing (its O may never have been written)
+            auto factor = [](float2 x, float top) {
+                return x.x == -CUDART_INF_F && !(x.y != x.y) ? 0.f : ptx::ex2(x.x - top);
+            };
+            // where row r (of tile qs) and column x of this segment go
+            auto out_at = [&](int tk, int r, int x) {
+                return ((int64_t)(w.row0 + tk) * d.Hq + w.h * t.G + r - by_g(r, t) * t.G) * D + x;
+            };
+            // a partial result's O stands by 4 columns: [slot][D / 4][rows][4], so that a
+            // warp's rows are written next to each other
+            auto part_row = [&](int r) { return (int64_t)slot * t.rp + qs * t.tpt * t.G + r; };
+            auto part_at = [&](int r, int x) {
+                return t.part_o + (((int64_t)slot * (D / 4) + x / 4) * t.rp + qs * t.tpt * t.G + r) * 4;
+            };
+            auto put_ml = [&](int tk, int r, float top, float zero, float sum) {
+                // log2 of the sum, without the weights' 2^base
+                if (!whole)
+                    t.part_ml[part_row(r)] = make_float2(top - p_base<E4M3>(), sum);
+                else if (a.lse)
+                    a.lse[out_at(tk, r, 0) / D] =
+                        sum == 0.f ? -CUDART_INF_F : (zero - p_base<E4M3>() + log2f(sum)) * 0.69314718055994531f;
+            };
+            // Infinities and NaN of V that row r sees in columns [x, x + n), put over
+            // what is there: from the first cleaned key on, or (all) from the part's first.
+            auto specials = [&](int tk, int r, int x, int n, bool all) {
+                const int key0 = w.k0 * KT, total = w.c + w.n, key1 = total < w.k1 * KT ? total : w.k1 * KT;
+                VColumn col;
+                col.v = reinterpret_cast<const uint8_t*>(a.v_cache) + w.h * d.head_stride * (E4M3 ? 1 : 2);
+                col.pages = a.block_table + (int64_t)w.b * d.max_pages;
+                col.mask = d.W ? a.mask + (int64_t)(w.row0 + tk) * d.W : nullptr;
+                col.page_stride = d.page_stride;
+                col.token_stride = d.token_stride;
+                col.page = d.page;
+                col.n_pages = d.n_pages;
+                col.c = w.c;
+                col.i = w.tok0 + tk;
+#pragma unroll 1
+                for (int y = x; y < x + n; ++y) {
+                    VColumn one = col;
+                    one.v = reinterpret_cast<const uint8_t*>(col.v) + y * (E4M3 ? 1 : 2);
+                    const float e = v_specials<E4M3>(one, all || see < key0 ? key0 : see, key1);
+                    if (e == 0.f) continue;
+                    if (whole)
+                        reinterpret_cast<__nv_bfloat16*>(a.out)[out_at(tk, r, y)] = __float2bfloat16_rn(e);
+                    else
+                        part_at(r, y)[y % 4] = e;
+                }
+            };
+            if (nc == 1) {
+                // one query tile: both streams' O of a row, half its columns a warpgroup
+                float2 x0 = make_float2(mc, l), x1 = make_float2(-CUDART_INF_F, 0.f);
+                if (!two) x1 = m->ml[g ^ 1][row];
+                const float top = fmaxf(x0.x, x1.x), zero = top == -CUDART_INF_F ? 0.f : top;
+                float f0 = factor(x0, zero), f1 = factor(x1, zero);
+                const float sum = x0.y * f0 + x1.y * f1;
+                const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) * v_scale : 1.f;
+                f0 *= scale;
+                f1 *= scale;
+                if (live) {
+                    const int c0 = two ? 0 : g * (D / 2), c1 = two ? D : c0 + D / 2;
+#pragma unroll 1
+                    for (int x = c0; x < c1; x += 16) {
+                        uint32_t u[16], v[16];
+                        ptx::tmem_ld16(t_o + x, u);
+                        ptx::tmem_ld16((two ? t_o : tmem + lanes + C::T_O + (g ^ 1) * 128) + x, v);
+                        ptx::tmem_ld_wait16(u);
+                        ptx::tmem_ld_wait16(v);
+                        float o[16];
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        o[y] = have0 ? __uint_as_float(u[y]) * f0 : 0.f;
-                        if (!two) o[y] += have1 ? __uint_as_float(v[y]) * f1 : 0.f;
-                        o[y] *= scale;
-                    }
-                    if (flagged && mine) {
-                        const int kb = see > w.k0 * KT ? see : w.k0 * KT, ke = total < w.k1 * KT ? total : w.k1 * KT;
-                        for (int key = kb; key < ke; ++key) {
-                            const int j = key - w.r.c;
-                            if (j >= 0 && !row_sees(d, a, grow, tok, j)) continue;
-                            const int pg = ld_dep(a.block_table + (int64_t)w.b * d.max_pages + key / d.page);
-                            if (pg < 0 || pg >= d.n_pages) continue;
-                            const int64_t at = pg * d.page_stride + w.h * d.head_stride +
-                                               (key % d.page) * d.token_stride + x;
+                        for (int y = 0; y < 16; ++y)
+                            o[y] = (f0 != 0.f ? __uint_as_float(u[y]) * f0 : 0.f) +
+                                   (f1 != 0.f ? __uint_as_float(v[y]) * f1 : 0.f);
+                        if (row < rows && whole) {
+                            uint32_t z[8];
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) {
-                                float e;
-                                if (E4M3) {
-                                    const uint8_t q8 = reinterpret_cast<const uint8_t*>(a.v_cache)[at + y];
-                                    e = (q8 & 0x7F) == 0x7F ? CUDART_NAN_F : 0.f;
-                                } else {
-                                    e = __uint_as_float(
-                                        (uint32_t) reinterpret_cast<const uint16_t*>(a.v_cache)[at + y] << 16);
-                                }
-                                if (!isfinite(e)) o[y] += e;
-                            }
+                            for (int y = 0; y < 8; ++y) z[y] = ptx::cvt_bf16x2(o[2 * y], o[2 * y + 1]);
+                            uint4* const to =
+                                reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + out_at(tok, row, x));
+                            to[0] = make_uint4(z[0], z[1], z[2], z[3]);
+                            to[1] = make_uint4(z[4], z[5], z[6], z[7]);
+                        } else if (row < rows) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                *reinterpret_cast<float4*>(part_at(row, x + 4 * y)) =
+                                    make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                         }
                     }
-                    if (mine && whole) {
-                        uint32_t z[8];
+                    if (row < rows && (two || g == 0)) put_ml(tok, row, top, zero, sum);
+                    if (flagged && row < rows && !(sum != sum)) specials(tok, row, c0, c1 - c0, false);
+                }
+            } else {
+                // few rows: the copies' and streams' O of a row are added through the
+                // memory of Q, half the columns a warpgroup, in two passes
+                auto group_sync = [&] {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&m->wg[g]);
+                    return wait(&m->wg[g], n_wg++ & 1, m, 19);
+                };
+                constexpr int W4 = D / 16;                               // 16-byte pieces a row and pass
+                float4* const stage = reinterpret_cast<float4*>(sm + qb * C::QT + g * (C::QT / 2));
+                auto piece = [](int r, int k) {                          // spread over the banks
+                    return r * W4 + (W4 == 8 ? k ^ (r & 7) : k ^ ((r >> 1) & 3));
+                };
+                float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < nc; ++k) top = ptx::max3(top, m->ml[0][k * rs + rl].x, m->ml[1][k * rs + rl].x);
+                const float zero = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll 1
+                for (int k = 0; k < nc; ++k) {
+                    const float2 x0 = m->ml[0][k * rs + rl], x1 = m->ml[1][k * rs + rl];
+                    sum += x0.y * factor(x0, zero) + x1.y * factor(x1, zero);
+                }
+                const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) * v_scale : 1.f;
+                const float f0 = factor(m->ml[0][row], zero) * scale, f1 = factor(m->ml[1][row], zero) * scale;
+                if (g == 0 && row < rows) put_ml(tok, row, top, zero, sum);
+#pragma unroll 1
+                for (int pass = 0; pass < 2 && ok; ++pass) {
+                    const int x0 = g * (D / 2) + pass * (D / 4);
+                    if (pass == 1) ok = group_sync();                    // the first pass has been read
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int x = 0; x < D / 4; x += 16) {
+                        uint32_t u[16], v[16];
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + x0 + x, u);
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + 128 + x0 + x, v);
+                        ptx::tmem_ld_wait16(u);
+                        ptx::tmem_ld_wait16(v);
+                        float o[16];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) z[y] = ptx::cvt_bf16x2(o[2 * y], o[2 * y + 1]);
-                        uint4* const to = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                                                   ((int64_t)grow * d.Hq + head) * D + x);
-                        to[0] = make_uint4(z[0], z[1], z[2], z[3]);
-                        to[1] = make_uint4(z[4], z[5], z[6], z[7]);
-                    } else if (mine) {
-                        float4* const to = reinterpret_cast<float4*>(t.part_o + ((int64_t)slot * t.rp + prow) * D + x);
+                        for (int y = 0; y < 16; ++y)
+                            o[y] = (f0 != 0.f ? __uint_as_float(u[y]) * f0 : 0.f) +
+                                   (f1 != 0.f ? __uint_as_float(v[y]) * f1 : 0.f);
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            to[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                            stage[piece(row, x / 4 + y)] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                    ok = group_sync();
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int i = row; i < rows * W4; i += 128) {
+                        const int r = i / W4, k = i % W4, x = x0 + 4 * k, tk = by_g(r, t);
+                        float4 z = stage[piece(r, k)];
+#pragma unroll 1
+                        for (int e = rs; e < 128; e += rs) {
+                            const float4 q = stage[piece(e + r, k)];
+                            z.x += q.x; z.y += q.y; z.z += q.z; z.w += q.w;
+                        }
+                        if (whole)
+                            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + out_at(tk, r, x)) =
+                                make_uint2(ptx::cvt_bf16x2(z.x, z.y), ptx::cvt_bf16x2(z.z, z.w));
+                        else
+                            *reinterpret_cast<float4*>(part_at(r, x)) = z;
+                        // (a copy's weights of 0 make NaN of a seen infinity; a row whose own
+                        // scores are NaN has a NaN sum)
+                        const bool bad = !isfinite(z.x + z.y + z.z + z.w);
+                        if (bad || flagged) {
+                            float l_all = 0.f;
+                            for (int e = 0; e < nc; ++e) l_all += m->ml[0][e * rs + r].y + m->ml[1][e * rs + r].y;
+                            if (!(l_all != l_all)) specials(tk, r, x, 4, bad);
+                        }
                     }
                 }
-                if (mine && (two || g == 0)) {
-                    // log2 of the sum, without the weights' 2^BASE
-                    if (!whole)
-                        t.part_ml[(int64_t)slot * t.rp + prow] = make_float2(top - p_base<E4M3>(), sum);
-                    else if (a.lse)
-                        a.lse[(int64_t)grow * d.Hq + head] =
-                            sum == 0.f ? -CUDART_INF_F : (zero - p_base<E4M3>() + log2f(sum)) * 0.69314718055994531f;
-                }
+                if (!ok) break;
+                ptx::fence_proxy_async_shared();                         // Q's next tile comes by TMA
+                ok = group_sync();
+                if (!ok) break;
+                if (wq == 0 && lane == 0) ptx::mbar_arrive(&m->q_empty[qb]);
             }
-            if (warp == 4 && lane == 0 && w.k0 == 0 && !whole) {
-                Joint jn;
-                jn.rows = w.ntok(pt) * t.G;
-                jn.row0 = w.r.r0 + w.tok0(pt);
-                jn.kvh = w.h;
-                // the CTA that holds the segment's last tile
-                jn.last = (int)(((w.pos + w.kt) * A_CTAS - 1) / m->total);
-                jn.total = m->total;
-                jn.pad[0] = jn.pad[1] = 0;
-                t.joint[blockIdx.x] = jn;
-            }
+            if (warp == 4 && lane == 0 && w.k0 == 0 && !whole)
+                t.joint[blockIdx.x] = Joint{w.ntok * t.G, w.row0, w.h, w.last, m->total, {0, 0}};
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&m->o_free);
@@ -864,63 +1178,51 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    if (tid == 0 && m->abort) latch_status(t.sb, MOE_ERR_TIMEOUT, 200 + m->abort);
     KT_MARK(K_TREE_ATTN, 2);
 }
 
-// The parts of the divided segments: CTA x of the first grid axis joins the
-// segment whose first tile share x holds, a warp a row, parts in key order.
+// The parts of the divided segments, added in key order: CTA x of the first grid
+// axis joins the segment whose first tile share x holds; a warp takes 4 columns of
+// 32 rows, a lane a row.
 constexpr int JOIN_WARPS = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) k_tree_join(const KvDims d, const AttnArgs a, const ATabs t) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), cta = blockIdx.x;
+    const int lane = threadIdx.x & 31, cta = blockIdx.x, row = blockIdx.y * 32 + lane;
+    const int x = (blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5)) * 4;
     KT_MARK(K_TREE_JOIN, 0);
     pdl_wait();
     KT_MARK(K_TREE_JOIN, 1);
-    const Joint* const jp = t.joint + cta;
-    if (row >= ld_dep(&jp->rows)) return;
-    const int last = ld_dep(&jp->last);
-    const long long total = ld_dep(&jp->total);
-    // part slots: 2 cta + 1 (the first), then 2 c of the CTAs that hold any tile
-    float top = -CUDART_INF_F;
-    for (int c = cta + lane; c <= last; c += 32) {
-        if (c > cta && share_begin(total, c) == share_begin(total, c + 1)) continue;
-        top = fmaxf(top, ld_dep(t.part_ml + (int64_t)(2 * c + (c == cta)) * t.rp + row).x);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float zero = top == -CUDART_INF_F ? 0.f : top;
-    float sum = 0.f, o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    const int4 j = ld_dep(reinterpret_cast<const int4*>(t.joint + cta));   // rows, row0, kvh, last
+    if (row >= j.x) return;
+    const long long total = ld_dep(&t.joint[cta].total);
+    // part slots: 2 cta + 1 (the first), then 2 c of the CTAs that hold any tile;
+    // the running maximum moves from part to part as from tile to tile
+    float m = -CUDART_INF_F, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = cta; c <= last; ++c) {
-        if (c > cta && share_begin(total, c) == share_begin(total, c + 1)) continue;
-        const int64_t at = (int64_t)(2 * c + (c == cta)) * t.rp + row;
-        const float2 ml = ld_dep(t.part_ml + at);
-        float p[V];
-        if (V == 4) {
-            const float4 x = ld_dep(reinterpret_cast<const float4*>(t.part_o + at * D) + lane);
-            p[0] = x.x; p[1] = x.y; p[2 % V] = x.z; p[3 % V] = x.w;
-        } else {
-            const float2 x = ld_dep(reinterpret_cast<const float2*>(t.part_o + at * D) + lane);
-            p[0] = x.x; p[1] = x.y;
-        }
-        const float f = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - zero);
-        sum += ml.y * f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] += p[v] * f;
+    for (int c = cta; c <= j.w; ++c) {
+        const int64_t slot = 2 * c + (c == cta);
+        const bool any = c == cta || total >= A_CTAS || share_begin(total, c) != share_begin(total, c + 1);
+        const float2 ml = any ? ld_dep(t.part_ml + slot * t.rp + row) : make_float2(-CUDART_INF_F, 0.f);
+        const float4 p = any ? ld_dep(reinterpret_cast<const float4*>(t.part_o) + (slot * (D / 4) + x / 4) * t.rp + row)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float top = fmaxf(m, ml.x), zero = top == -CUDART_INF_F ? 0.f : top;
+        const float f = ptx::ex2(m - zero), e = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - zero);
+        m = top;
+        sum = sum * f + ml.y * e;
+        o.x = o.x * f + p.x * e;
+        o.y = o.y * f + p.y * e;
+        o.z = o.z * f + p.z * e;
+        o.w = o.w * f + p.w * e;
     }
-    const int G = t.G, kvh = ld_dep(&jp->kvh), grow = ld_dep(&jp->row0) + row / G, head = kvh * G + row % G;
-    const float s = (sum == 0.f ? 0.f : 1.f / sum) * (d.e4m3 ? ld_dep(a.v_scale + kvh) : 1.f);
-    uint32_t* const to = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                                     ((int64_t)grow * d.Hq + head) * D) + lane * (V / 2);
-#pragma unroll
-    for (int v = 0; v < V; v += 2) to[v / 2] = ptx::cvt_bf16x2(o[v] * s, o[v + 1] * s);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)grow * d.Hq + head] =
-            sum == 0.f ? -CUDART_INF_F : (zero + log2f(sum)) * 0.69314718055994531f;
+    const int tk = by_g(row, t), head = j.z * t.G + row - tk * t.G;
+    const int64_t at = (int64_t)(j.y + tk) * d.Hq + head;
+    const float s = (sum == 0.f ? 0.f : 1.f / sum) * (d.e4m3 ? ld_dep(a.v_scale + j.z) : 1.f);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + x) =
+        make_uint2(ptx::cvt_bf16x2(o.x * s, o.y * s), ptx::cvt_bf16x2(o.z * s, o.w * s));
+    if (a.lse && x == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
     KT_MARK(K_TREE_JOIN, 2);
 }
 
@@ -930,8 +1232,8 @@ ATabs attn_tabs(const KvDims& d, char* ws, size_t* bytes) {
     ATabs t{};
     t.G = d.Hq / d.Hkv;
     t.tpt = 128 / t.G;
+    t.g_inv = (65536u + t.G - 1) / t.G;
     t.box = gcd(d.page, KT);
-    t.qbox = t.tpt < 8 ? t.tpt : 8;
     const int64_t tokens = d.T < 2 * t.tpt ? d.T : 2 * t.tpt;
     t.rp = (int)(tokens * t.G);
     size_t o = sizeof(StatusBlock);
@@ -951,7 +1253,7 @@ template <int D, bool E4M3>
 cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     using C = ACfg<D, E4M3>;
     const ATabs t = attn_tabs(d, a.ws, nullptr);
-    CUtensorMap tm_q, tm_q1, tm_k, tm_v;
+    CUtensorMap tm_q, tm_q8, tm_q1, tm_k, tm_v;
     const uint64_t el = E4M3 ? 1 : 2;
     const CUtensorMapDataType dt = E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = C::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -960,24 +1262,27 @@ cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     const uint32_t box[4] = {(uint32_t)(C::SW / el), (uint32_t)t.box, 1, 1};
     if (!make_map(&tm_k, dt, a.k_cache, 4, dims, str, box, sw) || !make_map(&tm_v, dt, a.v_cache, 4, dims, str, box, sw))
         return cudaErrorInvalidValue;
-    tm_q = tm_q1 = tm_k;
+    tm_q = tm_q8 = tm_q1 = tm_k;
     if (!E4M3) {
         const uint64_t qd[3] = {(uint64_t)D, (uint64_t)d.Hq, (uint64_t)d.T};
         const uint64_t qs[2] = {(uint64_t)D * 2, (uint64_t)d.q_stride * 2};
-        const uint32_t qb[3] = {64, (uint32_t)t.G, (uint32_t)t.tpt}, qb1[3] = {64, (uint32_t)t.G, (uint32_t)t.qbox};
-        if (!make_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !make_map(&tm_q1, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qd, qs, qb1, CU_TENSOR_MAP_SWIZZLE_128B))
+        // boxes of a whole tile, of 8 tokens (where they fit 64 rows) and of one
+        auto q_map = [&](CUtensorMap* m, int tokens) {
+            const uint32_t qb[3] = {64, (uint32_t)t.G, (uint32_t)tokens};
+            return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        if (!q_map(&tm_q, t.tpt) || !q_map(&tm_q8, 8 * t.G <= 64 ? 8 : 1) || !q_map(&tm_q1, 1))
             return cudaErrorInvalidValue;
     }
     cudaError_t e = cudaFuncSetAttribute(k_tree_attn<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin(K_TREE_ATTN, st);
-    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(A_CTAS), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q1, tm_k, tm_v, d, a, t);
+    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(A_CTAS), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
     timing_end(st);
     if (e != cudaSuccess) return e;
     timing_begin(K_TREE_JOIN, st);
-    e = launch_pdl(k_tree_join<D>, dim3(A_CTAS, (t.rp + JOIN_WARPS - 1) / JOIN_WARPS), dim3(32 * JOIN_WARPS), 0, st, d, a,
-                   t);
+    e = launch_pdl(k_tree_join<D>, dim3(A_CTAS, (t.rp + 31) / 32, D / 4 / JOIN_WARPS), dim3(32 * JOIN_WARPS), 0, st,
+                   d, a, t);
     timing_end(st);
     return e;
 }

@@ -422,6 +422,20 @@ def test_a_seen_infinity_in_v_reaches_its_column_only():
     assert torch.isfinite(t.out[30:][:, :, rest]).all()
 
 
+@pytest.mark.parametrize("new,Hq", [(1, 4), (9, 4), (20, 4), (60, 8)])
+def test_a_seen_infinity_among_the_cached_tokens(new, Hq):
+    # every row sees it, few rows or many: its column is infinite, the others are what they were
+    t = Batch([700], [new], Hq, 1, 128, 16, tree=True, seed=11)
+    t.run()
+    clean = t.out.clone()
+    t.v[t.table[0][333 // 16], 0, 333 % 16, 100] = float("inf")
+    t.run()
+    moe.check_device_status(t.ws)
+    assert (t.out[:, :, 100] == float("inf")).all()
+    rest = [d for d in range(128) if d != 100]
+    assert torch.equal(t.out[:, :, rest], clean[:, :, rest])
+
+
 def test_scores_far_apart():
     # one key per row takes all the weight; the running maximum moves by hundreds between tiles
     t = Batch([900], [3], 4, 2, 64, 16, gain=40.0, seed=6)
