@@ -966,12 +966,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     if (g == 1 || n_turn > 0) ok = wait(&m->turn[g], (n_turn - (g ^ 1)) & 1, m, 20);
                     if (!ok) break;
                     ++n_turn;
-                    if (live)
-                        softmax_cols<D, E4M3, 128>(t_s, t_s, t_s + 32, t_o, c, part, vis, have_o, [&] { stored(0); }, mc, l);
-                    else
+                    auto half_done = [&] {
                         stored(0);
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
+                        if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
+                    };
+                    if (live)
+                        softmax_cols<D, E4M3, 128>(t_s, t_s, t_s + 32, t_o, c, part, vis, have_o, half_done, mc, l);
+                    else
+                        half_done();
                 }
                 stored(last_half);
             }
