@@ -130,7 +130,7 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // ---------------------------------------------------------------------------
 enum KernelId {
     K_ROUTER = 0, K_TOPK, K_SORT, K_GATHER, K_EXPERTS, K_COMBINE, K_ROUTE_GATHER,
-    K_LATENT_DOWN, K_LATENT_MID, K_LATENT_UP, K_KV_PLAN, K_KV_APPEND, K_TREE_ATTN, K_TREE_JOIN, K_NUM
+    K_LATENT_DOWN, K_LATENT_MID, K_LATENT_UP, K_KV_PLAN, K_KV_APPEND, K_TREE_ATTN, K_NUM
 };
 void timing_begin(int kernel_id, cudaStream_t st);
 void timing_end(cudaStream_t st);

@@ -13,7 +13,8 @@
 // its key tiles.  The segments' key tiles laid end to end are cut into equal
 // shares, one a CTA (persistent, one CTA an SM), whatever the lengths; every
 // CTA finds its share from the lengths itself.  A segment that a cut divides
-// leaves fp32 partial results, which k_tree_join adds in key order.
+// leaves fp32 partial results; at the kernel's end the CTAs that hold parts of
+// it wait for one another's and add them in key order, each some of its columns.
 //
 // Two streams keep the tensor core and the exponentials busy side by side:
 // S, P and O exist twice in TMEM, each with a warpgroup of softmax threads
@@ -38,7 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int A_THREADS = 512;
-constexpr int A_CTAS = 152;                 // shares (SMs of a GB300)
+constexpr int A_CTAS = 152;                 // CTAs at most (the SMs of a GB300)
 constexpr int KT = 128;                     // keys a tile
 constexpr int A_MISC = 3072;                // barriers and small tables
 constexpr int SEGS = 4;                     // segments handed out ahead
@@ -65,7 +66,7 @@ struct ACfg {
 struct Seg {
     int b, h, c, n;             // request, K/V head, its cached and new tokens
     int row0, tok0, ntok, kt;   // first row of the batch and token of the request, tokens, key tiles of the whole
-    int k0, k1, flags, last;    // this part's key tiles; SEG_*; last CTA that holds a part
+    int k0, k1, flags, parts;   // this part's key tiles; SEG_*; first CTA << 16 | CTAs that hold parts
 };
 constexpr int SEG_VALID = 1;    // (0: the share is done)
 constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read once
@@ -75,12 +76,14 @@ struct AMisc {
     Seg seg[SEGS];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
     uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], v_clean[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
-        o_full, o_free, ml_full, qs_full, wg[2], turn[2], drain[2];
+        o_full, o_free, ml_full, qs_full, wg[2], turn[2], joins, drain[2];
     uint32_t tmem;
     int abort;
     int first_b;
     int nan_seg[NAN_SLOTS];
-    long long first_base, total;
+    long long first_off, total;
+    int first_c, first_n, first_r0;
+    Seg join[2];                // the divided segments: one that began elsewhere, one that ends elsewhere
     unsigned warp_sum[A_THREADS / 32];
     float2 ml[2][128];
 };
@@ -90,24 +93,23 @@ struct ATabs {
     int G, tpt;                 // heads a group, tokens a query tile
     uint32_t g_inv;             // ceil(2^16 / G): r / G = r g_inv >> 16 for the rows r < 256 of a pair
     int box;                    // keys a TMA box: gcd(page, 128)
+    int ctas;                   // CTAs of the grid: all run at once, one an SM
     int rp;                     // rows a partial result holds
     float2* part_ml;            // [2 A_CTAS][rp]: m (log2 units), l
-    float* part_o;              // [2 A_CTAS][rp][D]
-    struct Joint* joint;        // [A_CTAS]
+    float* part_o;              // [2 A_CTAS][D / 4][rp][4]
+    uint32_t* arrived;          // [A_CTAS][2]: warps that have written, and read, the parts of a
+                                // segment that begins in this share; 0 between calls
     StatusBlock* sb;
 };
 
-// A divided segment, left by the CTA that holds its first key tile.
-struct Joint {
-    int rows;                   // 0: none
-    int row0;                   // row of its first token
-    int kvh;
-    int last;                   // last CTA that holds a part
-    long long total;
-    int pad[2];
-};
-
-__device__ __forceinline__ long long share_begin(long long total, int c) { return total * c / A_CTAS; }
+// The shares of `ctas` CTAs, one key tile each at least (CTAs past the tiles have
+// none): first tile of share c, and the share that holds tile x.
+__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) {
+    return total < ctas ? (c < total ? c : total) : total * c / ctas;
+}
+__device__ __forceinline__ int share_of(long long total, int ctas, long long x) {
+    return total < ctas ? (int)x : (int)(((x + 1) * ctas - 1) / total);
+}
 
 // ---------------------------------------------------------------------------
 // bounded waits, whole warps
@@ -116,6 +118,7 @@ __device__ __forceinline__ long long share_begin(long long total, int c) { retur
 // A wait that runs out, or finds that another one did, leaves its number in
 // m->abort, and the kernel's end reports it.
 constexpr int WAIT_TRIES = 1 << 22;
+constexpr int JOIN_TRIES = 1 << 24;         // polls of another CTA's counter, some seconds
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, AMisc* m, int site) {
 #pragma unroll 1
     for (int i = 0; i < WAIT_TRIES; ++i) {
@@ -317,6 +320,67 @@ __device__ __forceinline__ float v_specials(VColumn x, int k0, int k1) {
     return sum;
 }
 
+// Some of a divided segment's output, from its parts in key order: the running
+// maximum moves from part to part as from tile to tile.
+struct JoinWork {
+    int i0, i1;                 // items (4 columns of a row) from i0 on in steps of 256
+    int rows, c0, parts;        // rows of the segment, first CTA, CTAs that hold parts
+    int row0, h;                // first row of the batch, K/V head
+};
+template <int D, int U>
+__device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, const ATabs& t, const JoinWork& w,
+                                           float v_scale) {
+#pragma unroll 1
+    for (int i0 = w.i0; i0 < w.i1; i0 += 256 * U) {
+        int r[U], x4[U];
+        float mx[U], sum[U];
+        float4 o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + 256 * u < w.i1 ? i0 + 256 * u : i0;   // (one past the end is done twice)
+            x4[u] = i / w.rows;
+            r[u] = i - x4[u] * w.rows;
+            mx[u] = -CUDART_INF_F;
+            sum[u] = 0.f;
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll (U == 1 ? 4 : 2)
+        for (int k = 0; k < w.parts; ++k) {
+            const int64_t slot = 2 * (w.c0 + k) + (k == 0);
+            const float2* const pm = t.part_ml + slot * t.rp;
+            const float4* const po = reinterpret_cast<const float4*>(t.part_o) + slot * (D / 4) * t.rp;
+            float2 ml[U];
+            float4 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                ml[u] = ld_dep(pm + r[u]);
+                q[u] = ld_dep(po + x4[u] * t.rp + r[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float top = fmaxf(mx[u], ml[u].x), zero = top == -CUDART_INF_F ? 0.f : top;
+                const float f = ptx::ex2(mx[u] - zero), e = ml[u].y == 0.f ? 0.f : ptx::ex2(ml[u].x - zero);
+                mx[u] = top;
+                sum[u] = sum[u] * f + ml[u].y * e;
+                o[u].x = o[u].x * f + q[u].x * e;
+                o[u].y = o[u].y * f + q[u].y * e;
+                o[u].z = o[u].z * f + q[u].z * e;
+                o[u].w = o[u].w * f + q[u].w * e;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int tk = by_g(r[u], t);
+            const int64_t at = (int64_t)(w.row0 + tk) * d.Hq + w.h * t.G + r[u] - tk * t.G;
+            const float sc = (sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u])) * v_scale;
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + 4 * x4[u]) =
+                make_uint2(ptx::cvt_bf16x2(o[u].x * sc, o[u].y * sc), ptx::cvt_bf16x2(o[u].z * sc, o[u].w * sc));
+            if (a.lse && x4[u] == 0)
+                a.lse[at] = sum[u] == 0.f ? -CUDART_INF_F : (mx[u] + log2f(sum[u])) * 0.69314718055994531f;
+        }
+    }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(A_THREADS, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
@@ -351,9 +415,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             if (i == at(&m->o_full)) n = 2;
             if (i >= at(&m->o_free) && i < at(m->wg)) n = 8;
             if (i >= at(m->wg) && i < at(m->drain)) n = 4;                                   // and turn
+            if (i == at(&m->joins)) n = 256;
             ptx::mbar_init(&m->seg_full[i], n);
         }
         if (lane < NAN_SLOTS) m->nan_seg[lane] = 0;
+        if (lane < 2) m->join[lane].parts = 0;
         if (lane == 0) {
             m->abort = 0;
             ptx::prefetch_tensormap(&tm_k);
@@ -365,53 +431,51 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     if (warp == 1) ptx::tmem_alloc(&m->tmem, 512);
     pdl_wait();
     KT_MARK(K_TREE_ATTN, 1);
-    pdl_trigger();   // k_tree_join, which waits for this grid before it reads anything
 
-    // this CTA's share: a scan of the requests' key tiles (in 32 bits: a thread's
-    // requests' tiles are below 2^30 by the shape's limits unless prompts are
-    // immense, so in units that fit; see the 64-bit total below)
+    // this CTA's share: a scan of the requests' key tiles
     {
         const int per = (d.B + A_THREADS - 1) / A_THREADS;
         const int b0 = tid * per, b1 = b0 + per < d.B ? b0 + per : d.B;
         long long sum = 0;
+        KvReq r{0, 0, 0, true};
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const KvReq r = kv_request(d, a.ctx_len, a.row_start, b);
+            r = kv_request(d, a.ctx_len, a.row_start, b);
             if (!r.ok && blockIdx.x == 0) latch_status(t.sb, MOE_ERR_BAD_LENGTHS, b);
             sum += head_tiles(d, r, pt) * d.Hkv;
         }
-        long long s = sum;
+        auto scan = [&](long long v) {
 #pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
-        }
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            return v;
+        };
+        const long long s = scan(sum);
         long long* const part = reinterpret_cast<long long*>(m->ml);   // free until the first segment's end
         if (lane == 31) part[warp] = s;
         __syncthreads();
-        long long total = 0, before = 0;
-#pragma unroll 1
-        for (int w = 0; w < A_THREADS / 32; ++w) {
-            if (w == warp) before = total;
-            total += part[w];
-        }
-        long long base = before + s - sum;
-        const long long pos = share_begin(total, blockIdx.x);
-        if (tid == 0) {
-            m->total = total;
-            t.joint[blockIdx.x].rows = 0;
-        }
+        const long long w = scan(lane < A_THREADS / 32 ? part[lane] : 0);
+        const long long total = __shfl_sync(0xffffffffu, w, 31);
+        const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+        long long base = (warp > 0 ? before : 0) + s - sum;
+        const long long pos = share_begin(total, t.ctas, blockIdx.x);
+        if (tid == 0) m->total = total;
         if (pos >= base && pos < base + sum) {
+            int b = b0;
 #pragma unroll 1
-            for (int b = b0; b < b1; ++b) {
-                const long long n = per == 1 ? sum : head_tiles(d, kv_request(d, a.ctx_len, a.row_start, b), pt) * d.Hkv;
-                if (pos < base + n) {
-                    m->first_b = b;
-                    m->first_base = base;
-                    break;
-                }
+            for (; per > 1; ++b) {
+                r = kv_request(d, a.ctx_len, a.row_start, b);
+                const long long n = head_tiles(d, r, pt) * d.Hkv;
+                if (pos < base + n) break;
                 base += n;
             }
+            m->first_b = b;
+            m->first_c = r.c;
+            m->first_n = r.n;
+            m->first_r0 = r.r0;
+            m->first_off = pos - base;
         }
     }
     ptx::tc_fence_before();
@@ -426,18 +490,23 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         if (warp == 14) {
             // ---- the share's segments -----------------------------------------
             const long long total = m->total;
-            long long pos = share_begin(total, blockIdx.x);
-            const long long end = share_begin(total, blockIdx.x + 1);
+            long long pos = share_begin(total, t.ctas, blockIdx.x);
+            const long long end = share_begin(total, t.ctas, blockIdx.x + 1);
             int b = 0, h = 0, p = 0, np = 1, kt = 0, k0 = 0;
             KvReq r{0, 0, 0, true};
             if (pos < end) {
                 b = m->first_b;
-                r = kv_request(d, a.ctx_len, a.row_start, b);
+                r = KvReq{m->first_c, m->first_n, m->first_r0, true};
                 np = (r.n + pt - 1) / pt;
                 const long long per_head = head_tiles(d, r, pt);
-                long long off = pos - m->first_base;
-                h = (int)(off / per_head);
+                long long off = m->first_off;
+                h = (off | per_head) >> 32 ? (int)(off / per_head) : (int)((uint32_t)off / (uint32_t)per_head);
                 off -= h * per_head;
+                if (d.W) {
+                    kt = pair_tiles(d, r, 0, pt);
+                    p = (int)((uint32_t)off / (uint32_t)kt);
+                    off -= (long long)p * kt;
+                }
 #pragma unroll 1
                 while (off >= (kt = pair_tiles(d, r, p, pt))) {
                     off -= kt;
@@ -463,8 +532,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     s->k0 = k0;
                     s->k1 = k1;
                     s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
-                    // a segment that begins here and ends elsewhere: the CTA of its last tile
-                    s->last = more && k0 == 0 && k1 < kt ? (int)(((pos + kt) * A_CTAS - 1) / total) : 0;
+                    s->parts = 0;
+                    if (more && (k0 > 0 || k1 < kt)) {   // divided: where its first and last tile are
+                        const int c0 = share_of(total, t.ctas, pos - k0);
+                        s->parts = c0 << 16 | (share_of(total, t.ctas, pos - k0 + kt - 1) - c0 + 1);
+                    }
                     ptx::mbar_arrive(&m->seg_full[i % SEGS]);
                 }
                 __syncwarp();
@@ -1169,11 +1241,62 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (!ok) break;
                 if (wq == 0 && lane == 0) ptx::mbar_arrive(&m->q_empty[qb]);
             }
-            if (warp == 4 && lane == 0 && w.k0 == 0 && !whole)
-                t.joint[blockIdx.x] = Joint{w.ntok * t.G, w.row0, w.h, w.last, m->total, {0, 0}};
             ptx::tc_fence_before();
+            if (!whole) {
+                // this warp's rows of the part are written: who counts them sees them
+                __threadfence();
+                if (warp == 4 && lane == 0) m->join[w.k0 == 0] = w;
+            }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&m->o_free);
+            if (lane == 0) {
+                ptx::mbar_arrive(&m->o_free);
+                if (!whole) ptx::red_release_gpu_add(t.arrived + 2 * (w.parts >> 16), 1);
+            }
+        }
+        // ---- divided segments --------------------------------------------------
+        // The CTAs that hold parts of a segment are few and all run (one an SM);
+        // each has written all its parts before it waits here.
+        ptx::mbar_arrive(&m->joins);
+        ok = ok && wait(&m->joins, 0, m, 22);
+#pragma unroll 1
+        for (int x = 0; x < 2 && ok; ++x) {
+            w = m->join[x];
+            if (w.parts == 0) continue;
+            const int c0 = w.parts >> 16, parts = w.parts & 0xFFFF;
+            uint32_t* const arrived = t.arrived + 2 * c0;
+            if (lane == 0) {
+#pragma unroll 1
+                for (int i = 0; ptx::ld_acquire_gpu(arrived) != 8u * parts; ++i) {
+                    if (i == JOIN_TRIES || *(volatile int*)&m->abort) {
+                        *(volatile int*)&m->abort = 23;
+                        ok = false;
+                        break;
+                    }
+                    __nanosleep(i < 16 ? 32 : 500);
+                }
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // the running maximum moves from part to part as from tile to tile
+            const int rows = w.ntok * t.G, mine = blockIdx.x - c0;
+            const float v_scale = E4M3 ? ld_dep(a.v_scale + w.h) : 1.f;
+            // 4 columns of a row an item.  Where a thread has several, four at once: the
+            // loads of a part for all of them, and of the next part, are under way
+            // together (256 rows and 3 parts: 10 us against 18 us one by one).
+            const int all = rows * (D / 4);
+            const JoinWork jw{(int)((long long)all * mine / parts) + tid - 128,
+                              (int)((long long)all * (mine + 1) / parts), rows, c0, parts, w.row0, w.h};
+            if (all / parts > 256)
+                join_items<D, 4>(d, a, t, jw, v_scale);
+            else
+                join_items<D, 1>(d, a, t, jw, v_scale);
+            // the last warp past the wait leaves the counters as it found them
+            __syncwarp();
+            if (lane == 0 && atomicAdd(arrived + 1, 1u) == 8u * parts - 1) {
+                arrived[0] = 0;
+                arrived[1] = 0;
+            }
         }
     }
     ptx::tc_fence_before();
@@ -1182,50 +1305,6 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
     if (tid == 0 && m->abort) latch_status(t.sb, MOE_ERR_TIMEOUT, 200 + m->abort);
     KT_MARK(K_TREE_ATTN, 2);
-}
-
-// The parts of the divided segments, added in key order: CTA x of the first grid
-// axis joins the segment whose first tile share x holds; a warp takes 4 columns of
-// 32 rows, a lane a row.
-constexpr int JOIN_WARPS = 8;
-
-template <int D>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) k_tree_join(const KvDims d, const AttnArgs a, const ATabs t) {
-    const int lane = threadIdx.x & 31, cta = blockIdx.x, row = blockIdx.y * 32 + lane;
-    const int x = (blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5)) * 4;
-    KT_MARK(K_TREE_JOIN, 0);
-    pdl_wait();
-    KT_MARK(K_TREE_JOIN, 1);
-    const int4 j = ld_dep(reinterpret_cast<const int4*>(t.joint + cta));   // rows, row0, kvh, last
-    if (row >= j.x) return;
-    const long long total = ld_dep(&t.joint[cta].total);
-    // part slots: 2 cta + 1 (the first), then 2 c of the CTAs that hold any tile;
-    // the running maximum moves from part to part as from tile to tile
-    float m = -CUDART_INF_F, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = cta; c <= j.w; ++c) {
-        const int64_t slot = 2 * c + (c == cta);
-        const bool any = c == cta || total >= A_CTAS || share_begin(total, c) != share_begin(total, c + 1);
-        const float2 ml = any ? ld_dep(t.part_ml + slot * t.rp + row) : make_float2(-CUDART_INF_F, 0.f);
-        const float4 p = any ? ld_dep(reinterpret_cast<const float4*>(t.part_o) + (slot * (D / 4) + x / 4) * t.rp + row)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float top = fmaxf(m, ml.x), zero = top == -CUDART_INF_F ? 0.f : top;
-        const float f = ptx::ex2(m - zero), e = ml.y == 0.f ? 0.f : ptx::ex2(ml.x - zero);
-        m = top;
-        sum = sum * f + ml.y * e;
-        o.x = o.x * f + p.x * e;
-        o.y = o.y * f + p.y * e;
-        o.z = o.z * f + p.z * e;
-        o.w = o.w * f + p.w * e;
-    }
-    const int tk = by_g(row, t), head = j.z * t.G + row - tk * t.G;
-    const int64_t at = (int64_t)(j.y + tk) * d.Hq + head;
-    const float s = (sum == 0.f ? 0.f : 1.f / sum) * (d.e4m3 ? ld_dep(a.v_scale + j.z) : 1.f);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + x) =
-        make_uint2(ptx::cvt_bf16x2(o.x * s, o.y * s), ptx::cvt_bf16x2(o.z * s, o.w * s));
-    if (a.lse && x == 0) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
-    KT_MARK(K_TREE_JOIN, 2);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -1240,11 +1319,13 @@ ATabs attn_tabs(const KvDims& d, char* ws, size_t* bytes) {
     t.rp = (int)(tokens * t.G);
     size_t o = sizeof(StatusBlock);
     auto take = [&](size_t n) { const size_t at = o; o = (o + n + 255) & ~(size_t)255; return at; };
-    const size_t joint = take(A_CTAS * sizeof(Joint));
+    const size_t arrived = take(A_CTAS * 2 * sizeof(uint32_t));   // in the prefix that moe_workspace_init clears
+    static_assert(sizeof(StatusBlock) + A_CTAS * 2 * sizeof(uint32_t) <= WS_ZERO_PREFIX, "zeroed prefix");
+    if (o < WS_ZERO_PREFIX) o = (WS_ZERO_PREFIX + 255) & ~(size_t)255;
     const size_t ml = take((size_t)2 * A_CTAS * t.rp * sizeof(float2));
     const size_t po = take((size_t)2 * A_CTAS * t.rp * d.D * sizeof(float));
     if (bytes) *bytes = o;
-    t.joint = reinterpret_cast<Joint*>(ws + joint);
+    t.arrived = reinterpret_cast<uint32_t*>(ws + arrived);
     t.part_ml = reinterpret_cast<float2*>(ws + ml);
     t.part_o = reinterpret_cast<float*>(ws + po);
     t.sb = reinterpret_cast<StatusBlock*>(ws);
@@ -1254,7 +1335,7 @@ ATabs attn_tabs(const KvDims& d, char* ws, size_t* bytes) {
 template <int D, bool E4M3>
 cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     using C = ACfg<D, E4M3>;
-    const ATabs t = attn_tabs(d, a.ws, nullptr);
+    ATabs t = attn_tabs(d, a.ws, nullptr);
     CUtensorMap tm_q, tm_q8, tm_q1, tm_k, tm_v;
     const uint64_t el = E4M3 ? 1 : 2;
     const CUtensorMapDataType dt = E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1276,15 +1357,11 @@ cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
         if (!q_map(&tm_q, t.tpt) || !q_map(&tm_q8, 8 * t.G <= 64 ? 8 : 1) || !q_map(&tm_q1, 1))
             return cudaErrorInvalidValue;
     }
+    t.ctas = num_sms() < A_CTAS ? num_sms() : A_CTAS;
     cudaError_t e = cudaFuncSetAttribute(k_tree_attn<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin(K_TREE_ATTN, st);
-    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(A_CTAS), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
-    timing_end(st);
-    if (e != cudaSuccess) return e;
-    timing_begin(K_TREE_JOIN, st);
-    e = launch_pdl(k_tree_join<D>, dim3(A_CTAS, (t.rp + 31) / 32, D / 4 / JOIN_WARPS), dim3(32 * JOIN_WARPS), 0, st,
-                   d, a, t);
+    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(t.ctas), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
     timing_end(st);
     return e;
 }
