@@ -200,6 +200,25 @@ def test_append(T, Hkv, D, page, e4m3, layout):
             assert torch.equal(got.contiguous().view(torch.int16), w.contiguous().view(torch.int16))
 
 
+def test_append_codes_of_every_bf16():
+    """Every bf16 value under ordinary, exact, tiny and huge scales: the codes of the rounded quotient, ties among them."""
+    x = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    scales = torch.tensor([0.0137, 1.0, 0.75, 3.0, 1e-3, 1e-38, 1e-41, 1e30, 2.0 ** -8, 0.3333, 7.7, 100.0])
+    Hkv, D = len(scales), 64
+    T = (1 << 16) // D
+    rows = x.view(T, 1, D).expand(T, Hkv, D).contiguous()
+    want = (rows.float() / scales[None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
+    shape = moe.KVShape.of(1, T, Hkv, Hkv, D, 16, T // 16, T // 16, e4m3=True)
+    ws = moe.new_kv_workspace(shape)
+    k, v = (torch.zeros(T // 16, Hkv, 16, D, dtype=torch.uint8, device=DEV) for _ in range(2))
+    sc = scales.to(DEV)
+    moe.kv_append(shape, rows.to(DEV), rows.to(DEV), torch.arange(T, device=DEV), sc, sc, k, v, ws)
+    moe.check_device_status(ws, "kv_append")
+    got = k.transpose(1, 2).reshape(T, Hkv, D).cpu()
+    nan = (want & 0x7F) == 0x7F
+    assert torch.equal(nan, (got & 0x7F) == 0x7F) and torch.equal(got[~nan], want[~nan]) and torch.equal(k, v)
+
+
 def test_append_refuses_slots():
     shape = moe.KVShape.of(1, 2, 1, 1, 64, 8, 4, 4)
     ws = moe.new_kv_workspace(shape)
