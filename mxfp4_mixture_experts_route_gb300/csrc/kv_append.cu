@@ -25,7 +25,7 @@ struct Scale {
         const float r = __fdiv_rn(1.f, v);
         // (a scale whose reciprocal is not an ordinary number: always by division)
         const bool fine = v > 0x1p-120f && v < 0x1p120f;
-        lo = fine ? r * (1.f - 0x1p-21f) : 0.f;
+        lo = fine ? r * (1.f - 0x1p-21f) : 1.f;
         hi = fine ? r * (1.f + 0x1p-21f) : CUDART_NAN_F;
     }
 };

@@ -24,7 +24,7 @@
 //
 // Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q, 1 and 3
 // MMA issuers (one a stream), 2 cleans V tiles that hold keys some row does not
-// see, 14 finds the CTA's segments and hands them to the others, 4-7 and 8-11
+// see and counts them, 15 counts K tiles, 14 finds the CTA's segments and hands them to the others, 4-7 and 8-11
 // the softmax; 15 only keeps the register shares whole.
 //
 // Instructions come from a small cache, and a call's first pass through any code
@@ -75,11 +75,12 @@ constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read
 struct AMisc {
     Seg seg[SEGS];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
-    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], v_clean[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
         o_full, o_free, ml_full, qs_full, wg[2], turn[2], joins, drain[2];
     uint32_t tmem;
     int abort;
     int first_b;
+    uint32_t landed[2];         // tiles of K, and of V, that have landed (and are clean): in order, never reset
     int nan_seg[NAN_SLOTS];
     long long first_off, total;
     int first_c, first_n, first_r0;
@@ -124,6 +125,18 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, AMisc* m, i
     for (int i = 0; i < WAIT_TRIES; ++i) {
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity, 1000u))) return true;
         if (*(volatile int*)&m->abort) return false;
+    }
+    *(volatile int*)&m->abort = site;
+    return false;
+}
+
+// Waits until tile number `tile` (from 0 on) of a ring has landed.
+__device__ __forceinline__ bool wait_landed(const uint32_t* landed, uint32_t tile, AMisc* m, int site) {
+#pragma unroll 1
+    for (int i = 0; i < JOIN_TRIES; ++i) {
+        if ((int32_t)(ptx::ld_acquire_cta(landed) - tile) > 0) return true;
+        if (*(volatile int*)&m->abort) return false;
+        if (i > 8) __nanosleep(40);
     }
     *(volatile int*)&m->abort = site;
     return false;
@@ -406,9 +419,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
         for (int i = lane; i < N; i += 32) {
             uint32_t n = 1;
-            if (i >= at(m->seg_empty) && i < at(m->k_full)) n = E4M3 ? 13 : 14;              // roles
+            if (i >= at(m->seg_empty) && i < at(m->k_full)) n = E4M3 ? 14 : 15;              // roles
             if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
-            if (i >= at(m->v_empty) && i < at(m->v_clean)) n = 2;
+            if (i >= at(m->v_empty) && i < at(m->q_full)) n = 2;
             if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
             if (i >= at(m->q_empty) && i < at(m->s_full)) n = 2;
             if (i >= at(&m->p_full[0][0]) && i < at(&m->o_full)) n = 4;
@@ -419,7 +432,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             ptx::mbar_init(&m->seg_full[i], n);
         }
         if (lane < NAN_SLOTS) m->nan_seg[lane] = 0;
-        if (lane < 2) m->join[lane].parts = 0;
+        if (lane < 2) {
+            m->join[lane].parts = 0;
+            m->landed[lane] = 0;
+        }
         if (lane == 0) {
             m->abort = 0;
             ptx::prefetch_tensormap(&tm_k);
@@ -675,10 +691,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // ---- MMA issuers: warp 1 for stream 0, warp 3 for stream 1 ---------
             // The whole warp walks and waits, one lane issues: descriptors built
             // from values that are the same in the whole warp stay in uniform
-            // registers, and a product costs a few instructions.  An issuer waits
-            // for, and releases, every tile of the rings, also those that only the
-            // other stream uses, so that neither can be two phases ahead of or
-            // behind a barrier (a parity wait takes two phases for none).
+            // registers, and a product costs a few instructions.  Tiles are waited for
+            // by count, not by their barriers' phases, so that an issuer can pass over
+            // the tiles of the other stream (a phase may be two ahead, which a parity
+            // wait takes for none); who uses a tile alone releases it for both.
             // S of the stream's next tile is begun right after the product with
             // this one's weights, in whose place it lies; that product in two
             // halves, the first while the weights of the second are made (one go
@@ -688,8 +704,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
             const int s = warp >> 1;
             uint32_t nq = 0, n_p0 = 0, n_p1 = 0, n_seg = 0;
-            Ring<C::NK> kr;
-            Ring<C::NV> vr;
+            uint32_t base = 0;                                                 // the segment's first tile in the rings
             bool ok = true;
             const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring), v0 = ptx::smem_u32(v_ring);
             const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
@@ -703,31 +718,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
                 ok = wait(&m->q_full[qb], (nq_s >> 1) & 1, m, 5);
                 // the previous segment's O is read before the first product into it
-                bool o_free = n_seg == 0, add = false, have = false;
-                uint32_t ks = 0, vs = 0;
-                // step j: tile j of V, with K of the stream's next tile taken before
-                int jk = 0;
+                bool o_free = n_seg == 0, add = false;
+                // step j: V of tile j and K of the stream's next one
 #pragma unroll 1
                 for (int j = first - step; j < mt && ok; j += step) {
-                    const bool nx = j + step < mt && j + step >= 0;
-                    // past tiles of the other stream, to the own ones
-#pragma unroll 1
-                    for (const int to = nx ? j + step : mt - 1; jk <= to && ok; ++jk) {
-                        ks = same(kr.slot);
-                        ok = wait(&m->k_full[ks], kr.phase, m, 6);
-                        kr.next();
-                        if (!(nx && jk == to) && ok && ptx::elect_one()) ptx::mma_commit(&m->k_empty[ks]);
-                        __syncwarp();
-                    }
-#pragma unroll 1
-                    for (int jv = have ? j - step + 1 : 0; jv <= j && ok; ++jv) {
-                        vs = same(vr.slot);
-                        ok = wait(&m->v_clean[vs], vr.phase, m, 7);            // landed and clean
-                        vr.next();
-                        if (jv != j && ok && ptx::elect_one()) ptx::mma_commit(&m->v_empty[vs]);
-                        __syncwarp();
-                    }
-                    if (j >= 0) have = true;
+                    const bool nx = j + step < mt;
+                    const uint32_t ks = same((base + j + step) % C::NK), vs = same((base + j) % C::NV);
+                    if (nx) ok = wait_landed(&m->landed[0], base + j + step, m, 6);
+                    if (j >= 0) ok = ok && wait_landed(&m->landed[1], base + j, m, 7);
                     if (j >= 0 && !o_free && ok) {
                         ok = wait(&m->o_free, (n_seg - 1) & 1, m, 8);
                         o_free = true;
@@ -759,7 +757,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                                           ptx::smem_desc<C::SW>(vh + (e * C::KSTEP * C::SW >> 4)), id_o,
                                                           (part | e) ? 1u : more_o);
                                 }
-                                if (half) ptx::mma_commit(&m->v_empty[vs]);
+                                if (half) {
+                                    ptx::mma_commit(&m->v_empty[vs]);
+                                    if (!two) ptx::mma_commit(&m->v_empty[vs]);
+                                }
                             }
                             if (half && nx) {       // S = Q K^T
 #pragma unroll
@@ -773,27 +774,12 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                 }
                                 ptx::mma_commit(&m->s_full[s]);
                                 ptx::mma_commit(&m->k_empty[ks]);
+                                if (!two) ptx::mma_commit(&m->k_empty[ks]);
                             }
                         }
                         __syncwarp();
                         add = j >= 0;
                     }
-                }
-                // what is left of the rings is the other stream's
-#pragma unroll 1
-                for (; jk < mt && ok; ++jk) {
-                    ok = wait(&m->k_full[kr.slot], kr.phase, m, 10);
-                    if (ok && ptx::elect_one()) ptx::mma_commit(&m->k_empty[kr.slot]);
-                    __syncwarp();
-                    kr.next();
-                }
-                const int own_last = first < mt ? first + (mt - 1 - first) / step * step : -1;
-#pragma unroll 1
-                for (int jv = own_last + 1; jv < mt && ok; ++jv) {
-                    ok = wait(&m->v_clean[vr.slot], vr.phase, m, 11);
-                    if (ok && ptx::elect_one()) ptx::mma_commit(&m->v_empty[vr.slot]);
-                    __syncwarp();
-                    vr.next();
                 }
                 // (a stream without tiles keeps step with the segments)
                 if (ok && !o_free) ok = wait(&m->o_free, (n_seg - 1) & 1, m, 12);
@@ -807,6 +793,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 }
                 __syncwarp();
                 nq += two ? 2 : 1;
+                base += mt;
             }
             if (!ok) {
                 // products in flight end before TMEM and shared memory are given up
@@ -821,9 +808,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // reach rows whose weight for it is 0 (0 * NaN).  Rows of V past the end
             // are zeroed; non-finite entries of new tokens too, and the segment is
             // flagged, so that its epilogue puts them where they are seen.
-            // Every V tile passes through this warp: one that looked only at the tiles
-            // it cleans could be two phases ahead of or behind their barriers, which a
-            // parity wait takes for complete, or waits on for ever.
+            // Every V tile passes through this warp, which counts them.
+            uint32_t tiles = 0;
             Ring<C::NV> vr;
             bool ok = true;
 #pragma unroll 1
@@ -865,7 +851,23 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         if (bad && lane == 0) *(volatile int*)&m->nan_seg[seg % NAN_SLOTS] = seg + 1;
                         __syncwarp();
                     }
-                    if (lane == 0) ptx::mbar_arrive(&m->v_clean[vr.slot]);
+                    if (lane == 0) ptx::st_release_cta(&m->landed[1], ++tiles);
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 15) {
+            // ---- K tiles are counted ---------------------------------------------
+            Ring<C::NK> kr;
+            uint32_t tiles = 0;
+            bool ok = true;
+#pragma unroll 1
+            while (ok && in.next(m, w)) {
+#pragma unroll 1
+                for (int j = w.k0; j < w.k1; ++j, kr.next()) {
+                    ok = wait(&m->k_full[kr.slot], kr.phase, m, 10);
+                    if (!ok) break;
+                    if (lane == 0) ptx::st_release_cta(&m->landed[0], ++tiles);
+                    __syncwarp();
                 }
             }
         }
