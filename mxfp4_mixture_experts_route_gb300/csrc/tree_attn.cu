@@ -80,7 +80,8 @@ struct AMisc {
     uint32_t tmem;
     int abort;
     int first_b;
-    uint32_t landed[2];         // tiles of K, and of V, that have landed (and are clean): in order, never reset
+    uint32_t landed[3];         // tiles of K, and of V, that have landed (and are clean), and query tiles whose
+                                // buffer is free: in order, never reset
     int nan_seg[NAN_SLOTS];
     long long first_off, total;
     int first_c, first_n, first_r0;
@@ -394,6 +395,65 @@ __device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, c
     }
 }
 
+// A query tile as e4m3 rows hi and lo (leading and next 4 significant bits) under
+// one power of two a row, in `nc` copies, into the swizzled K-major layout: 16 (8)
+// lanes a row, 8 elements a lane; warp wi of nw.
+template <int D>
+__device__ __forceinline__ void q_terms(const KvDims& d, const AttnArgs& a, const ATabs& t, const Seg& w, int tile, int rows,
+                                        int nc, int wi, int nw, uint8_t* hi, float* scale) {
+    constexpr int SW = ACfg<D, true>::SW, QT = ACfg<D, true>::QT;
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, rs = 128 / nc;
+#pragma unroll 1
+    for (int r = wi * RPW + lane / LPR; r < (rows + RPW - 1) / RPW * RPW; r += nw * RPW) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+            x = ld_dep(reinterpret_cast<const uint4*>(
+                           reinterpret_cast<const uint16_t*>(a.q) +
+                           (int64_t)(w.row0 + tile * t.tpt + by_g(r, t)) * d.q_stride +
+                           (int64_t)(w.h * t.G + r - by_g(r, t) * t.G) * D) + sub);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        float f[8], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            top = fmaxf(top, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+        }
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^(134 - e) brings the row's maximum (exponent field e) to [128, 256)
+        // (a row below 2^-87 is as good as 0; one with an infinity has NaN scores)
+        int e = (int)(__float_as_uint(top) >> 23);
+        const bool inf = e == 255;
+        e = e < 40 ? 40 : (e > 250 ? 250 : e);
+        const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+        if (sub == 0) scale[r] = inf ? CUDART_NAN_F : __uint_as_float((uint32_t)(e - 7) << 23);
+        uint32_t vh[2], vl[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float y[4], z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = f[4 * i + k] * up;
+            const uint32_t p0 = ptx::cvt_e4m3x2(y[0], y[1]), p1 = ptx::cvt_e4m3x2(y[2], y[3]);
+            ptx::e4m3x2_to_f32(p0, z[0], z[1]);
+            ptx::e4m3x2_to_f32(p1, z[2], z[3]);
+            vh[i] = p0 | p1 << 16;
+            vl[i] = ptx::cvt_e4m3x2(y[0] - z[0], y[1] - z[1]) |
+                    ptx::cvt_e4m3x2(y[2] - z[2], y[3] - z[3]) << 16;
+        }
+        // row r of SW bytes, its 16-byte pieces exchanged by the swizzle
+        // (copies are a multiple of 32 rows apart: the same exchange)
+        const uint32_t chunk = (uint32_t)(sub >> 1) ^ (SW == 128 ? (r & 7) : ((r >> 1) & 3));
+#pragma unroll 1
+        for (int k = 0; k < nc; ++k) {
+            uint8_t* const to = hi + (k * rs + r) * SW + chunk * 16 + (sub & 1) * 8;
+            *reinterpret_cast<uint2*>(to) = make_uint2(vh[0], vh[1]);
+            *reinterpret_cast<uint2*>(to + QT / 2) = make_uint2(vl[0], vl[1]);
+        }
+    }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(A_THREADS, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q8,
@@ -419,7 +479,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
         for (int i = lane; i < N; i += 32) {
             uint32_t n = 1;
-            if (i >= at(m->seg_empty) && i < at(m->k_full)) n = E4M3 ? 14 : 15;              // roles
+            if (i >= at(m->seg_empty) && i < at(m->k_full)) n = 15;                          // roles
             if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
             if (i >= at(m->v_empty) && i < at(m->q_full)) n = 2;
             if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
@@ -432,10 +492,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             ptx::mbar_init(&m->seg_full[i], n);
         }
         if (lane < NAN_SLOTS) m->nan_seg[lane] = 0;
-        if (lane < 2) {
-            m->join[lane].parts = 0;
-            m->landed[lane] = 0;
-        }
+        if (lane < 2) m->join[lane].parts = 0;
+        if (lane < 3) m->landed[lane] = 0;
         if (lane == 0) {
             m->abort = 0;
             ptx::prefetch_tensormap(&tm_k);
@@ -648,7 +706,29 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 for (uint32_t i = loads > slots ? loads - slots : 0; i < loads; ++i)
                     ptx::mbar_wait_warp(&full[i % slots], (i / slots) & 1, &none, 10000000ull);
             }
-        } else if (warp == 13 && !E4M3) {
+        } else if (warp == 13 && E4M3) {
+            // ---- query tiles of few rows, and leave to make the others' terms -----
+            uint32_t nq = 0;
+            bool ok = true;
+#pragma unroll 1
+            while (ok && in.next(m, w)) {
+                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies(w.ntok, t);
+#pragma unroll 1
+                for (int i = 0; i < nt; ++i, ++nq) {
+                    const uint32_t qb = nq & 1;
+                    ok = wait(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, m, 4);
+                    if (!ok) break;
+                    if (nc > 1) {
+                        q_terms<D>(d, a, t, w, 0, w.ntok * t.G, nc, 0, 1, sm + qb * C::QT, q_scale + qb * 128);
+                        ptx::fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_n(&m->q_full[qb], 8);
+                    }
+                    if (lane == 0) ptx::st_release_cta(&m->landed[2], nq + 1);
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 13) {
             // ---- query tiles ----------------------------------------------------
             uint32_t nq = 0;
             bool ok = true;
@@ -895,73 +975,26 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             const uint32_t qb = (nq + qs) & 1;
             float c = d.scale * 1.4426950408889634f;
             if (E4M3) {
-                // the query tile as e4m3 rows hi and lo (leading and next 4
-                // significant bits) under one power of two a row, into the
-                // swizzled K-major layout: 16 (8) lanes a row, 8 elements a lane
+                // wide tiles: these warps make the e4m3 terms, once the buffer is free;
+                // few rows: warp 13 does
                 c *= ld_dep(a.k_scale + w.h);
-                ok = wait(&m->q_empty[qb], (((nq + qs) >> 1) & 1) ^ 1, m, 14);
-                if (!ok) break;
-                constexpr int LPR = D / 8, RPW = 32 / LPR;
-                uint8_t* const hi = sm + qb * C::QT;
-                const int nw = two ? 4 : 8, wi = two ? wq : warp - 4;    // warps that share the tile
-                const int sub = lane % LPR;
-#pragma unroll 1
-                for (int r = wi * RPW + lane / LPR; r < (rows + RPW - 1) / RPW * RPW; r += nw * RPW) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        x = ld_dep(reinterpret_cast<const uint4*>(
-                                       reinterpret_cast<const uint16_t*>(a.q) +
-                                       (int64_t)(w.row0 + qs * t.tpt + by_g(r, t)) * d.q_stride +
-                                       (int64_t)(w.h * t.G + r - by_g(r, t) * t.G) * D) + sub);
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    float f[8], top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[2 * i] = __uint_as_float(u[i] << 16);
-                        f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-                        top = fmaxf(top, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+                if (nc == 1) {
+                    ok = wait_landed(&m->landed[2], nq + qs, m, 14);
+                    if (!ok) break;
+                    q_terms<D>(d, a, t, w, qs, rows, 1, two ? wq : warp - 4, two ? 4 : 8, sm + qb * C::QT,
+                               q_scale + qb * 128);
+                    ptx::fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive_n(&m->q_full[qb], two ? 2 : 1);
+                        ptx::mbar_arrive(&m->qs_full);
                     }
-#pragma unroll
-                    for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // 2^(134 - e) brings the row's maximum (exponent field e) to [128, 256)
-                    // (a row below 2^-87 is as good as 0; one with an infinity has NaN scores)
-                    int e = (int)(__float_as_uint(top) >> 23);
-                    const bool inf = e == 255;
-                    e = e < 40 ? 40 : (e > 250 ? 250 : e);
-                    const float up = __uint_as_float((uint32_t)(261 - e) << 23);
-                    if (sub == 0) q_scale[qb * 128 + r] = inf ? CUDART_NAN_F : __uint_as_float((uint32_t)(e - 7) << 23);
-                    uint32_t vh[2], vl[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float y[4], z[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) y[k] = f[4 * i + k] * up;
-                        const uint32_t p0 = ptx::cvt_e4m3x2(y[0], y[1]), p1 = ptx::cvt_e4m3x2(y[2], y[3]);
-                        ptx::e4m3x2_to_f32(p0, z[0], z[1]);
-                        ptx::e4m3x2_to_f32(p1, z[2], z[3]);
-                        vh[i] = p0 | p1 << 16;
-                        vl[i] = ptx::cvt_e4m3x2(y[0] - z[0], y[1] - z[1]) |
-                                ptx::cvt_e4m3x2(y[2] - z[2], y[3] - z[3]) << 16;
-                    }
-                    // row r of SW bytes, its 16-byte pieces exchanged by the swizzle
-                    // (copies are a multiple of 32 rows apart: the same exchange)
-                    const uint32_t chunk = (uint32_t)(sub >> 1) ^ (C::SW == 128 ? (r & 7) : ((r >> 1) & 3));
-#pragma unroll 1
-                    for (int k = 0; k < nc; ++k) {
-                        uint8_t* const to = hi + (k * rs + r) * C::SW + chunk * 16 + (sub & 1) * 8;
-                        *reinterpret_cast<uint2*>(to) = make_uint2(vh[0], vh[1]);
-                        *reinterpret_cast<uint2*>(to + C::QT / 2) = make_uint2(vl[0], vl[1]);
-                    }
+                    ok = wait(&m->qs_full, n_qs & 1, m, 15);             // the row scales are there
+                    ++n_qs;
+                } else {
+                    ok = wait(&m->q_full[qb], (nq >> 1) & 1, m, 15);
                 }
-                ptx::fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive_n(&m->q_full[qb], two ? 2 : 1);
-                    ptx::mbar_arrive(&m->qs_full);
-                }
-                ok = wait(&m->qs_full, n_qs & 1, m, 15);                 // the row scales are there
                 if (!ok) break;
-                ++n_qs;
                 c *= q_scale[qb * 128 + rl];
             }
             float mc = -CUDART_INF_F, l = 0.f;
@@ -1195,21 +1228,25 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     const int x0 = g * (D / 2) + pass * (D / 4);
                     if (pass == 1) ok = group_sync();                    // the first pass has been read
                     if (!ok) break;
-#pragma unroll 1
-                    for (int x = 0; x < D / 4; x += 16) {
-                        uint32_t u[16], v[16];
-                        ptx::tmem_ld16(tmem + lanes + C::T_O + x0 + x, u);
-                        ptx::tmem_ld16(tmem + lanes + C::T_O + 128 + x0 + x, v);
-                        ptx::tmem_ld_wait16(u);
-                        ptx::tmem_ld_wait16(v);
-                        float o[16];
+                    float u[32], v[32];
+                    if constexpr (D == 128) {
+                        ptx::tmem_ld32(tmem + lanes + C::T_O + x0, u);
+                        ptx::tmem_ld32(tmem + lanes + C::T_O + 128 + x0, v);
+                        ptx::tmem_ld_wait32(u);
+                        ptx::tmem_ld_wait32(v);
+                    } else {
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + x0, reinterpret_cast<uint32_t*>(u));
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + 128 + x0, reinterpret_cast<uint32_t*>(v));
+                        ptx::tmem_ld_wait16(reinterpret_cast<uint32_t*>(u));
+                        ptx::tmem_ld_wait16(reinterpret_cast<uint32_t*>(v));
+                    }
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            o[y] = (f0 != 0.f ? __uint_as_float(u[y]) * f0 : 0.f) +
-                                   (f1 != 0.f ? __uint_as_float(v[y]) * f1 : 0.f);
+                    for (int y = 0; y < W4; ++y) {
+                        float o[4];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            stage[piece(row, x / 4 + y)] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = (f0 != 0.f ? u[4 * y + e] * f0 : 0.f) + (f1 != 0.f ? v[4 * y + e] * f1 : 0.f);
+                        stage[piece(row, y)] = make_float4(o[0], o[1], o[2], o[3]);
                     }
                     ok = group_sync();
                     if (!ok) break;
@@ -1260,27 +1297,27 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         // each has written all its parts before it waits here.
         ptx::mbar_arrive(&m->joins);
         ok = ok && wait(&m->joins, 0, m, 22);
+        if (ok && lane < 2 && m->join[lane].parts) {
+            const int parts = m->join[lane].parts;
+            const uint32_t* const arrived = t.arrived + 2 * (parts >> 16);
+#pragma unroll 1
+            for (int i = 0; ptx::ld_acquire_gpu(arrived) != 8u * (parts & 0xFFFF); ++i) {
+                if (i == JOIN_TRIES || *(volatile int*)&m->abort) {
+                    *(volatile int*)&m->abort = 23;
+                    ok = false;
+                    break;
+                }
+                __nanosleep(i < 16 ? 32 : 500);
+            }
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
             w = m->join[x];
             if (w.parts == 0) continue;
             const int c0 = w.parts >> 16, parts = w.parts & 0xFFFF;
             uint32_t* const arrived = t.arrived + 2 * c0;
-            if (lane == 0) {
-#pragma unroll 1
-                for (int i = 0; ptx::ld_acquire_gpu(arrived) != 8u * parts; ++i) {
-                    if (i == JOIN_TRIES || *(volatile int*)&m->abort) {
-                        *(volatile int*)&m->abort = 23;
-                        ok = false;
-                        break;
-                    }
-                    __nanosleep(i < 16 ? 32 : 500);
-                }
-            }
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            // the running maximum moves from part to part as from tile to tile
             const int rows = w.ntok * t.G, mine = blockIdx.x - c0;
             const float v_scale = E4M3 ? ld_dep(a.v_scale + w.h) : 1.f;
             // 4 columns of a row an item.  Where a thread has several, four at once: the
