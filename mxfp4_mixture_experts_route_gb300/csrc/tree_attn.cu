@@ -39,7 +39,7 @@ namespace moe {
 namespace {
 
 constexpr int A_THREADS = 512;
-constexpr int A_CTAS = 152;                 // CTAs at most (the SMs of a GB300)
+constexpr int A_CTAS = 152;                 // CTAs, all running at once: the SMs of a GB300
 constexpr int KT = 128;                     // keys a tile
 constexpr int A_MISC = 3072;                // barriers and small tables
 constexpr int SEGS = 4;                     // segments handed out ahead
@@ -76,7 +76,7 @@ struct AMisc {
     Seg seg[SEGS];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
     uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
-        o_full, o_free, ml_full, qs_full, wg[2], turn[2], joins, drain[2];
+        o_full, o_free, ml_full, qs_full, wg[2], turn[2], drain[2];
     uint32_t tmem;
     int abort;
     int first_b;
@@ -95,7 +95,6 @@ struct ATabs {
     int G, tpt;                 // heads a group, tokens a query tile
     uint32_t g_inv;             // ceil(2^16 / G): r / G = r g_inv >> 16 for the rows r < 256 of a pair
     int box;                    // keys a TMA box: gcd(page, 128)
-    int ctas;                   // CTAs of the grid: all run at once, one an SM
     int rp;                     // rows a partial result holds
     float2* part_ml;            // [2 A_CTAS][rp]: m (log2 units), l
     float* part_o;              // [2 A_CTAS][D / 4][rp][4]
@@ -104,13 +103,15 @@ struct ATabs {
     StatusBlock* sb;
 };
 
-// The shares of `ctas` CTAs, one key tile each at least (CTAs past the tiles have
-// none): first tile of share c, and the share that holds tile x.
-__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) {
-    return total < ctas ? (c < total ? c : total) : total * c / ctas;
+// The shares, one key tile each at least (CTAs past the tiles have none): first
+// tile of share c, and the share that holds tile x.
+__device__ __forceinline__ long long share_begin(long long total, int c) {
+    return total < A_CTAS ? (c < total ? c : total) : total * c / A_CTAS;
 }
-__device__ __forceinline__ int share_of(long long total, int ctas, long long x) {
-    return total < ctas ? (int)x : (int)(((x + 1) * ctas - 1) / total);
+__device__ __forceinline__ int share_of(long long total, long long x) {
+    return total < A_CTAS ? (int)x
+           : total >> 24  ? (int)(((x + 1) * A_CTAS - 1) / total)
+                          : (int)(((uint32_t)(x + 1) * A_CTAS - 1) / (uint32_t)total);
 }
 
 // ---------------------------------------------------------------------------
@@ -334,32 +335,46 @@ __device__ __forceinline__ float v_specials(VColumn x, int k0, int k1) {
     return sum;
 }
 
-// Some of a divided segment's output, from its parts in key order: the running
-// maximum moves from part to part as from tile to tile.
+// Some of a divided segment's output, from its parts: the running maximum moves
+// from part to part as from tile to tile.  U items a thread at once, or one by
+// SPLIT threads next to each other, each with every SPLIT-th part.
 struct JoinWork {
-    int i0, i1;                 // items (4 columns of a row) from i0 on in steps of 256
+    int i0, i1;                 // items (4 columns of a row)
+    int th, nth;                // this thread of the threads that share them
     int rows, c0, parts;        // rows of the segment, first CTA, CTAs that hold parts
     int row0, h;                // first row of the batch, K/V head
 };
-template <int D, int U>
+template <int D, int U, int SPLIT>
 __device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, const ATabs& t, const JoinWork& w,
                                            float v_scale) {
+    const int sub = w.th % SPLIT, step = w.nth / SPLIT;
 #pragma unroll 1
-    for (int i0 = w.i0; i0 < w.i1; i0 += 256 * U) {
+    for (int base = w.i0; base < w.i1; base += step * U) {
         int r[U], x4[U];
         float mx[U], sum[U];
         float4 o[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + 256 * u < w.i1 ? i0 + 256 * u : i0;   // (one past the end is done twice)
+            int i = base + w.th / SPLIT + step * u;
+            if (i >= w.i1) i = w.i0;   // (past the end: the first is done again)
             x4[u] = i / w.rows;
             r[u] = i - x4[u] * w.rows;
             mx[u] = -CUDART_INF_F;
             sum[u] = 0.f;
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll (U == 1 ? 4 : 2)
-        for (int k = 0; k < w.parts; ++k) {
+        auto add = [&](int u, float m2, float s2, float4 q) {
+            const float top = fmaxf(mx[u], m2), zero = top == -CUDART_INF_F ? 0.f : top;
+            const float f = ptx::ex2(mx[u] - zero), e = s2 == 0.f ? 0.f : ptx::ex2(m2 - zero);
+            mx[u] = top;
+            sum[u] = sum[u] * f + s2 * e;
+            o[u].x = o[u].x * f + q.x * e;
+            o[u].y = o[u].y * f + q.y * e;
+            o[u].z = o[u].z * f + q.z * e;
+            o[u].w = o[u].w * f + q.w * e;
+        };
+#pragma unroll 2
+        for (int k = sub; k < w.parts; k += SPLIT) {
             const int64_t slot = 2 * (w.c0 + k) + (k == 0);
             const float2* const pm = t.part_ml + slot * t.rp;
             const float4* const po = reinterpret_cast<const float4*>(t.part_o) + slot * (D / 4) * t.rp;
@@ -371,19 +386,21 @@ __device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, c
                 q[u] = ld_dep(po + x4[u] * t.rp + r[u]);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float top = fmaxf(mx[u], ml[u].x), zero = top == -CUDART_INF_F ? 0.f : top;
-                const float f = ptx::ex2(mx[u] - zero), e = ml[u].y == 0.f ? 0.f : ptx::ex2(ml[u].x - zero);
-                mx[u] = top;
-                sum[u] = sum[u] * f + ml[u].y * e;
-                o[u].x = o[u].x * f + q[u].x * e;
-                o[u].y = o[u].y * f + q[u].y * e;
-                o[u].z = o[u].z * f + q[u].z * e;
-                o[u].w = o[u].w * f + q[u].w * e;
-            }
+            for (int u = 0; u < U; ++u) add(u, ml[u].x, ml[u].y, q[u]);
+        }
+#pragma unroll 1
+        for (int s = 1; s < SPLIT; s <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, mx[0], s), s2 = __shfl_xor_sync(0xffffffffu, sum[0], s);
+            float4 q;
+            q.x = __shfl_xor_sync(0xffffffffu, o[0].x, s);
+            q.y = __shfl_xor_sync(0xffffffffu, o[0].y, s);
+            q.z = __shfl_xor_sync(0xffffffffu, o[0].z, s);
+            q.w = __shfl_xor_sync(0xffffffffu, o[0].w, s);
+            add(0, m2, s2, q);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            if (sub != 0) continue;
             const int tk = by_g(r[u], t);
             const int64_t at = (int64_t)(w.row0 + tk) * d.Hq + w.h * t.G + r[u] - tk * t.G;
             const float sc = (sum[u] == 0.f ? 0.f : __fdividef(1.f, sum[u])) * v_scale;
@@ -483,12 +500,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
             if (i >= at(m->v_empty) && i < at(m->q_full)) n = 2;
             if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
-            if (i >= at(m->q_empty) && i < at(m->s_full)) n = 2;
+            if (i >= at(m->q_empty) && i < at(m->s_full)) n = 8;                             // softmax warps, or 4 an issuer
             if (i >= at(&m->p_full[0][0]) && i < at(&m->o_full)) n = 4;
             if (i == at(&m->o_full)) n = 2;
             if (i >= at(&m->o_free) && i < at(m->wg)) n = 8;
             if (i >= at(m->wg) && i < at(m->drain)) n = 4;                                   // and turn
-            if (i == at(&m->joins)) n = 256;
             ptx::mbar_init(&m->seg_full[i], n);
         }
         if (lane < NAN_SLOTS) m->nan_seg[lane] = 0;
@@ -534,7 +550,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         const long long total = __shfl_sync(0xffffffffu, w, 31);
         const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
         long long base = (warp > 0 ? before : 0) + s - sum;
-        const long long pos = share_begin(total, t.ctas, blockIdx.x);
+        const long long pos = share_begin(total, blockIdx.x);
         if (tid == 0) m->total = total;
         if (pos >= base && pos < base + sum) {
             int b = b0;
@@ -564,8 +580,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         if (warp == 14) {
             // ---- the share's segments -----------------------------------------
             const long long total = m->total;
-            long long pos = share_begin(total, t.ctas, blockIdx.x);
-            const long long end = share_begin(total, t.ctas, blockIdx.x + 1);
+            long long pos = share_begin(total, blockIdx.x);
+            const long long end = share_begin(total, blockIdx.x + 1);
             int b = 0, h = 0, p = 0, np = 1, kt = 0, k0 = 0;
             KvReq r{0, 0, 0, true};
             if (pos < end) {
@@ -608,8 +624,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
                     s->parts = 0;
                     if (more && (k0 > 0 || k1 < kt)) {   // divided: where its first and last tile are
-                        const int c0 = share_of(total, t.ctas, pos - k0);
-                        s->parts = c0 << 16 | (share_of(total, t.ctas, pos - k0 + kt - 1) - c0 + 1);
+                        const int c0 = share_of(total, pos - k0);
+                        s->parts = c0 << 16 | (share_of(total, pos - k0 + kt - 1) - c0 + 1);
                     }
                     ptx::mbar_arrive(&m->seg_full[i % SEGS]);
                 }
@@ -868,8 +884,13 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     ptx::mma_commit(&m->o_full);
                     // every product of this stream is issued, those that read Q among them
                     // (of few rows, the epilogue uses Q's memory and releases it)
-                    if (!narrow) ptx::mma_commit(&m->q_empty[nq & 1]);
-                    if (two) ptx::mma_commit(&m->q_empty[(nq + 1) & 1]);
+                    if (!narrow) {
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            ptx::mma_commit(&m->q_empty[nq & 1]);
+                            if (two) ptx::mma_commit(&m->q_empty[(nq + 1) & 1]);
+                        }
+                    }
                 }
                 __syncwarp();
                 nq += two ? 2 : 1;
@@ -1200,17 +1221,17 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 }
             } else {
                 // few rows: the copies' and streams' O of a row are added through the
-                // memory of Q, half the columns a warpgroup, in two passes
+                // memory of Q, half the columns a warpgroup, in two passes (one where
+                // all of them fit)
                 auto group_sync = [&] {
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&m->wg[g]);
                     return wait(&m->wg[g], n_wg++ & 1, m, 19);
                 };
-                constexpr int W4 = D / 16;                               // 16-byte pieces a row and pass
+                const int passes = nc * rows > 64 ? 2 : 1, cols = D / 2 / passes, w4 = cols / 4;
+                const int srow = cp * (passes == 1 ? rows : rs) + rl;    // this thread's row in the stage
                 float4* const stage = reinterpret_cast<float4*>(sm + qb * C::QT + g * (C::QT / 2));
-                auto piece = [](int r, int k) {                          // spread over the banks
-                    return r * W4 + (W4 == 8 ? k ^ (r & 7) : k ^ ((r >> 1) & 3));
-                };
+                auto piece = [&](int r, int k) { return r * w4 + (k ^ (r & (w4 - 1))); };   // spread over the banks
                 float top = -CUDART_INF_F, sum = 0.f;
 #pragma unroll 1
                 for (int k = 0; k < nc; ++k) top = ptx::max3(top, m->ml[0][k * rs + rl].x, m->ml[1][k * rs + rl].x);
@@ -1224,39 +1245,40 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 const float f0 = factor(m->ml[0][row], zero) * scale, f1 = factor(m->ml[1][row], zero) * scale;
                 if (g == 0 && row < rows) put_ml(tok, row, top, zero, sum);
 #pragma unroll 1
-                for (int pass = 0; pass < 2 && ok; ++pass) {
-                    const int x0 = g * (D / 2) + pass * (D / 4);
+                for (int pass = 0; pass < passes && ok; ++pass) {
+                    const int x0 = g * (D / 2) + pass * cols;
                     if (pass == 1) ok = group_sync();                    // the first pass has been read
                     if (!ok) break;
-                    float u[32], v[32];
-                    if constexpr (D == 128) {
-                        ptx::tmem_ld32(tmem + lanes + C::T_O + x0, u);
-                        ptx::tmem_ld32(tmem + lanes + C::T_O + 128 + x0, v);
-                        ptx::tmem_ld_wait32(u);
-                        ptx::tmem_ld_wait32(v);
-                    } else {
-                        ptx::tmem_ld16(tmem + lanes + C::T_O + x0, reinterpret_cast<uint32_t*>(u));
-                        ptx::tmem_ld16(tmem + lanes + C::T_O + 128 + x0, reinterpret_cast<uint32_t*>(v));
-                        ptx::tmem_ld_wait16(reinterpret_cast<uint32_t*>(u));
-                        ptx::tmem_ld_wait16(reinterpret_cast<uint32_t*>(v));
-                    }
+#pragma unroll 1
+                    for (int x = 0; x < cols; x += 16) {
+                        uint32_t u[16], v[16];
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + x0 + x, u);
+                        ptx::tmem_ld16(tmem + lanes + C::T_O + 128 + x0 + x, v);
+                        ptx::tmem_ld_wait16(u);
+                        ptx::tmem_ld_wait16(v);
+                        if (rl < rows) {
 #pragma unroll
-                    for (int y = 0; y < W4; ++y) {
-                        float o[4];
+                            for (int y = 0; y < 4; ++y) {
+                                float o[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = (f0 != 0.f ? u[4 * y + e] * f0 : 0.f) + (f1 != 0.f ? v[4 * y + e] * f1 : 0.f);
-                        stage[piece(row, y)] = make_float4(o[0], o[1], o[2], o[3]);
+                                for (int e = 0; e < 4; ++e)
+                                    o[e] = (f0 != 0.f ? __uint_as_float(u[4 * y + e]) * f0 : 0.f) +
+                                           (f1 != 0.f ? __uint_as_float(v[4 * y + e]) * f1 : 0.f);
+                                stage[piece(srow, x / 4 + y)] = make_float4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
+                        __syncwarp();
                     }
                     ok = group_sync();
                     if (!ok) break;
+                    const int next = passes == 1 ? rows : rs, sh = passes == 1 ? (D == 128 ? 4 : 3) : (D == 128 ? 3 : 2);
 #pragma unroll 1
-                    for (int i = row; i < rows * W4; i += 128) {
-                        const int r = i / W4, k = i % W4, x = x0 + 4 * k, tk = by_g(r, t);
+                    for (int i = row; i < rows << sh; i += 128) {
+                        const int r = i >> sh, k = i & (w4 - 1), x = x0 + 4 * k, tk = by_g(r, t);
                         float4 z = stage[piece(r, k)];
 #pragma unroll 1
-                        for (int e = rs; e < 128; e += rs) {
-                            const float4 q = stage[piece(e + r, k)];
+                        for (int e = 1; e < nc; ++e) {
+                            const float4 q = stage[piece(e * next + r, k)];
                             z.x += q.x; z.y += q.y; z.z += q.z; z.w += q.w;
                         }
                         if (whole)
@@ -1276,29 +1298,28 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 }
                 if (!ok) break;
                 ptx::fence_proxy_async_shared();                         // Q's next tile comes by TMA
-                ok = group_sync();
-                if (!ok) break;
-                if (wq == 0 && lane == 0) ptx::mbar_arrive(&m->q_empty[qb]);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&m->q_empty[qb]);
             }
             ptx::tc_fence_before();
-            if (!whole) {
-                // this warp's rows of the part are written: who counts them sees them
-                __threadfence();
-                if (warp == 4 && lane == 0) m->join[w.k0 == 0] = w;
-            }
             __syncwarp();
             if (lane == 0) {
                 ptx::mbar_arrive(&m->o_free);
-                if (!whole) ptx::red_release_gpu_add(t.arrived + 2 * (w.parts >> 16), 1);
+                if (!whole) {
+                    // (every warp leaves the same, and reads what it has left)
+                    m->join[w.k0 == 0] = w;
+                    // this warp's rows of the part are written: who counts them sees them
+                    ptx::red_release_gpu_add(t.arrived + 2 * (w.parts >> 16), 1);
+                }
             }
         }
         // ---- divided segments --------------------------------------------------
         // The CTAs that hold parts of a segment are few and all run (one an SM);
         // each has written all its parts before it waits here.
-        ptx::mbar_arrive(&m->joins);
-        ok = ok && wait(&m->joins, 0, m, 22);
-        if (ok && lane < 2 && m->join[lane].parts) {
-            const int parts = m->join[lane].parts;
+        __syncwarp();
+        const Seg* const mine = m->join;
+        if (ok && lane < 2 && mine[lane].parts) {
+            const int parts = mine[lane].parts;
             const uint32_t* const arrived = t.arrived + 2 * (parts >> 16);
 #pragma unroll 1
             for (int i = 0; ptx::ld_acquire_gpu(arrived) != 8u * (parts & 0xFFFF); ++i) {
@@ -1312,24 +1333,29 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, ok);
+        // two segments: one a warpgroup; one: both take it
+        const bool both = mine[0].parts && mine[1].parts;
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
-            w = m->join[x];
+            w = mine[x];
             if (w.parts == 0) continue;
             const int c0 = w.parts >> 16, parts = w.parts & 0xFFFF;
             uint32_t* const arrived = t.arrived + 2 * c0;
-            const int rows = w.ntok * t.G, mine = blockIdx.x - c0;
+            const int rows = w.ntok * t.G, at = blockIdx.x - c0;
             const float v_scale = E4M3 ? ld_dep(a.v_scale + w.h) : 1.f;
-            // 4 columns of a row an item.  Where a thread has several, four at once: the
-            // loads of a part for all of them, and of the next part, are under way
-            // together (256 rows and 3 parts: 10 us against 18 us one by one).
-            const int all = rows * (D / 4);
-            const JoinWork jw{(int)((long long)all * mine / parts) + tid - 128,
-                              (int)((long long)all * (mine + 1) / parts), rows, c0, parts, w.row0, w.h};
-            if (all / parts > 256)
-                join_items<D, 4>(d, a, t, jw, v_scale);
-            else
-                join_items<D, 1>(d, a, t, jw, v_scale);
+            if (!both || x == g) {
+                // 4 columns of a row an item.  Where a thread has several, four at once: the
+                // loads of a part for all of them, and of the next part, are under way
+                // together (256 rows and 3 parts: 10 us against 18 us one by one).  Where
+                // there are few, four threads an item, each with every fourth part.
+                const int all = rows * (D / 4), th = both ? row : tid - 128, nth = both ? 128 : 256;
+                const JoinWork jw{(int)((long long)all * at / parts), (int)((long long)all * (at + 1) / parts),
+                                  th, nth, rows, c0, parts, w.row0, w.h};
+                if (jw.i1 - jw.i0 > nth)
+                    join_items<D, 4, 1>(d, a, t, jw, v_scale);
+                else
+                    join_items<D, 1, 4>(d, a, t, jw, v_scale);
+            }
             // the last warp past the wait leaves the counters as it found them
             __syncwarp();
             if (lane == 0 && atomicAdd(arrived + 1, 1u) == 8u * parts - 1) {
@@ -1374,7 +1400,7 @@ ATabs attn_tabs(const KvDims& d, char* ws, size_t* bytes) {
 template <int D, bool E4M3>
 cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     using C = ACfg<D, E4M3>;
-    ATabs t = attn_tabs(d, a.ws, nullptr);
+    const ATabs t = attn_tabs(d, a.ws, nullptr);
     CUtensorMap tm_q, tm_q8, tm_q1, tm_k, tm_v;
     const uint64_t el = E4M3 ? 1 : 2;
     const CUtensorMapDataType dt = E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1396,11 +1422,11 @@ cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
         if (!q_map(&tm_q, t.tpt) || !q_map(&tm_q8, 8 * t.G <= 64 ? 8 : 1) || !q_map(&tm_q1, 1))
             return cudaErrorInvalidValue;
     }
-    t.ctas = num_sms() < A_CTAS ? num_sms() : A_CTAS;
+    if (num_sms() < A_CTAS) return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(k_tree_attn<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     timing_begin(K_TREE_ATTN, st);
-    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(t.ctas), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
+    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(A_CTAS), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
     timing_end(st);
     return e;
 }
