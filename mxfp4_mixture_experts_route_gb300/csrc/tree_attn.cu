@@ -1063,12 +1063,22 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 };
                 auto nothing = [] {};
                 int last_half = 0;
+                // The warpgroups take turns: two at once would each take longer, and
+                // reach the tensor core together, which then waits for both.
+                if (g == 1 || n_turn > 0) ok = wait(&m->turn[g], (n_turn - (g ^ 1)) & 1, m, 20);
+                if (!ok) break;
+                ++n_turn;
+                auto hand_over = [&] {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
+                };
                 if (nc == 4) {
                     // this warp's quarter of the keys; the other quarters' weights are 0 in its rows
                     const uint32_t v = cp == 0 ? vis[0] : cp == 1 ? vis[1] : cp == 2 ? vis[2] : vis[3];
                     constexpr int PC = E4M3 ? 8 : 16;                    // columns of 32 keys' weights
                     softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, &v, have_o,
                                               nothing, mc, l);
+                    hand_over();
 #pragma unroll 1
                     for (int k = 1; k < 4; ++k) {
                         const uint32_t other = t_s + PC * ((cp + k) & 3);
@@ -1084,16 +1094,12 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     const uint32_t v[2] = {cp ? vis[2] : vis[0], cp ? vis[3] : vis[1]};
                     softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, v, have_o,
                                               nothing, mc, l);
+                    hand_over();
                     const uint32_t other = t_s + PC * (cp ^ 1);
                     ptx::tmem_st16_rep(other, 0);
                     ptx::tmem_st16_rep(other + (E4M3 ? 32 : 16), 0);
                 } else {
-                    // The warpgroups take turns: two at once would each take longer, and
-                    // reach the tensor core together, which then waits for both.
                     last_half = 1;
-                    if (g == 1 || n_turn > 0) ok = wait(&m->turn[g], (n_turn - (g ^ 1)) & 1, m, 20);
-                    if (!ok) break;
-                    ++n_turn;
                     auto half_done = [&] {
                         stored(0);
                         if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
@@ -1106,7 +1112,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 stored(last_half);
             }
             if (!ok) break;
-            if (nc == 1 && !two && g == 1 && mt % 2) {                   // the turn of a tile that stream 1 does not have
+            if (!two && g == 1 && mt % 2) {                   // the turn of a tile that stream 1 does not have
                 ok = wait(&m->turn[1], n_turn & 1, m, 21);
                 if (!ok) break;
                 ++n_turn;
