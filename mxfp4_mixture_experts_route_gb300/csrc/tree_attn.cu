@@ -71,6 +71,12 @@ struct Seg {
 constexpr int SEG_VALID = 1;    // (0: the share is done)
 constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read once
 
+// The line that shares are cut on: units a key tile with one and with two query
+// tiles, and a segment's own.
+struct Units {
+    int one, two, over;
+};
+
 // shared-memory tables behind the tiles
 struct AMisc {
     Seg seg[SEGS];
@@ -84,6 +90,7 @@ struct AMisc {
                                 // buffer is free: in order, never reset
     int nan_seg[NAN_SLOTS];
     long long first_off, total;
+    Units units;
     int first_c, first_n, first_r0;
     Seg join[2];                // the divided segments: one that began elsewhere, one that ends elsewhere
     unsigned warp_sum[A_THREADS / 32];
@@ -103,8 +110,16 @@ struct ATabs {
     StatusBlock* sb;
 };
 
-// The shares, one key tile each at least (CTAs past the tiles have none): first
-// tile of share c, and the share that holds tile x.
+// Shares are cut on a line on which a segment takes `over` units for its start and
+// end, then `two` (two query tiles) or `one` units a key tile; a share holds the
+// key tiles whose first unit lies in it.  Measured: 1.75 us a key tile for two
+// query tiles, 0.85 to 1.3 us for one, 4 to 5 us a segment.  With few key tiles a
+// share the line is the key tiles themselves, and a share holds one at least
+// (shares past the tiles none).
+__device__ __forceinline__ Units units_for(long long tiles) {
+    return tiles >= 8 * A_CTAS ? Units{2, 3, 8} : Units{1, 1, 0};   // (a share of 16 units or more holds a tile)
+}
+// first unit of share c, and the share that holds unit x
 __device__ __forceinline__ long long share_begin(long long total, int c) {
     return total < A_CTAS ? (c < total ? c : total) : total * c / A_CTAS;
 }
@@ -152,14 +167,19 @@ __device__ __forceinline__ int pair_tiles(const KvDims& d, const KvReq& r, int p
     const int upto = d.W || (p + 1) * pt > r.n ? r.n : (p + 1) * pt;
     return (r.c + upto + KT - 1) / KT;
 }
-// key tiles of a request, a K/V head
-__device__ __forceinline__ long long head_tiles(const KvDims& d, const KvReq& r, int pt) {
+// whether pair p of a request has two query tiles
+__device__ __forceinline__ bool pair_two(const KvReq& r, int p, int pt) { return r.n - p * pt > pt / 2; }
+__device__ __forceinline__ long long pair_units(const KvDims& d, const KvReq& r, int p, int pt, Units u) {
+    return u.over + (long long)(pair_two(r, p, pt) ? u.two : u.one) * pair_tiles(d, r, p, pt);
+}
+// units of a request, a K/V head
+__device__ __forceinline__ long long head_units(const KvDims& d, const KvReq& r, int pt, Units u) {
     if (r.n == 0) return 0;
     const int np = (r.n + pt - 1) / pt;
-    if (d.W) return (long long)np * pair_tiles(d, r, 0, pt);
+    if (d.W) return (np - 1) * pair_units(d, r, 0, pt, u) + pair_units(d, r, np - 1, pt, u);
     long long s = 0;
 #pragma unroll 1
-    for (int p = 0; p < np; ++p) s += pair_tiles(d, r, p, pt);
+    for (int p = 0; p < np; ++p) s += pair_units(d, r, p, pt, u);
     return s;
 }
 
@@ -526,13 +546,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     {
         const int per = (d.B + A_THREADS - 1) / A_THREADS;
         const int b0 = tid * per, b1 = b0 + per < d.B ? b0 + per : d.B;
-        long long sum = 0;
+        long long tiles = 0, cost = 0;
         KvReq r{0, 0, 0, true};
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             r = kv_request(d, a.ctx_len, a.row_start, b);
             if (!r.ok && blockIdx.x == 0) latch_status(t.sb, MOE_ERR_BAD_LENGTHS, b);
-            sum += head_tiles(d, r, pt) * d.Hkv;
+            tiles += head_units(d, r, pt, Units{1, 1, 0}) * d.Hkv;
+            cost += head_units(d, r, pt, units_for(8 * A_CTAS)) * d.Hkv;
         }
         auto scan = [&](long long v) {
 #pragma unroll 1
@@ -542,22 +563,31 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             }
             return v;
         };
-        const long long s = scan(sum);
+        const long long s1 = scan(tiles), s2 = scan(cost);
         long long* const part = reinterpret_cast<long long*>(m->ml);   // free until the first segment's end
-        if (lane == 31) part[warp] = s;
+        if (lane == 31) {
+            part[warp] = s1;
+            part[32 + warp] = s2;
+        }
         __syncthreads();
-        const long long w = scan(lane < A_THREADS / 32 ? part[lane] : 0);
-        const long long total = __shfl_sync(0xffffffffu, w, 31);
+        long long w = scan(lane < A_THREADS / 32 ? part[lane] : 0);
+        const Units u = units_for(__shfl_sync(0xffffffffu, w, 31));
+        const bool line = u.over > 0;
+        if (line) w = scan(lane < A_THREADS / 32 ? part[32 + lane] : 0);
+        const long long total = __shfl_sync(0xffffffffu, w, 31), sum = line ? cost : tiles;
         const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-        long long base = (warp > 0 ? before : 0) + s - sum;
+        long long base = (warp > 0 ? before : 0) + (line ? s2 : s1) - sum;
         const long long pos = share_begin(total, blockIdx.x);
-        if (tid == 0) m->total = total;
+        if (tid == 0) {
+            m->total = total;
+            m->units = u;
+        }
         if (pos >= base && pos < base + sum) {
             int b = b0;
 #pragma unroll 1
             for (; per > 1; ++b) {
                 r = kv_request(d, a.ctx_len, a.row_start, b);
-                const long long n = head_tiles(d, r, pt) * d.Hkv;
+                const long long n = head_units(d, r, pt, u) * d.Hkv;
                 if (pos < base + n) break;
                 base += n;
             }
@@ -579,61 +609,71 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         Seg w;
         if (warp == 14) {
             // ---- the share's segments -----------------------------------------
-            const long long total = m->total;
-            long long pos = share_begin(total, blockIdx.x);
+            const long long total = m->total, begin = share_begin(total, blockIdx.x);
             const long long end = share_begin(total, blockIdx.x + 1);
-            int b = 0, h = 0, p = 0, np = 1, kt = 0, k0 = 0;
+            const Units u = m->units;
+            long long at = begin;                         // first unit of the segment
+            int b = 0, h = 0, p = 0, np = 1, kt = 0, k0 = 0, per_tile = 1;
             KvReq r{0, 0, 0, true};
-            if (pos < end) {
+            if (begin < end) {
                 b = m->first_b;
                 r = KvReq{m->first_c, m->first_n, m->first_r0, true};
                 np = (r.n + pt - 1) / pt;
-                const long long per_head = head_tiles(d, r, pt);
+                const long long per_head = head_units(d, r, pt, u);
                 long long off = m->first_off;
                 h = (off | per_head) >> 32 ? (int)(off / per_head) : (int)((uint32_t)off / (uint32_t)per_head);
                 off -= h * per_head;
-                if (d.W) {
-                    kt = pair_tiles(d, r, 0, pt);
-                    p = (int)((uint32_t)off / (uint32_t)kt);
-                    off -= (long long)p * kt;
+                if (d.W && np > 1) {                      // all pairs but the last are alike
+                    const uint32_t n = (uint32_t)pair_units(d, r, 0, pt, u);
+                    p = (int)((uint32_t)off / n);
+                    if (p > np - 1) p = np - 1;
+                    off -= (long long)p * n;
                 }
 #pragma unroll 1
-                while (off >= (kt = pair_tiles(d, r, p, pt))) {
-                    off -= kt;
-                    ++p;
-                }
-                k0 = (int)off;
+                for (long long n; off >= (n = pair_units(d, r, p, pt, u)); ++p) off -= n;
+                at -= off;
+                per_tile = pair_two(r, p, pt) ? u.two : u.one;
+                kt = pair_tiles(d, r, p, pt);
+                if (off > u.over) k0 = (int)((uint32_t)(off - u.over + per_tile - 1) / (uint32_t)per_tile);
             }
 #pragma unroll 1
-            for (uint32_t i = 0;; ++i) {
-                const bool more = pos < end;
-                if (!wait(&m->seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1, m, 2)) break;
-                const int k1 = (int)(kt - k0 < end - pos ? kt : k0 + (end - pos));
-                if (lane == 0) {
-                    Seg* const s = &m->seg[i % SEGS];
-                    s->b = b;
-                    s->h = h;
-                    s->c = r.c;
-                    s->n = r.n;
-                    s->row0 = r.r0 + p * pt;
-                    s->tok0 = p * pt;
-                    s->ntok = r.n - p * pt < pt ? r.n - p * pt : pt;
-                    s->kt = kt;
-                    s->k0 = k0;
-                    s->k1 = k1;
-                    s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
-                    s->parts = 0;
-                    if (more && (k0 > 0 || k1 < kt)) {   // divided: where its first and last tile are
-                        const int c0 = share_of(total, pos - k0);
-                        s->parts = c0 << 16 | (share_of(total, pos - k0 + kt - 1) - c0 + 1);
+            for (uint32_t i = 0;;) {
+                const long long left = end - at - u.over;   // units from the segment's first tile to the share's end
+                const bool more = begin < end && left > (long long)k0 * per_tile;
+                if (!more || k0 < kt) {
+                    if (!wait(&m->seg_empty[i % SEGS], ((i / SEGS) & 1) ^ 1, m, 2)) break;
+                    const int k1 = left >= (long long)kt * per_tile
+                                       ? kt
+                                       : (int)((uint32_t)(left + per_tile - 1) / (uint32_t)per_tile);
+                    if (lane == 0) {
+                        Seg* const s = &m->seg[i % SEGS];
+                        s->b = b;
+                        s->h = h;
+                        s->c = r.c;
+                        s->n = r.n;
+                        s->row0 = r.r0 + p * pt;
+                        s->tok0 = p * pt;
+                        s->ntok = r.n - p * pt < pt ? r.n - p * pt : pt;
+                        s->kt = kt;
+                        s->k0 = k0;
+                        s->k1 = k1;
+                        s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
+                        s->parts = 0;
+                        if (more && (k0 > 0 || k1 < kt)) {   // divided: where its first and last tile are
+                            const int c0 = share_of(total, at + u.over);
+                            s->parts =
+                                c0 << 16 | (share_of(total, at + u.over + (long long)(kt - 1) * per_tile) - c0 + 1);
+                        }
+                        ptx::mbar_arrive(&m->seg_full[i % SEGS]);
                     }
-                    ptx::mbar_arrive(&m->seg_full[i % SEGS]);
+                    __syncwarp();
+                    ++i;
+                    if (!more) break;
                 }
-                __syncwarp();
-                if (!more) break;
-                pos += k1 - k0;
+                // (k0 == kt: the share begins inside the segment's last tile, which is another's)
+                at += u.over + (long long)kt * per_tile;
                 k0 = 0;
-                if (pos < end) {
+                if (at + u.over < end) {
                     if (++p == np) {
                         p = 0;
                         if (++h == d.Hkv) {
@@ -644,6 +684,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                             np = (r.n + pt - 1) / pt;
                         }
                     }
+                    per_tile = pair_two(r, p, pt) ? u.two : u.one;
                     kt = pair_tiles(d, r, p, pt);
                 }
             }
