@@ -116,9 +116,7 @@ struct ATabs {
 // query tiles, 0.85 to 1.3 us for one, 4 to 5 us a segment.  With few key tiles a
 // share the line is the key tiles themselves, and a share holds one at least
 // (shares past the tiles none).
-__device__ __forceinline__ Units units_for(long long tiles) {
-    return tiles >= 8 * A_CTAS ? Units{2, 3, 8} : Units{1, 1, 0};   // (a share of 16 units or more holds a tile)
-}
+constexpr int LINE_TILES = 8 * A_CTAS;      // (a share of 16 units or more holds a key tile)
 // first unit of share c, and the share that holds unit x
 __device__ __forceinline__ long long share_begin(long long total, int c) {
     return total < A_CTAS ? (c < total ? c : total) : total * c / A_CTAS;
@@ -546,37 +544,39 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     {
         const int per = (d.B + A_THREADS - 1) / A_THREADS;
         const int b0 = tid * per, b1 = b0 + per < d.B ? b0 + per : d.B;
-        long long tiles = 0, cost = 0;
+        long long sum = 0, upto = 0, total = 0;       // this thread's requests, those up to them, all
         KvReq r{0, 0, 0, true};
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            r = kv_request(d, a.ctx_len, a.row_start, b);
-            if (!r.ok && blockIdx.x == 0) latch_status(t.sb, MOE_ERR_BAD_LENGTHS, b);
-            tiles += head_units(d, r, pt, Units{1, 1, 0}) * d.Hkv;
-            cost += head_units(d, r, pt, units_for(8 * A_CTAS)) * d.Hkv;
-        }
-        auto scan = [&](long long v) {
-#pragma unroll 1
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            return v;
-        };
-        const long long s1 = scan(tiles), s2 = scan(cost);
         long long* const part = reinterpret_cast<long long*>(m->ml);   // free until the first segment's end
-        if (lane == 31) {
-            part[warp] = s1;
-            part[32 + warp] = s2;
+        Units u{1, 1, 0};
+        // first in key tiles; again in the line's units if there are enough of them
+#pragma unroll 1
+        for (int round = 0;; ++round) {
+            sum = 0;
+#pragma unroll 1
+            for (int b = b0; b < b1; ++b) {
+                r = kv_request(d, a.ctx_len, a.row_start, b);
+                if (!r.ok && blockIdx.x == 0) latch_status(t.sb, MOE_ERR_BAD_LENGTHS, b);
+                sum += head_units(d, r, pt, u) * d.Hkv;
+            }
+            auto scan = [&](long long v) {
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long x = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += x;
+                }
+                return v;
+            };
+            const long long s = scan(sum);
+            if (lane == 31) part[16 * round + warp] = s;
+            __syncthreads();
+            const long long w = scan(lane < A_THREADS / 32 ? part[16 * round + lane] : 0);
+            const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+            total = __shfl_sync(0xffffffffu, w, 31);
+            upto = (warp > 0 ? before : 0) + s;
+            if (round == 1 || total < LINE_TILES) break;
+            u = Units{2, 3, 8};
         }
-        __syncthreads();
-        long long w = scan(lane < A_THREADS / 32 ? part[lane] : 0);
-        const Units u = units_for(__shfl_sync(0xffffffffu, w, 31));
-        const bool line = u.over > 0;
-        if (line) w = scan(lane < A_THREADS / 32 ? part[32 + lane] : 0);
-        const long long total = __shfl_sync(0xffffffffu, w, 31), sum = line ? cost : tiles;
-        const long long before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-        long long base = (warp > 0 ? before : 0) + (line ? s2 : s1) - sum;
+        long long base = upto - sum;
         const long long pos = share_begin(total, blockIdx.x);
         if (tid == 0) {
             m->total = total;
