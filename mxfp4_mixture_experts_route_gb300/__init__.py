@@ -93,6 +93,7 @@ class MoEError(RuntimeError):
 
 
 _lib = None
+_raw_stream = None
 
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(MoEShape)
@@ -162,10 +163,14 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    # the current stream's handle without a Stream object around it (which costs 3 us a call)
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(torch.cuda.current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # the current stream's handle without a Stream object around it (which costs 3 us a call)
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = (lambda: raw(dev())) if raw and dev and torch.cuda.is_initialized() else None
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
 
 
 def abi_version() -> int:
@@ -261,27 +266,35 @@ def new_kv_workspace(shape: KVShape, device="cuda", stream=None):
     return _workspace(kv_workspace_bytes(shape), device, stream)
 
 
+# The cache calls run once a layer or a step on a few microseconds of GPU work, so
+# their marshalling is kept short: tensors that are always there are not asked for None.
 def kv_plan(shape, ctx_len, n_new, parents, free_pages, block_table, row_start, slots, positions, mask, used, ws,
             stream=None) -> None:
-    _check(lib().moe_kv_plan(ctypes.byref(shape), _ptr(ctx_len), _ptr(n_new), _ptr(parents), _ptr(free_pages),
-                             0 if free_pages is None else free_pages.numel(), _ptr(block_table), _ptr(row_start),
-                             _ptr(slots), _ptr(positions), _ptr(mask), _ptr(used), _ptr(ws), ws.numel(),
-                             _stream(stream)), "moe_kv_plan")
+    rc = (_lib or lib()).moe_kv_plan(
+        ctypes.byref(shape), ctx_len.data_ptr(), n_new.data_ptr(), _ptr(parents), _ptr(free_pages),
+        0 if free_pages is None else free_pages.numel(), block_table.data_ptr(), row_start.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), _ptr(mask), used.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_kv_plan")
 
 
 def kv_append(shape, k_new, v_new, slots, k_scale, v_scale, k_cache, v_cache, ws, stream=None) -> None:
-    _check(lib().moe_kv_append(ctypes.byref(shape), _ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(k_scale),
-                               _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_kv_append")
+    rc = (_lib or lib()).moe_kv_append(
+        ctypes.byref(shape), k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+        k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_kv_append")
 
 
 def tree_attention(shape, q, k_cache, v_cache, block_table, ctx_len, row_start, mask, k_scale, v_scale, out, lse, ws,
                    stream=None) -> None:
     """Attention of the new tokens over the cache; lse may be None."""
-    _check(lib().moe_tree_attention(ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                    _ptr(ctx_len), _ptr(row_start), _ptr(mask), _ptr(k_scale), _ptr(v_scale),
-                                    _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_tree_attention")
+    rc = (_lib or lib()).moe_tree_attention(
+        ctypes.byref(shape), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        ctx_len.data_ptr(), row_start.data_ptr(), _ptr(mask), _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _ptr(lse),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_tree_attention")
 
 
 def device_status(ws, stream=None) -> tuple[int, int]:

@@ -3,6 +3,8 @@
 // combine) on the caller's stream.  Declarations and contracts: include/moe.h.
 #include "moe_internal.cuh"
 
+#include <atomic>
+
 #include <stdio.h>
 
 namespace moe {
@@ -89,13 +91,17 @@ static int check_ws(const moe_shape* s, void* ws, size_t ws_bytes) {
 int check_device() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return MOE_ERR_NO_DEVICE; }
+    static std::atomic<signed char> known[64];   // 0: not asked yet, 1: sm_103, -1: not
+    if (dev < 64 && known[dev]) return known[dev] > 0 ? MOE_OK : MOE_ERR_NO_DEVICE;
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_NO_DEVICE;
     }
-    return (major == 10 && minor == 3) ? MOE_OK : MOE_ERR_NO_DEVICE;
+    const bool ok = major == 10 && minor == 3;
+    if (dev < 64) known[dev] = ok ? 1 : -1;
+    return ok ? MOE_OK : MOE_ERR_NO_DEVICE;
 }
 
 int cuda_rc(cudaError_t e) {

@@ -35,6 +35,8 @@
 
 #include <math_constants.h>
 
+#include <atomic>
+
 namespace moe {
 namespace {
 
@@ -134,7 +136,8 @@ __device__ __forceinline__ int share_of(long long total, long long x) {
 // A wait that runs out, or finds that another one did, leaves its number in
 // m->abort, and the kernel's end reports it.
 constexpr int WAIT_TRIES = 1 << 22;
-constexpr int JOIN_TRIES = 1 << 24;         // polls of another CTA's counter, some seconds
+constexpr int LANDED_TRIES = 1 << 24;       // polls of a counter in shared memory, a second or so
+constexpr int JOIN_TRIES = 1 << 22;         // polls of another CTA's counter, two seconds
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, AMisc* m, int site) {
 #pragma unroll 1
     for (int i = 0; i < WAIT_TRIES; ++i) {
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, AMisc* m, i
 // Waits until tile number `tile` (from 0 on) of a ring has landed.
 __device__ __forceinline__ bool wait_landed(const uint32_t* landed, uint32_t tile, AMisc* m, int site) {
 #pragma unroll 1
-    for (int i = 0; i < JOIN_TRIES; ++i) {
+    for (int i = 0; i < LANDED_TRIES; ++i) {
         if ((int32_t)(ptx::ld_acquire_cta(landed) - tile) > 0) return true;
         if (*(volatile int*)&m->abort) return false;
         if (i > 8) __nanosleep(40);
@@ -1361,8 +1364,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             }
         }
         // ---- divided segments --------------------------------------------------
-        // The CTAs that hold parts of a segment are few and all run (one an SM);
-        // each has written all its parts before it waits here.
+        // The CTAs that hold parts of a segment are few and all run (the launch is
+        // cooperative); each has written all its parts before it waits here.
         __syncwarp();
         const Seg* const mine = m->join;
         if (ok && lane < 2 && mine[lane].parts) {
@@ -1444,6 +1447,25 @@ ATabs attn_tabs(const KvDims& d, char* ws, size_t* bytes) {
     return t;
 }
 
+// The CTAs of a launch wait for one another's parts, so it is cooperative: all of
+// them run at once or none does yet, whatever other streams have on the SMs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_together(void (*kern)(KArgs...), size_t smem, cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(A_CTAS);
+    cfg.blockDim = dim3(A_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 template <int D, bool E4M3>
 cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     using C = ACfg<D, E4M3>;
@@ -1470,10 +1492,16 @@ cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     if (num_sms() < A_CTAS) return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(k_tree_attn<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<bool> attribute_set[64];   // (a device's kernel attribute: set once)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !attribute_set[dev])) {
+        e = cudaFuncSetAttribute(k_tree_attn<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e == cudaSuccess && dev < 64) attribute_set[dev] = true;
+    }
     if (e != cudaSuccess) return e;
     timing_begin(K_TREE_ATTN, st);
-    e = launch_pdl(k_tree_attn<D, E4M3>, dim3(A_CTAS), dim3(A_THREADS), C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
+    e = launch_together(k_tree_attn<D, E4M3>, C::SMEM, st, tm_q, tm_q8, tm_q1, tm_k, tm_v, d, a, t);
     timing_end(st);
     return e;
 }

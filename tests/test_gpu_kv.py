@@ -307,6 +307,11 @@ class Batch:
     def run(self, stream=None, lse=True, ctx=None, row_start=None, table=None):
         self.args = (i32(self.table if table is None else table), i32(self.ctx if ctx is None else ctx),
                      i32(self.row_start if row_start is None else row_start))
+        self.again(stream, lse)
+
+    def again(self, stream=None, lse=True):
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
         moe.tree_attention(self.shape, self.q_rows, self.k, self.v, *self.args, self.mask, self.ks, self.vs, self.out,
                            self.lse if lse else None, self.ws, stream)
 
@@ -521,11 +526,25 @@ def test_refused_lengths_and_pages():
 def test_other_stream_and_no_lse():
     t = Batch([500, 70], [8, 3], 16, 4, 128, 32, tree=True, seed=10)
     s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
     t.run(stream=s, lse=False)
     s.synchronize()
     t.check(lse=False)
     assert (t.lse == 77.0).all()
+
+
+def test_two_streams_at_once():
+    """Launches of two streams (one of high priority) compete for the SMs; the CTAs of each wait for one another's parts."""
+    ts = [Batch([3000, 70, 900], [8, 3, 1], 16, 4, 128, 32, tree=True, seed=11),
+          Batch([7000], [2], 8, 2, 64, 16, tree=True, seed=12)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    for t, s in zip(ts, streams):
+        t.run(stream=s)
+    for _ in range(50):
+        for t, s in zip(ts, streams):
+            t.again(stream=s)
+    for t, s in zip(ts, streams):
+        s.synchronize()
+        t.check()
 
 
 def test_captured_calls_follow_the_lengths():
