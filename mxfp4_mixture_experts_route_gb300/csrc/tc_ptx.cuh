@@ -428,9 +428,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Instruction descriptor, fp32 accumulator, A K-major, B K-major or MN-major:
-// bf16 operands (kind::f16) or e4m3 operands (kind::f8f6f4).
-__host__ __device__ constexpr uint32_t idesc_attn(bool e4m3, int m, int n, bool b_mn) {
-    return (1u << 4) | (e4m3 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+// bf16 operands (kind::f16), or those with the type number 0: f16 there, e4m3
+// in kind::f8f6f4.
+__host__ __device__ constexpr uint32_t idesc_attn(bool type0, int m, int n, bool b_mn) {
+    return (1u << 4) | (type0 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
@@ -570,13 +571,25 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
     lo = q;
 }
 
+// two e4m3 codes -> packed f16, exactly
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// two fp32 -> packed bf16 (round to nearest even), lo in bits 15..0
+// two fp32 -> packed f16 or bf16 (round to nearest even), lo in bits 15..0
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

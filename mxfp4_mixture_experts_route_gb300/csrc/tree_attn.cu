@@ -55,10 +55,19 @@ struct ACfg {
     static constexpr int SLOT = KT * ROWB;                   // a K or V tile
     static constexpr int QT = 128 * D * 2;                   // a query tile: bf16, or e4m3 hi and lo
     static constexpr int QMISC = E4M3 ? 1024 : 0;            // e4m3: row scales of two query tiles
-    static constexpr int FIT = (232448 - A_MISC - QMISC - 2 * QT) / SLOT;
+    // V as the second product takes it: as it lies in the cache, or (V16) e4m3 codes made f16
+    static constexpr bool V16 = E4M3 && D == 64;
+    static constexpr bool P8 = E4M3 && !V16;                 // the weights as two e4m3 terms
+    static constexpr int VROWB = V16 ? 2 * D : ROWB;
+    static constexpr int VSW = VROWB < 128 ? VROWB : 128;
+    static constexpr int VSLOT = KT * VROWB;
+    static constexpr int VSTEP = P8 ? 32 : 16;               // K of one MMA with V
+    static constexpr int NF = V16 ? 3 : 0;             // slots of f16 V
+    static constexpr int FIT = (232448 - A_MISC - QMISC - 2 * QT - NF * VSLOT) / SLOT;
     static constexpr int NK = FIT / 2 < 8 ? FIT / 2 : 8;     // slots of the K ring
     static constexpr int NV = FIT - NK < 8 ? FIT - NK : 8;   // and of the V ring
-    static constexpr int SMEM = 2 * QT + (NK + NV) * SLOT + QMISC + A_MISC;
+    static constexpr int NVM = V16 ? NF : NV;                // slots of the ring that the MMAs read
+    static constexpr int SMEM = 2 * QT + (NK + NV) * SLOT + NF * VSLOT + QMISC + A_MISC;
     static constexpr int KSTEP = E4M3 ? 32 : 16;             // K of one MMA
     // TMEM columns: S (P in its place) and O of each stream
     static constexpr uint32_t T_S = 0, T_O = 256;
@@ -83,7 +92,7 @@ struct Units {
 struct AMisc {
     Seg seg[SEGS];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
-    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], f_empty[4], q_full[2], q_empty[2], s_full[2], p_full[2][2],
         o_full, o_free, ml_full, qs_full, wg[2], turn[2], drain[2];
     uint32_t tmem;
     int abort;
@@ -242,7 +251,8 @@ __host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
 template <int D, bool E4M3, int COLS, class HalfDone>
 __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_t t_lo, uint32_t t_o, float c, bool part,
                                              const uint32_t* vis, bool have_o, HalfDone half_done, float& mc, float& l) {
-    constexpr float LAZY = E4M3 ? 3.f : 8.f;
+    using C = ACfg<D, E4M3>;
+    constexpr float LAZY = C::P8 ? 3.f : 8.f;
     constexpr int N = COLS / 32;
     float s[N][32], tops[2 * N];
 #pragma unroll
@@ -300,7 +310,7 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
             s[k][x] = a;
             s[k][x + 1] = b;
         }
-        if (E4M3) {
+        if (C::P8) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 uint32_t h0, h1, l0, l1;
@@ -313,7 +323,8 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
             ptx::tmem_st8(t_lo + 8 * k, u + 8);
         } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) u[x] = ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
+            for (int x = 0; x < 16; ++x)
+                u[x] = C::V16 ? ptx::cvt_f16x2(s[k][2 * x], s[k][2 * x + 1]) : ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
             ptx::tmem_st16(t_p + 16 * k, u);
         }
         if (N == 4 && k == 1) half_done();
@@ -324,6 +335,32 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
     float a, b;
     ptx::unpack2(all, a, b);
     l += a + b;
+}
+
+// A tile of V's e4m3 codes as f16, which holds every one of them: rows of D bytes
+// become rows of 2 D, both swizzled (a row's 16-byte pieces, by its number) and in
+// blocks of 128 bytes a row.  A warp's reads are 512 bytes in a row; of its writes,
+// eight lanes' pieces lie in different banks.
+template <int D>
+__device__ __forceinline__ void v_to_f16(const uint8_t* v, uint8_t* f, int lane) {
+    constexpr int PIECES = D / 16;                            // 16-byte pieces a row of codes
+#pragma unroll 4
+    for (int i = lane; i < KT * PIECES; i += 32) {
+        const int r = i / PIECES, x = (i % PIECES) ^ (D == 128 ? r & 7 : r >> 1 & 3);   // row, its piece
+        const uint4 u = *reinterpret_cast<const uint4*>(v + i * 16);
+        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            h[2 * y] = ptx::f16x2_of_e4m3(in[y] & 0xFFFF);
+            h[2 * y + 1] = ptx::f16x2_of_e4m3(in[y] >> 16);
+        }
+        uint8_t* const row = f + (x / 4) * (KT * 128) + r * 128;
+        const int p0 = 2 * (x % 4) ^ (r & 7), first = x / 4;  // (the second block's pieces the other way round)
+        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4*>(row + 16 * (p0 ^ first)) = first ? b : a;
+        *reinterpret_cast<uint4*>(row + 16 * (p0 ^ first ^ 1)) = first ? a : b;
+    }
 }
 
 // The sum of a V column's infinities and NaN over the keys [k0, k1) that row i
@@ -501,8 +538,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* const k_ring = sm + 2 * C::QT;
     uint8_t* const v_ring = k_ring + C::NK * C::SLOT;
-    float* const q_scale = reinterpret_cast<float*>(v_ring + C::NV * C::SLOT);   // e4m3: [2][128]
-    AMisc* const m = reinterpret_cast<AMisc*>(v_ring + C::NV * C::SLOT + C::QMISC);
+    uint8_t* const f_ring = v_ring + C::NV * C::SLOT;
+    float* const q_scale = reinterpret_cast<float*>(f_ring + C::NF * C::VSLOT);   // e4m3: [2][128]
+    AMisc* const m = reinterpret_cast<AMisc*>(f_ring + C::NF * C::VSLOT + C::QMISC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pt = 2 * t.tpt;
     KT_MARK(K_TREE_ATTN, 0);
@@ -519,7 +557,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             uint32_t n = 1;
             if (i >= at(m->seg_empty) && i < at(m->k_full)) n = 15;                          // roles
             if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
-            if (i >= at(m->v_empty) && i < at(m->q_full)) n = 2;
+            if (i >= at(m->v_empty) && i < at(m->f_empty)) n = C::V16 ? 1 : 2;               // warp 2, or issuers
+            if (i >= at(m->f_empty) && i < at(m->q_full)) n = 2;
             if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
             if (i >= at(m->q_empty) && i < at(m->s_full)) n = 8;                             // softmax warps, or 4 an issuer
             if (i >= at(&m->p_full[0][0]) && i < at(&m->o_full)) n = 4;
@@ -841,12 +880,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // where rows are few).  Waits come before the one for P, which ends a
             // tile's critical path.
             constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
-            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);
+            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);   // (V16: f16 has e4m3's number)
             const int s = warp >> 1;
             uint32_t nq = 0, n_p0 = 0, n_p1 = 0, n_seg = 0;
             uint32_t base = 0;                                                 // the segment's first tile in the rings
             bool ok = true;
-            const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring), v0 = ptx::smem_u32(v_ring);
+            const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring);
+            const uint32_t v0 = ptx::smem_u32(C::V16 ? f_ring : v_ring);
+            uint64_t* const v_free = C::V16 ? m->f_empty : m->v_empty;
             const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
             auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
 #pragma unroll 1
@@ -863,14 +904,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
                 for (int j = first - step; j < mt && ok; j += step) {
                     const bool nx = j + step < mt;
-                    const uint32_t ks = same((base + j + step) % C::NK), vs = same((base + j) % C::NV);
+                    const uint32_t ks = same((base + j + step) % C::NK), vs = same((base + j) % C::NVM);
                     if (nx) ok = wait_landed(&m->landed[0], base + j + step, m, 6);
                     if (j >= 0) ok = ok && wait_landed(&m->landed[1], base + j, m, 7);
                     if (j >= 0 && !o_free && ok) {
                         ok = wait(&m->o_free, (n_seg - 1) & 1, m, 8);
                         o_free = true;
                     }
-                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::SLOT, KT * C::SW);
+                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::VSLOT, KT * C::VSW);
                     const uint32_t kd = ptx::smem_desc_lo(k0 + ks * C::SLOT, 16);
 #pragma unroll 1
                     for (uint32_t half = j < 0 ? 1 : 0; half < 2 && ok; ++half) {
@@ -886,20 +927,20 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         const uint32_t more_o = same(add);
                         if (ptx::elect_one()) {
                             if (j >= 0) {   // O += P V, 64 keys
-                                constexpr int E = KT / 2 / C::KSTEP;
-                                const uint32_t vh = vd + half * (KT / 2 * C::SW >> 4);
+                                constexpr int E = KT / 2 / C::VSTEP;
+                                const uint32_t vh = vd + half * (KT / 2 * C::VSW >> 4);
                                 const uint32_t pa = t_s + half * (8 * E);
 #pragma unroll
-                                for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
+                                for (int part = 0; part < (C::P8 ? 2 : 1); ++part) {
 #pragma unroll
                                     for (int e = 0; e < E; ++e)
-                                        ptx::mma_ts<E4M3>(t_o, pa + part * 32 + e * 8,
-                                                          ptx::smem_desc<C::SW>(vh + (e * C::KSTEP * C::SW >> 4)), id_o,
+                                        ptx::mma_ts<C::P8>(t_o, pa + part * 32 + e * 8,
+                                                          ptx::smem_desc<C::VSW>(vh + (e * C::VSTEP * C::VSW >> 4)), id_o,
                                                           (part | e) ? 1u : more_o);
                                 }
                                 if (half) {
-                                    ptx::mma_commit(&m->v_empty[vs]);
-                                    if (!two) ptx::mma_commit(&m->v_empty[vs]);
+                                    ptx::mma_commit(&v_free[vs]);
+                                    if (!two) ptx::mma_commit(&v_free[vs]);
                                 }
                             }
                             if (half && nx) {       // S = Q K^T
@@ -956,6 +997,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // Every V tile passes through this warp, which counts them.
             uint32_t tiles = 0;
             Ring<C::NV> vr;
+            Ring<C::V16 ? C::NF : 1> fr;
             bool ok = true;
 #pragma unroll 1
             for (int seg = 0; ok && in.next(m, w); ++seg) {
@@ -991,10 +1033,19 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                 bad |= hit;
                             }
                         }
-                        ptx::fence_proxy_async_shared();
+                        if (!C::V16) ptx::fence_proxy_async_shared();
                         bad = __any_sync(0xffffffffu, bad != 0);
                         if (bad && lane == 0) *(volatile int*)&m->nan_seg[seg % NAN_SLOTS] = seg + 1;
                         __syncwarp();
+                    }
+                    if (C::V16) {
+                        ok = wait(&m->f_empty[fr.slot], fr.phase ^ 1, m, 22);
+                        if (!ok) break;
+                        v_to_f16<D>(v_ring + vr.slot * C::SLOT, f_ring + fr.slot * C::VSLOT, lane);
+                        ptx::fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&m->v_empty[vr.slot]);
+                        fr.next();
                     }
                     if (lane == 0) ptx::st_release_cta(&m->landed[1], ++tiles);
                     __syncwarp();
@@ -1119,14 +1170,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (nc == 4) {
                     // this warp's quarter of the keys; the other quarters' weights are 0 in its rows
                     const uint32_t v = cp == 0 ? vis[0] : cp == 1 ? vis[1] : cp == 2 ? vis[2] : vis[3];
-                    constexpr int PC = E4M3 ? 8 : 16;                    // columns of 32 keys' weights
+                    constexpr int PC = C::P8 ? 8 : 16;                   // columns of 32 keys' weights
                     softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, &v, have_o,
                                               nothing, mc, l);
                     hand_over();
 #pragma unroll 1
                     for (int k = 1; k < 4; ++k) {
                         const uint32_t other = t_s + PC * ((cp + k) & 3);
-                        if (E4M3) {
+                        if (C::P8) {
                             ptx::tmem_st8_rep(other, 0);
                             ptx::tmem_st8_rep(other + 32, 0);
                         } else {
@@ -1134,14 +1185,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         }
                     }
                 } else if (nc == 2) {
-                    constexpr int PC = E4M3 ? 16 : 32;
+                    constexpr int PC = C::P8 ? 16 : 32;
                     const uint32_t v[2] = {cp ? vis[2] : vis[0], cp ? vis[3] : vis[1]};
                     softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, v, have_o,
                                               nothing, mc, l);
                     hand_over();
                     const uint32_t other = t_s + PC * (cp ^ 1);
                     ptx::tmem_st16_rep(other, 0);
-                    ptx::tmem_st16_rep(other + (E4M3 ? 32 : 16), 0);
+                    ptx::tmem_st16_rep(other + (C::P8 ? 32 : 16), 0);
                 } else {
                     last_half = 1;
                     auto half_done = [&] {
