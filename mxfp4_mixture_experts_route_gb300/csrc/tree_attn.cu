@@ -340,26 +340,37 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
 // A tile of V's e4m3 codes as f16, which holds every one of them: rows of D bytes
 // become rows of 2 D, both swizzled (a row's 16-byte pieces, by its number) and in
 // blocks of 128 bytes a row.  A warp's reads are 512 bytes in a row; of its writes,
-// eight lanes' pieces lie in different banks.
+// eight lanes' pieces lie in different banks (D = 128: the second block's pieces go
+// the other way round).  Loads of BATCH pieces are under way together.
 template <int D>
 __device__ __forceinline__ void v_to_f16(const uint8_t* v, uint8_t* f, int lane) {
-    constexpr int PIECES = D / 16;                            // 16-byte pieces a row of codes
-#pragma unroll 4
-    for (int i = lane; i < KT * PIECES; i += 32) {
-        const int r = i / PIECES, x = (i % PIECES) ^ (D == 128 ? r & 7 : r >> 1 & 3);   // row, its piece
-        const uint4 u = *reinterpret_cast<const uint4*>(v + i * 16);
-        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-        uint32_t h[8];
+    constexpr int PIECES = D / 16, STEP = 32 / PIECES;        // 16-byte pieces a row of codes, rows a warp's reads
+    constexpr int BATCH = 4;
+    const int r = lane / PIECES, p = lane % PIECES;           // row of the first read, where its piece lies
+    const uint8_t* from = v + lane * 16;
+#pragma unroll 1
+    for (int n = 0; n < KT / STEP; n += BATCH, from += BATCH * 512, f += BATCH * STEP * 128) {
+        uint4 u[BATCH];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            h[2 * y] = ptx::f16x2_of_e4m3(in[y] & 0xFFFF);
-            h[2 * y + 1] = ptx::f16x2_of_e4m3(in[y] >> 16);
+        for (int k = 0; k < BATCH; ++k) u[k] = *reinterpret_cast<const uint4*>(from + k * 512);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int rk = (r + k * STEP) & 7;                // the row's number in its swizzle
+            const int x = p ^ (D == 128 ? rk : rk >> 1);      // the piece
+            const int block = D == 128 ? x / 4 : 0;
+            const uint32_t in[4] = {block ? u[k].z : u[k].x, block ? u[k].w : u[k].y, block ? u[k].x : u[k].z,
+                                    block ? u[k].y : u[k].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                h[2 * y] = ptx::f16x2_of_e4m3(in[y] & 0xFFFF);
+                h[2 * y + 1] = ptx::f16x2_of_e4m3(in[y] >> 16);
+            }
+            uint8_t* const row = f + block * (KT * 128) + (r + k * STEP) * 128;
+            const int at = (2 * (x % 4) ^ rk) ^ block;
+            *reinterpret_cast<uint4*>(row + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + 16 * (at ^ 1)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        uint8_t* const row = f + (x / 4) * (KT * 128) + r * 128;
-        const int p0 = 2 * (x % 4) ^ (r & 7), first = x / 4;  // (the second block's pieces the other way round)
-        const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-        *reinterpret_cast<uint4*>(row + 16 * (p0 ^ first)) = first ? b : a;
-        *reinterpret_cast<uint4*>(row + 16 * (p0 ^ first ^ 1)) = first ? a : b;
     }
 }
 
