@@ -358,8 +358,10 @@ typedef struct moe_kv_shape {
 
 /*
  * Workspace size of the three calls in *bytes (pure host function).  Prepared
- * once with moe_workspace_init; errors found on the device are reported by
- * moe_device_status as for the block's calls.
+ * once with moe_workspace_init, and again after a MOE_ERR_TIMEOUT: counters in
+ * it are 0 between calls, and a call that gave up leaves them as they were.
+ * Calls that share a workspace must be ordered (one stream); errors found on
+ * the device are reported by moe_device_status as for the block's calls.
  */
 int moe_kv_workspace_bytes(const moe_kv_shape* shape, size_t* bytes);
 
@@ -415,8 +417,9 @@ int moe_kv_append(const moe_kv_shape* shape, const void* k_new, const void* v_ne
  * A row that sees nothing (a score of -inf counts as not seen) gets out 0 and
  * lse -inf; rows that no request owns are not written.  What a row does not
  * see does not reach it, whatever it holds (NaN included).  Sums and the softmax's maximum and
- * sum are fp32; the weights enter the second product as bf16 (e4m3 cache: as
- * two e4m3 terms, as q does, like bf16).
+ * sum are fp32; the weights enter the second product as bf16.  With an e4m3 cache q
+ * and the weights enter as two e4m3 terms each, which together hold what bf16
+ * does (D = 64: the weights as f16, which holds more).
  *   q [T, Hq, D] bf16 (rows q_stride apart); block_table [B, max_pages],
  *   ctx_len [B], row_start [B + 1], mask [T, W] (NULL when W is 0) as
  *   moe_kv_plan leaves them; k_scale, v_scale [Hkv] with MOE_KV_E4M3 (else
@@ -432,11 +435,11 @@ int moe_tree_attention(const moe_kv_shape* shape, const void* q, const void* k_c
 
 /*
  * Synchronises `stream`, returns the status latched in the workspace by the
- * device since the last call (MOE_OK, MOE_ERR_BAD_IDS, MOE_ERR_BAD_SCALE or
- * MOE_ERR_TIMEOUT; MOE_ERR_CUDA if the synchronisation itself failed) and
+ * device since the last call (MOE_OK, MOE_ERR_BAD_IDS, MOE_ERR_BAD_SCALE,
+ * MOE_ERR_TIMEOUT or what the cache calls name; MOE_ERR_CUDA if the synchronisation itself failed) and
  * clears it.  *detail (may be NULL) receives a code-specific value: the first
- * offending flat pick index, the first bad scale byte's value, or the site of
- * the wait that ran out.
+ * offending flat pick index, the first bad scale byte's value, the site of
+ * the wait that ran out, or what the cache calls name.
  */
 int moe_device_status(void* ws, int32_t* detail, void* stream);
 

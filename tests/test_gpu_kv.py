@@ -587,3 +587,54 @@ def test_captured_calls_follow_the_lengths():
         moe.check_device_status(ws, "calls")
         assert torch.equal(got, out) and (got[:sum(news)].float().abs().sum((1, 2)) > 0).all()
         assert (got[sum(news):] == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_verify_steps(e4m3):
+    """The example's steps: what is accepted stays, in order, and every layer's attention and block see it."""
+    from mxfp4_mixture_experts_route_gb300.verify_step import VerifyStep
+    s = VerifyStep(B=3, n=6, layers=2, page=8, most_ctx=200, e4m3=e4m3)
+    kept = [[[[], []] for _ in range(s.B)] for _ in range(s.layers)]      # layer, request: rows of K, of V
+    scale = s.shape.scale
+
+    def stored(x):
+        if not e4m3:
+            return x.double()
+        return (x.float() / s.k_scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).double() * s.k_scale[:, None].double()
+
+    for _ in range(9):
+        trees, paths = s.draft()
+        s.step(trees)
+        assert s.used.tolist()[0] == sum(map(len, trees))
+        starts = s.row_start.tolist()
+        for layer in range(s.layers):
+            new = [stored(x) for x in s.kv_new[layer]]
+            for b, (tree, path) in enumerate(zip(trees, paths)):
+                q = s.q[layer][starts[b]:starts[b] + len(tree)].double()
+                rows = [kept[layer][b][x] + list(new[x][starts[b]:starts[b] + len(tree)]) for x in (0, 1)]
+                k, v = (torch.stack(x).repeat_interleave(4, 1) for x in rows)
+                c = len(kept[layer][b][0])
+                assert c == s.lens[b]
+                see = torch.ones(len(tree), c + len(tree), dtype=torch.bool, device=DEV)
+                for i, p in enumerate(tree):
+                    see[i, c:] = False
+                    while True:
+                        see[i, c + i] = True
+                        if p < 0:
+                            break
+                        see[i, c + p] = True
+                        p = tree[p]
+                x = torch.where(see[:, None], torch.einsum("ihd,jhd->ihj", q, k) * scale, float("-inf"))
+                p = torch.softmax(x, 2)
+                want, mass = torch.einsum("ihj,jhd->ihd", p, v), torch.einsum("ihj,jhd->ihd", p, v.abs())
+                got = s.attn[layer][starts[b]:starts[b] + len(tree)].double()
+                # bf16 weights (relative 2^-9 a weight, and of their sum) and a bf16 result; scores' errors lie below
+                assert ((got - want).abs() <= 2.0 ** -7 * mass + 2.0 ** -8 * want.abs() + 1e-6).all()
+                for y in (0, 1):
+                    kept[layer][b][y] += [new[y][starts[b] + t] for t in path]
+            block = s.blocks[layer]
+            out = block.out.clone()
+            assert torch.equal(out, block.forward(s.attn[layer].view(s.T, -1))[2]) and out.isfinite().all()
+        s.accept(paths)
+        held = sorted(p for x in s.pages for p in x)
+        assert sorted(held + s.free_pages) == list(range(s.shape.n_pages))
