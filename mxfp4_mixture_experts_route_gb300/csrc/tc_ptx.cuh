@@ -117,16 +117,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
     }
 }
 
-// The same without a read of the clock while the first tries succeed (for
-// waits on a critical path, or that mostly find the phase complete).
-__device__ __forceinline__ bool mbar_wait_warp_fast(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                                    uint64_t limit_ns) {
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i)
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return mbar_wait_warp(bar, parity, abort, limit_ns);
-}
-
 // ---------------------------------------------------------------------------
 // TMA (tiled, 2-D) and L2 policies
 // ---------------------------------------------------------------------------

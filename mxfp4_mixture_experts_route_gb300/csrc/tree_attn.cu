@@ -17,19 +17,28 @@
 // it wait for one another's and add them in key order, each some of its columns.
 //
 // Two streams keep the tensor core and the exponentials busy side by side:
-// S, P and O exist twice in TMEM, each with a warpgroup of softmax threads
-// (a thread a row).  With two query tiles the streams are the tiles, and each
-// K/V tile serves both; with one, the streams take alternate key tiles and are
-// added at the segment's end.
+// S, P and O exist twice in TMEM (all of its 512 columns), each with a warpgroup of
+// softmax threads (a thread a row).  With two query tiles the streams are the tiles,
+// and each K/V tile serves both; with one, the streams take alternate key tiles and
+// are added at the segment's end.
 //
-// Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q, 1 and 3
-// MMA issuers (one a stream), 2 cleans V tiles that hold keys some row does not
-// see and counts them, 15 counts K tiles, 14 finds the CTA's segments and hands them to the others, 4-7 and 8-11
-// the softmax; 15 only keeps the register shares whole.
+// Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q (e4m3: makes
+// its terms where rows are few), 1 and 3 MMA issuers (one a stream), 2 cleans V tiles
+// that hold keys some row does not see, makes f16 of e4m3 ones (D = 64) and counts
+// them, 15 counts K tiles, 14 finds the CTA's segments and hands them to the others,
+// 4-7 and 8-11 the softmax.
 //
-// Instructions come from a small cache, and a call's first pass through any code
-// waits for it line by line: what runs once a segment is written as loops, and
-// waits and error paths are calls.
+// What bounds it.  With few rows the bytes of K and V: 128 requests of one token,
+// e4m3, contexts to 16384: 555 to 590 us, 0.77 to 0.82 of the measured copy bandwidth;
+// 16 requests of 8, bf16: 70.5 us, 0.73.  With full tiles a stream's chain: 1,960 cycles
+// of softmax, 910 for the products that follow it (12 MMAs of 128 x 128 x 16), 500 from
+// their ends to the next step's start; two such chains keep the tensor core at 53% and
+// the exponentials at 27% (prompts of up to 2000 tokens: 440 us, 0.62 of the measured
+// bf16 rate).  S and O leave no room in TMEM for a third chain; S in halves of 64 keys,
+// the first made early, was slower (508 us), since an MMA of N = 64 takes as long as
+// one of 128.  A call of few tiles is latency, 12.4 us: 2.5 before the first load, 1.5
+// a load, then each step of the chain once, at the speed at which code is first
+// fetched, which is why what runs once a segment is written as loops.
 #include "kv.cuh"
 #include "tc_ptx.cuh"
 
@@ -55,7 +64,12 @@ struct ACfg {
     static constexpr int SLOT = KT * ROWB;                   // a K or V tile
     static constexpr int QT = 128 * D * 2;                   // a query tile: bf16, or e4m3 hi and lo
     static constexpr int QMISC = E4M3 ? 1024 : 0;            // e4m3: row scales of two query tiles
-    // V as the second product takes it: as it lies in the cache, or (V16) e4m3 codes made f16
+    // V as the second product takes it: as it lies in the cache, or (V16) e4m3 codes made
+    // f16 by warp 2.  The weights are then one f16 term; as two e4m3 terms their conversions
+    // took the softmax as long as its exponentials (D = 64, 33 rows a tree: 113 us against
+    // 138; prompts of 2000: 448 against 571).  With D = 128 the f16 tiles leave 5 slots for
+    // K and V, and one warp does not keep up with the cache (128 requests of one token: 765 us
+    // against 555), so there the weights stay two terms.
     static constexpr bool V16 = E4M3 && D == 64;
     static constexpr bool P8 = E4M3 && !V16;                 // the weights as two e4m3 terms
     static constexpr int VROWB = V16 ? 2 * D : ROWB;
@@ -216,9 +230,14 @@ __device__ __forceinline__ int all_see(const KvDims& d, const Seg& s) { return d
 // are few: with 4 (or 2) copies, each warp of a warpgroup makes the weights of
 // a quarter (half) of the keys of its copy, instead of one warp those of all.
 // The others' weights in its copy are 0; the copies' O are added at the end.
+// That pays where a tile's K and V, 32 KB or less, come faster than one warp makes
+// its weights: 128 requests of one token, e4m3, D = 128: 555 us against 724 without,
+// D = 64: 417 against 526, and bf16 450 against 477.  Tiles of 64 KB do not (904 us and
+// 906), and the sum at the end costs a call of few tiles a microsecond (15.4 us and 14.5).
+template <int ROWB>
 __device__ __forceinline__ int copies(int ntok, const ATabs& t) {
     const int rows = ntok * t.G;
-    return ntok > t.tpt || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+    return ROWB > 128 || ntok > t.tpt || rows > 64 ? 1 : rows > 32 ? 2 : 4;
 }
 
 __device__ __forceinline__ int by_g(int r, const ATabs& t) { return (int)(r * t.g_inv >> 16); }
@@ -483,21 +502,32 @@ __device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, c
 
 // A query tile as e4m3 rows hi and lo (leading and next 4 significant bits) under
 // one power of two a row, in `nc` copies, into the swizzled K-major layout: 16 (8)
-// lanes a row, 8 elements a lane; warp wi of nw.
+// lanes a row, 8 elements a lane; warp wi of nw.  Four loads are under way ahead of
+// the row that is made (a rolled loop: code that runs once a segment is fetched anew).
 template <int D>
 __device__ __forceinline__ void q_terms(const KvDims& d, const AttnArgs& a, const ATabs& t, const Seg& w, int tile, int rows,
                                         int nc, int wi, int nw, uint8_t* hi, float* scale) {
     constexpr int SW = ACfg<D, true>::SW, QT = ACfg<D, true>::QT;
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, sub = lane % LPR, rs = 128 / nc;
+    constexpr int AHEAD = 4;
+    uint4 q[AHEAD];
+    auto load = [&](int r) {
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        const int tk = by_g(r, t);
+        return ld_dep(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                     (int64_t)(w.row0 + tile * t.tpt + tk) * d.q_stride +
+                                                     (int64_t)(w.h * t.G + r - tk * t.G) * D) + sub);
+    };
+    const int first = wi * RPW + lane / LPR, step = nw * RPW;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) q[i] = load(first + i * step);
 #pragma unroll 1
-    for (int r = wi * RPW + lane / LPR; r < (rows + RPW - 1) / RPW * RPW; r += nw * RPW) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-            x = ld_dep(reinterpret_cast<const uint4*>(
-                           reinterpret_cast<const uint16_t*>(a.q) +
-                           (int64_t)(w.row0 + tile * t.tpt + by_g(r, t)) * d.q_stride +
-                           (int64_t)(w.h * t.G + r - by_g(r, t) * t.G) * D) + sub);
+    for (int r = first; r < (rows + RPW - 1) / RPW * RPW; r += step) {
+        const uint4 x = q[0];
+#pragma unroll
+        for (int i = 1; i < AHEAD; ++i) q[i - 1] = q[i];
+        q[AHEAD - 1] = load(r + AHEAD * step);
         const uint32_t u[4] = {x.x, x.y, x.z, x.w};
         float f[8], top = 0.f;
 #pragma unroll
@@ -817,18 +847,18 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     ptx::mbar_wait_warp(&full[i % slots], (i / slots) & 1, &none, 10000000ull);
             }
         } else if (warp == 13 && E4M3) {
-            // ---- query tiles of few rows, and leave to make the others' terms -----
+            // ---- query tiles of few rows but the first, and leave to make the others' terms
             uint32_t nq = 0;
             bool ok = true;
 #pragma unroll 1
             while (ok && in.next(m, w)) {
-                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies(w.ntok, t);
+                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies<C::ROWB>(w.ntok, t);
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i, ++nq) {
                     const uint32_t qb = nq & 1;
                     ok = wait(&m->q_empty[qb], ((nq >> 1) & 1) ^ 1, m, 4);
                     if (!ok) break;
-                    if (nc > 1) {
+                    if (nc > 1 && nq > 0) {
                         q_terms<D>(d, a, t, w, 0, w.ntok * t.G, nc, 0, 1, sm + qb * C::QT, q_scale + qb * 128);
                         ptx::fence_proxy_async_shared();
                         __syncwarp();
@@ -844,7 +874,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             bool ok = true;
 #pragma unroll 1
             while (ok && in.next(m, w)) {
-                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies(w.ntok, t);
+                const int nt = w.ntok > t.tpt ? 2 : 1, nc = copies<C::ROWB>(w.ntok, t);
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i, ++nq) {
                     const uint32_t qb = nq & 1;
@@ -904,7 +934,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
             for (; ok && in.next(m, w); ++n_seg) {
                 const int mt = w.k1 - w.k0;
-                const bool two = w.ntok > t.tpt, narrow = copies(w.ntok, t) > 1;
+                const bool two = w.ntok > t.tpt, narrow = copies<C::ROWB>(w.ntok, t) > 1;
                 const int step = two ? 1 : 2, first = two ? 0 : s;             // own tiles: first, first + step, ...
                 const uint32_t nq_s = nq + (two ? s : 0), qb = same(nq_s & 1);
                 const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
@@ -1092,7 +1122,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         for (; ok && in.next(m, w); ++n_seg) {
             const int mt = w.k1 - w.k0, see = all_see(d, w);
             const bool two = w.ntok > t.tpt;
-            const int nc = copies(w.ntok, t), rs = 128 / nc;             // copies of the rows, lanes each has
+            const int nc = copies<C::ROWB>(w.ntok, t), rs = 128 / nc;             // copies of the rows, lanes each has
             const int cp = row / rs, rl = row % rs;                      // this thread's copy, and row in it
             const int qs = two ? g : 0;                                  // this stream's query tile
             const int ntok = w.ntok - qs * t.tpt < t.tpt ? w.ntok - qs * t.tpt : t.tpt;
@@ -1102,13 +1132,13 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             const uint32_t qb = (nq + qs) & 1;
             float c = d.scale * 1.4426950408889634f;
             if (E4M3) {
-                // wide tiles: these warps make the e4m3 terms, once the buffer is free;
-                // few rows: warp 13 does
+                // wide tiles, and a CTA's first: these warps make the e4m3 terms, once the
+                // buffer is free; else warp 13 does, ahead of them
                 c *= ld_dep(a.k_scale + w.h);
-                if (nc == 1) {
+                if (nc == 1 || n_seg == 0) {
                     ok = wait_landed(&m->landed[2], nq + qs, m, 14);
                     if (!ok) break;
-                    q_terms<D>(d, a, t, w, qs, rows, 1, two ? wq : warp - 4, two ? 4 : 8, sm + qb * C::QT,
+                    q_terms<D>(d, a, t, w, qs, rows, nc, two ? wq : warp - 4, two ? 4 : 8, sm + qb * C::QT,
                                q_scale + qb * 128);
                     ptx::fence_proxy_async_shared();
                     __syncwarp();
@@ -1545,13 +1575,13 @@ cudaError_t launch_attn(const KvDims& d, const AttnArgs& a, cudaStream_t st) {
     if (!E4M3) {
         const uint64_t qd[3] = {(uint64_t)D, (uint64_t)d.Hq, (uint64_t)d.T};
         const uint64_t qs[2] = {(uint64_t)D * 2, (uint64_t)d.q_stride * 2};
-        // boxes of a whole tile, of 8 tokens (where they fit 64 rows) and of one
+        // boxes of a whole tile; for copies, of 8 tokens (where they fit 64 rows) and of one
         auto q_map = [&](CUtensorMap* m, int tokens) {
             const uint32_t qb[3] = {64, (uint32_t)t.G, (uint32_t)tokens};
             return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
         };
-        if (!q_map(&tm_q, t.tpt) || !q_map(&tm_q8, 8 * t.G <= 64 ? 8 : 1) || !q_map(&tm_q1, 1))
-            return cudaErrorInvalidValue;
+        if (!q_map(&tm_q, t.tpt)) return cudaErrorInvalidValue;
+        if (C::ROWB <= 128 && (!q_map(&tm_q8, 8 * t.G <= 64 ? 8 : 1) || !q_map(&tm_q1, 1))) return cudaErrorInvalidValue;
     }
     if (num_sms() < A_CTAS) return cudaErrorNotSupported;
     static std::atomic<bool> attribute_set[64];   // (a device's kernel attribute: set once)
