@@ -40,8 +40,10 @@ __device__ __forceinline__ uint32_t quant4(uint32_t lo, uint32_t hi, const Scale
     return codes4(__fdiv_rn(a, k.s), __fdiv_rn(b, k.s), __fdiv_rn(c, k.s), __fdiv_rn(e, k.s));
 }
 
-// U pieces a thread at once, their loads under way together (16,411 rows of 8 heads x
-// 128 to e4m3: 26.3 us one at a time).
+// U pieces a thread at once, their loads under way together.  Measured: 16,411 rows of
+// 8 heads x 128 to e4m3 21.0 us with two, 21.9 with one, more with four or eight (0.70 of
+// the measured copy bandwidth; what is left is the codes' arithmetic, 73% of the issue
+// slots; 26.4 us when every code was a division); 8 rows to bf16 1.3 us with one, 1.7 with two.
 template <bool E4M3, int U>
 __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvDims d, const AppendArgs a) {
     constexpr int EL = E4M3 ? 16 : 8;                 // elements a piece

@@ -33,9 +33,9 @@
 // 16 requests of 8, bf16: 70.5 us, 0.73.  With full tiles a stream's chain: 1,960 cycles
 // of softmax, 910 for the products that follow it (12 MMAs of 128 x 128 x 16), 500 from
 // their ends to the next step's start; two such chains keep the tensor core at 53% and
-// the exponentials at 27% (prompts of up to 2000 tokens: 440 us, 0.62 of the measured
+// the exponentials at 27% (prompts of up to 2000 tokens: 432 us, 0.64 of the measured
 // bf16 rate).  S and O leave no room in TMEM for a third chain; S in halves of 64 keys,
-// the first made early, was slower (508 us), since an MMA of N = 64 takes as long as
+// the first made early, was slower (508 us against 442), since an MMA of N = 64 takes as long as
 // one of 128.  A call of few tiles is latency, 12.4 us: 2.5 before the first load, 1.5
 // a load, then each step of the chain once, at the speed at which code is first
 // fetched, which is why what runs once a segment is written as loops.
@@ -141,7 +141,8 @@ struct ATabs {
 // query tiles, 0.85 to 1.3 us for one, 4 to 5 us a segment.  With few key tiles a
 // share the line is the key tiles themselves, and a share holds one at least
 // (shares past the tiles none).
-constexpr int LINE_TILES = 8 * A_CTAS;      // (a share of 16 units or more holds a key tile)
+constexpr int LINE_TILES = 8 * A_CTAS;      // (a share of 16 units or more holds a key tile; by key
+                                            // tiles alone 78.7 us against 70.5, 144 against 113)
 // first unit of share c, and the share that holds unit x
 __device__ __forceinline__ long long share_begin(long long total, int c) {
     return total < A_CTAS ? (c < total ? c : total) : total * c / A_CTAS;
@@ -789,6 +790,9 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             while (ok && in.next(m, w)) {
                 const int total = w.c + w.n, mt = w.k1 - w.k0;
                 const int32_t* const table = a.block_table + (int64_t)w.b * d.max_pages;
+                // (K and V that later segments of the request read again are kept in L2;
+                // first out always: prompts 460 us against 432, last out always: 16
+                // requests of 8 rows 75.5 us against 70.7)
                 const uint64_t pol = w.flags & SEG_ONCE ? ptx::policy_evict_first() : ptx::policy_evict_last();
                 const int key_end = total < w.k1 * KT ? total : w.k1 * KT;
                 int pg = 0, off = 0, pg2 = 0, off2 = 0;
