@@ -419,7 +419,7 @@ int moe_kv_append(const moe_kv_shape* shape, const void* k_new, const void* v_ne
  * see does not reach it, whatever it holds (NaN included).  Sums and the softmax's maximum and
  * sum are fp32; the weights enter the second product as bf16.  With an e4m3 cache q
  * and the weights enter as two e4m3 terms each, which together hold what bf16
- * does (D = 64: the weights as f16, which holds more).
+ * does (the weights as one f16 where that is faster, which holds more).
  *   q [T, Hq, D] bf16 (rows q_stride apart); block_table [B, max_pages],
  *   ctx_len [B], row_start [B + 1], mask [T, W] (NULL when W is 0) as
  *   moe_kv_plan leaves them; k_scale, v_scale [Hkv] with MOE_KV_E4M3 (else

@@ -24,7 +24,7 @@
 //
 // Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q (e4m3: makes
 // its terms where rows are few), 1 and 3 MMA issuers (one a stream), 2 cleans V tiles
-// that hold keys some row does not see, makes f16 of e4m3 ones (D = 64) and counts
+// that hold keys some row does not see, makes f16 of e4m3 ones and counts
 // them, 15 counts K tiles, 14 finds the CTA's segments and hands them to the others,
 // 4-7 and 8-11 the softmax.
 //
@@ -56,6 +56,8 @@ constexpr int A_MISC = 3072;                // barriers and small tables
 constexpr int SEGS = 4;                     // segments handed out ahead
 constexpr int NAN_SLOTS = 16;
 
+constexpr int least(int a, int b) { return a < b ? a : b; }
+
 template <int D, bool E4M3>
 struct ACfg {
     static constexpr int ROWB = E4M3 ? D : 2 * D;            // bytes a key
@@ -64,24 +66,19 @@ struct ACfg {
     static constexpr int SLOT = KT * ROWB;                   // a K or V tile
     static constexpr int QT = 128 * D * 2;                   // a query tile: bf16, or e4m3 hi and lo
     static constexpr int QMISC = E4M3 ? 1024 : 0;            // e4m3: row scales of two query tiles
-    // V as the second product takes it: as it lies in the cache, or (V16) e4m3 codes made
-    // f16 by warp 2.  The weights are then one f16 term; as two e4m3 terms their conversions
-    // took the softmax as long as its exponentials (D = 64, 33 rows a tree: 113 us against
-    // 138; prompts of 2000: 448 against 571).  With D = 128 the f16 tiles leave 5 slots for
-    // K and V, and one warp does not keep up with the cache (128 requests of one token: 765 us
-    // against 555), so there the weights stay two terms.
-    static constexpr bool V16 = E4M3 && D == 64;
-    static constexpr bool P8 = E4M3 && !V16;                 // the weights as two e4m3 terms
-    static constexpr int VROWB = V16 ? 2 * D : ROWB;
-    static constexpr int VSW = VROWB < 128 ? VROWB : 128;
-    static constexpr int VSLOT = KT * VROWB;
-    static constexpr int VSTEP = P8 ? 32 : 16;               // K of one MMA with V
-    static constexpr int NF = V16 ? 3 : 0;             // slots of f16 V
-    static constexpr int FIT = (232448 - A_MISC - QMISC - 2 * QT - NF * VSLOT) / SLOT;
-    static constexpr int NK = FIT / 2 < 8 ? FIT / 2 : 8;     // slots of the K ring
-    static constexpr int NV = FIT - NK < 8 ? FIT - NK : 8;   // and of the V ring
-    static constexpr int NVM = V16 ? NF : NV;                // slots of the ring that the MMAs read
-    static constexpr int SMEM = 2 * QT + (NK + NV) * SLOT + NF * VSLOT + QMISC + A_MISC;
+    // V's slots.  e4m3 codes are made f16 for the second product by warp 2, and the weights
+    // are one f16 term; as two e4m3 terms their conversions took the softmax as long as its
+    // exponentials (33 rows a tree, D = 64: 113 us against 138; prompts of 2000, D = 128: 562
+    // against 687).  Only copies of few rows with D = 128 keep two terms: there K and V
+    // come faster than one warp converts (128 requests of one token: 765 us against 555).
+    // The codes land at RAW in a slot, the f16 rows stand from its begin on, in blocks of
+    // 128 bytes a row; with D = 128 the second block takes the codes' own place, row by row.
+    static constexpr int RAW = E4M3 ? KT * 128 : 0;
+    static constexpr int VSLOT = E4M3 ? KT * (D == 128 ? 256 : 192) : SLOT;
+    static constexpr int FIT = 232448 - A_MISC - QMISC - 2 * QT;
+    static constexpr int NV = least(8, E4M3 ? FIT / (SLOT + VSLOT) : FIT / SLOT - FIT / SLOT / 2);   // slots of V,
+    static constexpr int NK = least(8, E4M3 ? (FIT - NV * VSLOT) / SLOT : FIT / SLOT / 2);           // and of K
+    static constexpr int SMEM = 2 * QT + NK * SLOT + NV * VSLOT + QMISC + A_MISC;
     static constexpr int KSTEP = E4M3 ? 32 : 16;             // K of one MMA
     // TMEM columns: S (P in its place) and O of each stream
     static constexpr uint32_t T_S = 0, T_O = 256;
@@ -106,7 +103,7 @@ struct Units {
 struct AMisc {
     Seg seg[SEGS];
     uint64_t seg_full[SEGS], seg_empty[SEGS];
-    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], f_empty[4], q_full[2], q_empty[2], s_full[2], p_full[2][2],
+    uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2][2],
         o_full, o_free, ml_full, qs_full, wg[2], turn[2], drain[2];
     uint32_t tmem;
     int abort;
@@ -257,12 +254,13 @@ struct Ring {
 
 // The weights are relative to a maximum m (kept as mc = m c) that follows the
 // true one only when that is LAZY ahead, so that O is rescaled rarely; P stays
-// below 2^(base + LAZY).  An e4m3 P is held above that format's smallest steps
-// (2^-9): 2^5 at the maximum, at most 2^8 of 448.
+// below 2^(base + LAZY).  With an e4m3 cache P is held above its format's smallest
+// steps (e4m3 terms 2^-9, f16 2^-24): 2^5 at the maximum, at most 2^8 of 448 and
+// 2^13 of 65504.
 template <bool E4M3>
 __host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
 
-// One thread's row and COLS keys: the scores at t_s become weights at t_p (bf16,
+// One thread's row and COLS keys: the scores at t_s become weights at t_p (bf16, f16,
 // or the e4m3 terms hi at t_p and lo at t_lo), which may lie over them.  When
 // the maximum moves, the row of O at t_o is rescaled (no product into it is
 // under way).  half_done() is called once the first half of the weights has been
@@ -271,8 +269,8 @@ __host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
 template <int D, bool E4M3, int COLS, class HalfDone>
 __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_t t_lo, uint32_t t_o, float c, bool part,
                                              const uint32_t* vis, bool have_o, HalfDone half_done, float& mc, float& l) {
-    using C = ACfg<D, E4M3>;
-    constexpr float LAZY = C::P8 ? 3.f : 8.f;
+    constexpr bool P8 = E4M3 && D == 128 && COLS < 128;       // two e4m3 terms
+    constexpr float LAZY = P8 ? 3.f : 8.f;
     constexpr int N = COLS / 32;
     float s[N][32], tops[2 * N];
 #pragma unroll
@@ -330,7 +328,7 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
             s[k][x] = a;
             s[k][x + 1] = b;
         }
-        if (C::P8) {
+        if (P8) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 uint32_t h0, h1, l0, l1;
@@ -344,7 +342,7 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
         } else {
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-                u[x] = C::V16 ? ptx::cvt_f16x2(s[k][2 * x], s[k][2 * x + 1]) : ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
+                u[x] = E4M3 ? ptx::cvt_f16x2(s[k][2 * x], s[k][2 * x + 1]) : ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
             ptx::tmem_st16(t_p + 16 * k, u);
         }
         if (N == 4 && k == 1) half_done();
@@ -357,22 +355,23 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
     l += a + b;
 }
 
-// A tile of V's e4m3 codes as f16, which holds every one of them: rows of D bytes
-// become rows of 2 D, both swizzled (a row's 16-byte pieces, by its number) and in
-// blocks of 128 bytes a row.  A warp's reads are 512 bytes in a row; of its writes,
-// eight lanes' pieces lie in different banks (D = 128: the second block's pieces go
-// the other way round).  Loads of BATCH pieces are under way together.
+// A tile of V's e4m3 codes as f16, which holds every one of them: its rows of D
+// bytes become rows of 2 D, both swizzled (a row's 16-byte
+// pieces, by its number).  A warp's reads are 512 bytes in a row, four under way
+// together; of its writes, eight lanes' pieces lie in different banks (D = 128: the
+// second block's pieces go the other way round).
 template <int D>
-__device__ __forceinline__ void v_to_f16(const uint8_t* v, uint8_t* f, int lane) {
+__device__ __forceinline__ void v_to_f16(uint8_t* slot, int lane) {
     constexpr int PIECES = D / 16, STEP = 32 / PIECES;        // 16-byte pieces a row of codes, rows a warp's reads
     constexpr int BATCH = 4;
-    const int r = lane / PIECES, p = lane % PIECES;           // row of the first read, where its piece lies
-    const uint8_t* from = v + lane * 16;
+    const int p = lane % PIECES;                              // where the read's piece lies in its row
 #pragma unroll 1
-    for (int n = 0; n < KT / STEP; n += BATCH, from += BATCH * 512, f += BATCH * STEP * 128) {
+    for (int r = lane / PIECES; r < KT; r += BATCH * STEP) {
         uint4 u[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) u[k] = *reinterpret_cast<const uint4*>(from + k * 512);
+        for (int k = 0; k < BATCH; ++k)
+            u[k] = *reinterpret_cast<const uint4*>(slot + ACfg<D, true>::RAW + (r + k * STEP) * D + p * 16);
+        __syncwarp();                                         // (their places are written now)
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int rk = (r + k * STEP) & 7;                // the row's number in its swizzle
@@ -386,7 +385,7 @@ __device__ __forceinline__ void v_to_f16(const uint8_t* v, uint8_t* f, int lane)
                 h[2 * y] = ptx::f16x2_of_e4m3(in[y] & 0xFFFF);
                 h[2 * y + 1] = ptx::f16x2_of_e4m3(in[y] >> 16);
             }
-            uint8_t* const row = f + block * (KT * 128) + (r + k * STEP) * 128;
+            uint8_t* const row = slot + block * (KT * 128) + (r + k * STEP) * 128;
             const int at = (2 * (x % 4) ^ rk) ^ block;
             *reinterpret_cast<uint4*>(row + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4*>(row + 16 * (at ^ 1)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -580,9 +579,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* const k_ring = sm + 2 * C::QT;
     uint8_t* const v_ring = k_ring + C::NK * C::SLOT;
-    uint8_t* const f_ring = v_ring + C::NV * C::SLOT;
-    float* const q_scale = reinterpret_cast<float*>(f_ring + C::NF * C::VSLOT);   // e4m3: [2][128]
-    AMisc* const m = reinterpret_cast<AMisc*>(f_ring + C::NF * C::VSLOT + C::QMISC);
+    float* const q_scale = reinterpret_cast<float*>(v_ring + C::NV * C::VSLOT);   // e4m3: [2][128]
+    AMisc* const m = reinterpret_cast<AMisc*>(v_ring + C::NV * C::VSLOT + C::QMISC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pt = 2 * t.tpt;
     KT_MARK(K_TREE_ATTN, 0);
@@ -599,8 +597,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             uint32_t n = 1;
             if (i >= at(m->seg_empty) && i < at(m->k_full)) n = 15;                          // roles
             if (i >= at(m->k_empty) && i < at(m->v_full)) n = 2;                             // issuers
-            if (i >= at(m->v_empty) && i < at(m->f_empty)) n = C::V16 ? 1 : 2;               // warp 2, or issuers
-            if (i >= at(m->f_empty) && i < at(m->q_full)) n = 2;
+            if (i >= at(m->v_empty) && i < at(m->q_full)) n = 2;
             if (E4M3 && i >= at(m->q_full) && i < at(m->q_empty)) n = 8;                     // softmax warps
             if (i >= at(m->q_empty) && i < at(m->s_full)) n = 8;                             // softmax warps, or 4 an issuer
             if (i >= at(&m->p_full[0][0]) && i < at(&m->o_full)) n = 4;
@@ -782,7 +779,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             uint64_t* const full = is_v ? m->v_full : m->k_full;
             uint64_t* const empty = is_v ? m->v_empty : m->k_empty;
             const uint32_t slots = is_v ? C::NV : C::NK;
-            uint8_t* const ring = is_v ? v_ring : k_ring;
+            uint8_t* const ring = is_v ? v_ring + C::RAW : k_ring;
+            const uint32_t slot_bytes = is_v ? C::VSLOT : C::SLOT;
             uint32_t slot = 0, phase = 0, loads = 0;
             const int nb = KT / t.box;
             bool ok = true;
@@ -829,7 +827,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     __syncwarp();
                     const int i = lane - at;
                     if (i >= 0 && i < boxes) {
-                        uint8_t* const to = ring + slot * C::SLOT + i * t.box * C::SW;
+                        uint8_t* const to = ring + slot * slot_bytes + i * t.box * C::SW;
 #pragma unroll
                         for (int hf = 0; hf < C::HALVES; ++hf)
                             ptx::tma_load_4d(to + hf * (KT * C::SW), tm, hf * (C::SW / (E4M3 ? 1 : 2)), off, w.h, pg,
@@ -925,20 +923,18 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // where rows are few).  Waits come before the one for P, which ends a
             // tile's critical path.
             constexpr uint32_t id_s = ptx::idesc_attn(E4M3, 128, KT, false);
-            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);   // (V16: f16 has e4m3's number)
+            constexpr uint32_t id_o = ptx::idesc_attn(E4M3, 128, D, true);   // (f16 has e4m3's number)
             const int s = warp >> 1;
             uint32_t nq = 0, n_p0 = 0, n_p1 = 0, n_seg = 0;
             uint32_t base = 0;                                                 // the segment's first tile in the rings
             bool ok = true;
-            const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring);
-            const uint32_t v0 = ptx::smem_u32(C::V16 ? f_ring : v_ring);
-            uint64_t* const v_free = C::V16 ? m->f_empty : m->v_empty;
+            const uint32_t sm0 = ptx::smem_u32(sm), k0 = ptx::smem_u32(k_ring), v0 = ptx::smem_u32(v_ring);
             const uint32_t t_s = tmem + C::T_S + s * 128, t_o = tmem + C::T_O + s * 128;
             auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
 #pragma unroll 1
             for (; ok && in.next(m, w); ++n_seg) {
                 const int mt = w.k1 - w.k0;
-                const bool two = w.ntok > t.tpt, narrow = copies<C::ROWB>(w.ntok, t) > 1;
+                const bool two = w.ntok > t.tpt, narrow = copies<C::ROWB>(w.ntok, t) > 1, f16 = E4M3 && (D == 64 || !narrow);
                 const int step = two ? 1 : 2, first = two ? 0 : s;             // own tiles: first, first + step, ...
                 const uint32_t nq_s = nq + (two ? s : 0), qb = same(nq_s & 1);
                 const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
@@ -949,14 +945,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
                 for (int j = first - step; j < mt && ok; j += step) {
                     const bool nx = j + step < mt;
-                    const uint32_t ks = same((base + j + step) % C::NK), vs = same((base + j) % C::NVM);
+                    const uint32_t ks = same((base + j + step) % C::NK), vs = same((base + j) % C::NV);
                     if (nx) ok = wait_landed(&m->landed[0], base + j + step, m, 6);
                     if (j >= 0) ok = ok && wait_landed(&m->landed[1], base + j, m, 7);
                     if (j >= 0 && !o_free && ok) {
                         ok = wait(&m->o_free, (n_seg - 1) & 1, m, 8);
                         o_free = true;
                     }
-                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::VSLOT, KT * C::VSW);
+                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::VSLOT + (f16 ? 0 : C::RAW), f16 ? KT * 128 : KT * C::SW);
                     const uint32_t kd = ptx::smem_desc_lo(k0 + ks * C::SLOT, 16);
 #pragma unroll 1
                     for (uint32_t half = j < 0 ? 1 : 0; half < 2 && ok; ++half) {
@@ -972,20 +968,28 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         const uint32_t more_o = same(add);
                         if (ptx::elect_one()) {
                             if (j >= 0) {   // O += P V, 64 keys
-                                constexpr int E = KT / 2 / C::VSTEP;
-                                const uint32_t vh = vd + half * (KT / 2 * C::VSW >> 4);
-                                const uint32_t pa = t_s + half * (8 * E);
+                                if (f16) {
 #pragma unroll
-                                for (int part = 0; part < (C::P8 ? 2 : 1); ++part) {
+                                    for (int e = 0; e < 4; ++e)
+                                        ptx::mma_ts<false>(t_o, t_s + half * 32 + e * 8,
+                                                           ptx::smem_desc<128>(vd + (half * 64 + e * 16) * 128 / 16), id_o,
+                                                           e ? 1u : more_o);
+                                } else {
+                                    constexpr int E = KT / 2 / C::KSTEP;
+                                    const uint32_t vh = vd + half * (KT / 2 * C::SW >> 4);
+                                    const uint32_t pa = t_s + half * (8 * E);
 #pragma unroll
-                                    for (int e = 0; e < E; ++e)
-                                        ptx::mma_ts<C::P8>(t_o, pa + part * 32 + e * 8,
-                                                          ptx::smem_desc<C::VSW>(vh + (e * C::VSTEP * C::VSW >> 4)), id_o,
-                                                          (part | e) ? 1u : more_o);
+                                    for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
+#pragma unroll
+                                        for (int e = 0; e < E; ++e)
+                                            ptx::mma_ts<E4M3>(t_o, pa + part * 32 + e * 8,
+                                                              ptx::smem_desc<C::SW>(vh + (e * C::KSTEP * C::SW >> 4)), id_o,
+                                                              (part | e) ? 1u : more_o);
+                                    }
                                 }
                                 if (half) {
-                                    ptx::mma_commit(&v_free[vs]);
-                                    if (!two) ptx::mma_commit(&v_free[vs]);
+                                    ptx::mma_commit(&m->v_empty[vs]);
+                                    if (!two) ptx::mma_commit(&m->v_empty[vs]);
                                 }
                             }
                             if (half && nx) {       // S = Q K^T
@@ -1042,11 +1046,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             // Every V tile passes through this warp, which counts them.
             uint32_t tiles = 0;
             Ring<C::NV> vr;
-            Ring<C::V16 ? C::NF : 1> fr;
             bool ok = true;
 #pragma unroll 1
             for (int seg = 0; ok && in.next(m, w); ++seg) {
                 const int mt = w.k1 - w.k0, total = w.c + w.n, see = all_see(d, w);
+                const bool f16 = E4M3 && (D == 64 || copies<C::ROWB>(w.ntok, t) == 1);
 #pragma unroll 1
                 for (int j = 0; j < mt; ++j, vr.next()) {
                     const int key0 = (w.k0 + j) * KT;
@@ -1057,7 +1061,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         uint32_t bad = 0;
 #pragma unroll 1
                         for (int hf = 0; hf < C::HALVES; ++hf) {
-                            uint8_t* const v = v_ring + vr.slot * C::SLOT + hf * (KT * C::SW);
+                            uint8_t* const v = v_ring + vr.slot * C::VSLOT + C::RAW + hf * (KT * C::SW);
 #pragma unroll 1
                             for (int o = r1 * C::SW + lane * 16; o < KT * C::SW; o += 512)
                                 *reinterpret_cast<uint4*>(v + o) = make_uint4(0, 0, 0, 0);
@@ -1078,19 +1082,15 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                 bad |= hit;
                             }
                         }
-                        if (!C::V16) ptx::fence_proxy_async_shared();
+                        ptx::fence_proxy_async_shared();
                         bad = __any_sync(0xffffffffu, bad != 0);
                         if (bad && lane == 0) *(volatile int*)&m->nan_seg[seg % NAN_SLOTS] = seg + 1;
                         __syncwarp();
                     }
-                    if (C::V16) {
-                        ok = wait(&m->f_empty[fr.slot], fr.phase ^ 1, m, 22);
-                        if (!ok) break;
-                        v_to_f16<D>(v_ring + vr.slot * C::SLOT, f_ring + fr.slot * C::VSLOT, lane);
+                    if (f16) {
+                        v_to_f16<D>(v_ring + vr.slot * C::VSLOT, lane);
                         ptx::fence_proxy_async_shared();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&m->v_empty[vr.slot]);
-                        fr.next();
                     }
                     if (lane == 0) ptx::st_release_cta(&m->landed[1], ++tiles);
                     __syncwarp();
@@ -1212,17 +1212,18 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
                 };
+                constexpr bool P8 = E4M3 && D == 128;
                 if (nc == 4) {
                     // this warp's quarter of the keys; the other quarters' weights are 0 in its rows
                     const uint32_t v = cp == 0 ? vis[0] : cp == 1 ? vis[1] : cp == 2 ? vis[2] : vis[3];
-                    constexpr int PC = C::P8 ? 8 : 16;                   // columns of 32 keys' weights
+                    constexpr int PC = P8 ? 8 : 16;                  // columns of 32 keys' weights
                     softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, &v, have_o,
                                               nothing, mc, l);
                     hand_over();
 #pragma unroll 1
                     for (int k = 1; k < 4; ++k) {
                         const uint32_t other = t_s + PC * ((cp + k) & 3);
-                        if (C::P8) {
+                        if (P8) {
                             ptx::tmem_st8_rep(other, 0);
                             ptx::tmem_st8_rep(other + 32, 0);
                         } else {
@@ -1230,14 +1231,14 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         }
                     }
                 } else if (nc == 2) {
-                    constexpr int PC = C::P8 ? 16 : 32;
+                    constexpr int PC = P8 ? 16 : 32;
                     const uint32_t v[2] = {cp ? vis[2] : vis[0], cp ? vis[3] : vis[1]};
                     softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, v, have_o,
                                               nothing, mc, l);
                     hand_over();
                     const uint32_t other = t_s + PC * (cp ^ 1);
                     ptx::tmem_st16_rep(other, 0);
-                    ptx::tmem_st16_rep(other + (C::P8 ? 32 : 16), 0);
+                    ptx::tmem_st16_rep(other + (P8 ? 32 : 16), 0);
                 } else {
                     last_half = 1;
                     auto half_done = [&] {
