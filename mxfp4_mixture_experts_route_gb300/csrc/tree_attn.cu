@@ -93,10 +93,10 @@ struct Seg {
 constexpr int SEG_VALID = 1;    // (0: the share is done)
 constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read once
 
-// The line that shares are cut on: units a key tile with one and with two query
-// tiles, and a segment's own.
+// The line that shares are cut on: units a key tile with few rows (tokens up to few_tok,
+// which stand in copies), with one and with two query tiles, and a segment's own.
 struct Units {
-    int one, two, over;
+    int few_tok, few, one, two, over;
 };
 
 // shared-memory tables behind the tiles
@@ -133,9 +133,11 @@ struct ATabs {
 };
 
 // Shares are cut on a line on which a segment takes `over` units for its start and
-// end, then `two` (two query tiles) or `one` units a key tile; a share holds the
-// key tiles whose first unit lies in it.  Measured: 1.75 us a key tile for two
-// query tiles, 0.85 to 1.3 us for one, 4 to 5 us a segment.  With few key tiles a
+// end, then `two`, `one` or `few` units a key tile; a share holds the key tiles whose
+// first unit lies in it.  Measured: 2.1 us a key tile for two query tiles (bf16, D = 128),
+// 1.0 to 1.3 with copies, 4 to 5 us a segment; 2 : 3 : 4 and 10 against one weight for few
+// and one, 2 : 3 and 8: 101 us to 109 (trees of 33, whose last token is a tile of its
+// own), 69.6 to 70.5 (trees of 8).  With few key tiles a
 // share the line is the key tiles themselves, and a share holds one at least
 // (shares past the tiles none).
 constexpr int LINE_TILES = 8 * A_CTAS;      // (a share of 16 units or more holds a key tile; by key
@@ -189,10 +191,13 @@ __device__ __forceinline__ int pair_tiles(const KvDims& d, const KvReq& r, int p
     const int upto = d.W || (p + 1) * pt > r.n ? r.n : (p + 1) * pt;
     return (r.c + upto + KT - 1) / KT;
 }
-// whether pair p of a request has two query tiles
-__device__ __forceinline__ bool pair_two(const KvReq& r, int p, int pt) { return r.n - p * pt > pt / 2; }
+// units a key tile of pair p of a request
+__device__ __forceinline__ int tile_units(const KvReq& r, int p, int pt, Units u) {
+    const int n = r.n - p * pt;
+    return n > pt / 2 ? u.two : n > u.few_tok ? u.one : u.few;
+}
 __device__ __forceinline__ long long pair_units(const KvDims& d, const KvReq& r, int p, int pt, Units u) {
-    return u.over + (long long)(pair_two(r, p, pt) ? u.two : u.one) * pair_tiles(d, r, p, pt);
+    return u.over + (long long)tile_units(r, p, pt, u) * pair_tiles(d, r, p, pt);
 }
 // units of a request, a K/V head
 __device__ __forceinline__ long long head_units(const KvDims& d, const KvReq& r, int pt, Units u) {
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         long long sum = 0, upto = 0, total = 0;       // this thread's requests, those up to them, all
         KvReq r{0, 0, 0, true};
         long long* const part = reinterpret_cast<long long*>(m->ml);   // free until the first segment's end
-        Units u{1, 1, 0};
+        Units u{0, 1, 1, 1, 0};
         // first in key tiles; again in the line's units if there are enough of them
 #pragma unroll 1
         for (int round = 0;; ++round) {
@@ -655,7 +660,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
             total = __shfl_sync(0xffffffffu, w, 31);
             upto = (warp > 0 ? before : 0) + s;
             if (round == 1 || total < LINE_TILES) break;
-            u = Units{2, 3, 8};
+            u = Units{C::ROWB <= 128 ? 64 / t.G : 0, 2, 3, 4, 10};
         }
         long long base = upto - sum;
         const long long pos = share_begin(total, blockIdx.x);
@@ -713,7 +718,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
                 for (long long n; off >= (n = pair_units(d, r, p, pt, u)); ++p) off -= n;
                 at -= off;
-                per_tile = pair_two(r, p, pt) ? u.two : u.one;
+                per_tile = tile_units(r, p, pt, u);
                 kt = pair_tiles(d, r, p, pt);
                 if (off > u.over) k0 = (int)((uint32_t)(off - u.over + per_tile - 1) / (uint32_t)per_tile);
             }
@@ -765,7 +770,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                             np = (r.n + pt - 1) / pt;
                         }
                     }
-                    per_tile = pair_two(r, p, pt) ? u.two : u.one;
+                    per_tile = tile_units(r, p, pt, u);
                     kt = pair_tiles(d, r, p, pt);
                 }
             }
