@@ -393,6 +393,9 @@ def test_attention(ctx, new, Hq, Hkv, page, tree, layout, D, e4m3):
     ([3001] * 40, [1] * 40, 8, 2, 64),    # many single tokens
     ([9000, 100, 4000], [61, 5, 64], 32, 2, 128),   # large trees: two query tiles side by side
     (list(range(0, 2100, 7)), [1 + b % 5 for b in range(300)], 4, 2, 64),   # a request for every few tiles
+    ([55, 300, 0], [302, 151, 513], 32, 8, 128),    # short segments of many rows: cuts move to their ends
+    ([512], [512], 32, 8, 64),
+    ([9000, 8000, 8191, 7777, 1000], [33, 17, 40, 33, 9], 32, 4, 64),   # segments of two, one and a part of a tile
 ])
 def test_attention_long(ctx, new, Hq, Hkv, D, e4m3):
     t = Batch(ctx, new, Hq, Hkv, D, 16, e4m3, tree=max(new) > 1, seed=1)
