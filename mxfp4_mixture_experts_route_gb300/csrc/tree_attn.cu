@@ -523,41 +523,49 @@ __device__ __forceinline__ void join_items(const KvDims& d, const AttnArgs& a, c
 }
 
 // A query tile as e4m3 rows hi and lo (leading and next 4 significant bits) under
-// one power of two a row, in `nc` copies, into the swizzled K-major layout: 16 (8)
-// lanes a row, 8 elements a lane; warp wi of nw.  Four loads are under way ahead of
-// the row that is made (a rolled loop: code that runs once a segment is fetched anew).
+// one power of two a row, in `nc` copies, into the swizzled K-major layout: 8 (4)
+// lanes a row, 16 elements a lane; warp wi of nw.  Chains of dependent steps bound it, so
+// a lane has many elements, and two rows' loads are under way ahead of the row that is
+// made (a rolled loop: code that runs once a segment is fetched anew).
 template <int D>
 __device__ __forceinline__ void q_terms(const KvDims& d, const AttnArgs& a, const ATabs& t, const Seg& w, int tile, int rows,
                                         int nc, int wi, int nw, uint8_t* hi, float* scale) {
     constexpr int SW = ACfg<D, true>::SW, QT = ACfg<D, true>::QT;
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int LPR = D / 16, RPW = 32 / LPR, AHEAD = 2;
     const int lane = threadIdx.x & 31, sub = lane % LPR, rs = 128 / nc;
-    constexpr int AHEAD = 4;
-    uint4 q[AHEAD];
-    auto load = [&](int r) {
-        if (r >= rows) return make_uint4(0, 0, 0, 0);
+    uint4 q[AHEAD][2];
+    auto load = [&](int r, uint4* x) {
+        x[0] = x[1] = make_uint4(0, 0, 0, 0);
+        if (r >= rows) return;
         const int tk = by_g(r, t);
-        return ld_dep(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                     (int64_t)(w.row0 + tile * t.tpt + tk) * d.q_stride +
-                                                     (int64_t)(w.h * t.G + r - tk * t.G) * D) + sub);
+        const uint4* const from = reinterpret_cast<const uint4*>(
+            reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(w.row0 + tile * t.tpt + tk) * d.q_stride +
+            (w.h * t.G + r - tk * t.G) * D + sub * 16);
+        x[0] = ld_dep(from);
+        x[1] = ld_dep(from + 1);
     };
     const int first = wi * RPW + lane / LPR, step = nw * RPW;
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) q[i] = load(first + i * step);
+    for (int i = 0; i < AHEAD; ++i) load(first + i * step, q[i]);
 #pragma unroll 1
     for (int r = first; r < (rows + RPW - 1) / RPW * RPW; r += step) {
-        const uint4 x = q[0];
+        const uint32_t u[8] = {q[0][0].x, q[0][0].y, q[0][0].z, q[0][0].w, q[0][1].x, q[0][1].y, q[0][1].z, q[0][1].w};
 #pragma unroll
-        for (int i = 1; i < AHEAD; ++i) q[i - 1] = q[i];
-        q[AHEAD - 1] = load(r + AHEAD * step);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-        float f[8], top = 0.f;
+        for (int i = 1; i < AHEAD; ++i) {
+            q[i - 1][0] = q[i][0];
+            q[i - 1][1] = q[i][1];
+        }
+        load(r + AHEAD * step, q[AHEAD - 1]);
+        float f[16], tops[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             f[2 * i] = __uint_as_float(u[i] << 16);
             f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-            top = fmaxf(top, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            tops[i] = fmaxf(fmaxf(fabsf(f[4 * i]), fabsf(f[4 * i + 1])), fmaxf(fabsf(f[4 * i + 2]), fabsf(f[4 * i + 3])));
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
 #pragma unroll
         for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         // 2^(134 - e) brings the row's maximum (exponent field e) to [128, 256)
@@ -567,9 +575,9 @@ __device__ __forceinline__ void q_terms(const KvDims& d, const AttnArgs& a, cons
         e = e < 40 ? 40 : (e > 250 ? 250 : e);
         const float up = __uint_as_float((uint32_t)(261 - e) << 23);
         if (sub == 0) scale[r] = inf ? CUDART_NAN_F : __uint_as_float((uint32_t)(e - 7) << 23);
-        uint32_t vh[2], vl[2];
+        uint32_t vh[4], vl[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             float y[4], z[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[k] = f[4 * i + k] * up;
@@ -582,12 +590,12 @@ __device__ __forceinline__ void q_terms(const KvDims& d, const AttnArgs& a, cons
         }
         // row r of SW bytes, its 16-byte pieces exchanged by the swizzle
         // (copies are a multiple of 32 rows apart: the same exchange)
-        const uint32_t chunk = (uint32_t)(sub >> 1) ^ (SW == 128 ? (r & 7) : ((r >> 1) & 3));
+        const uint32_t chunk = (uint32_t)sub ^ (SW == 128 ? (r & 7) : ((r >> 1) & 3));
 #pragma unroll 1
         for (int k = 0; k < nc; ++k) {
-            uint8_t* const to = hi + (k * rs + r) * SW + chunk * 16 + (sub & 1) * 8;
-            *reinterpret_cast<uint2*>(to) = make_uint2(vh[0], vh[1]);
-            *reinterpret_cast<uint2*>(to + QT / 2) = make_uint2(vl[0], vl[1]);
+            uint8_t* const to = hi + (k * rs + r) * SW + chunk * 16;
+            *reinterpret_cast<uint4*>(to) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+            *reinterpret_cast<uint4*>(to + QT / 2) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
         }
     }
 }
