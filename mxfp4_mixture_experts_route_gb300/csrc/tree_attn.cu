@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 off -= h * per_head;
                 if (d.W && np > 1) {                      // all pairs but the last are alike
                     const uint32_t n = (uint32_t)pair_units(d, r, 0, pt, u);
-                    p = (int)((uint32_t)off / n);
+                    p = off >> 32 ? (int)(off / n) : (int)((uint32_t)off / n);
                     if (p > np - 1) p = np - 1;
                     off -= (long long)p * n;
                 }
