@@ -417,9 +417,11 @@ int moe_kv_append(const moe_kv_shape* shape, const void* k_new, const void* v_ne
  * A row that sees nothing (a score of -inf counts as not seen) gets out 0 and
  * lse -inf; rows that no request owns are not written.  What a row does not
  * see does not reach it, whatever it holds (NaN included).  Sums and the softmax's maximum and
- * sum are fp32; the weights enter the second product as bf16.  With an e4m3 cache q
- * and the weights enter as two e4m3 terms each, which together hold what bf16
- * does (the weights as one f16 where that is faster, which holds more).
+ * sum are fp32; the weights enter the second product as bf16.  With an e4m3 cache
+ * the weights enter as f16 (11 bits for weights down to 2^-21 of the row's largest,
+ * below that an error of at most 2^-32 of it), and q as two e4m3 terms under one power of
+ * two a row: exact for elements down to 2^-9 of the row's largest, below that
+ * with an error of at most 2^-17 of it.
  *   q [T, Hq, D] bf16 (rows q_stride apart); block_table [B, max_pages],
  *   ctx_len [B], row_start [B + 1], mask [T, W] (NULL when W is 0) as
  *   moe_kv_plan leaves them; k_scale, v_scale [Hkv] with MOE_KV_E4M3 (else

@@ -24,9 +24,9 @@
 //
 // Warps: 0 and 12 TMA producers (K and V, by page boxes), 13 loads Q (e4m3: makes
 // its terms where rows are few), 1 and 3 MMA issuers (one a stream), 2 cleans V tiles
-// that hold keys some row does not see, makes f16 of e4m3 ones and counts
-// them, 15 counts K tiles, 14 finds the CTA's segments and hands them to the others,
-// 4-7 and 8-11 the softmax.
+// that hold keys some row does not see, makes f16 of e4m3 ones (with few rows and D = 128
+// the softmax warps do) and counts them, 15 counts K tiles, 14 finds the CTA's segments
+// and hands them to the others, 4-7 and 8-11 the softmax.
 //
 // What bounds it.  With few rows the bytes of K and V: 128 requests of one token,
 // e4m3, contexts to 16384: 555 to 590 us, 0.77 to 0.82 of the measured copy bandwidth;
@@ -66,11 +66,12 @@ struct ACfg {
     static constexpr int SLOT = KT * ROWB;                   // a K or V tile
     static constexpr int QT = 128 * D * 2;                   // a query tile: bf16, or e4m3 hi and lo
     static constexpr int QMISC = E4M3 ? 1024 : 0;            // e4m3: row scales of two query tiles
-    // V's slots.  e4m3 codes are made f16 for the second product by warp 2, and the weights
-    // are one f16 term; as two e4m3 terms their conversions took the softmax as long as its
-    // exponentials (33 rows a tree, D = 64: 113 us against 138; prompts of 2000, D = 128: 562
-    // against 687).  Only copies of few rows with D = 128 keep two terms: there K and V
-    // come faster than one warp converts (128 requests of one token: 765 us against 555).
+    // V's slots.  e4m3 codes are made f16 for the second product, and the weights are one
+    // f16 term.  (e4m3 terms of the weights have no room for small ones beside a large one;
+    // with three e5m2 terms 16 requests of 8 rows take 61 us against 58, 128 of one token
+    // 617 against 622.)  Warp 2 makes them, but for copies of few rows with D = 128: there K
+    // and V come faster than one warp converts (128 requests of one token: 655 us), and the
+    // softmax warps make a quarter of a tile each, after their weights (before them: 638).
     // The codes land at RAW in a slot, the f16 rows stand from its begin on, in blocks of
     // 128 bytes a row; with D = 128 the second block takes the codes' own place, row by row.
     static constexpr int RAW = E4M3 ? KT * 128 : 0;
@@ -274,25 +275,28 @@ struct Ring {
     }
 };
 
+// Whether the softmax warps make V's codes f16 (else warp 2 does).
+template <int D, bool E4M3>
+__host__ __device__ constexpr bool softmax_converts(bool narrow) { return E4M3 && D == 128 && narrow; }
+
 // The weights are relative to a maximum m (kept as mc = m c) that follows the
 // true one only when that is LAZY ahead, so that O is rescaled rarely; P stays
-// below 2^(base + LAZY).  With an e4m3 cache P is held above its format's smallest
-// steps (e4m3 terms 2^-9, f16 2^-24): 2^5 at the maximum, at most 2^8 of 448 and
-// 2^13 of 65504.
+// below 2^(base + LAZY).  With an e4m3 cache P is f16, whose smallest step is 2^-24 and
+// largest value 65504.  One key may take nearly all of a row's weight while the output is
+// made of the others' (a sink), so the maximum stands high: 2^7, at most 2^15.  A weight has
+// f16's 11 bits down to 2^-21 of the largest, and below that an error of at most 2^-32 of it.
 template <bool E4M3>
-__host__ __device__ constexpr float p_base() { return E4M3 ? 5.f : 0.f; }
+__host__ __device__ constexpr float p_base() { return E4M3 ? 7.f : 0.f; }
 
-// One thread's row and COLS keys: the scores at t_s become weights at t_p (bf16, f16,
-// or the e4m3 terms hi at t_p and lo at t_lo), which may lie over them.  When
-// the maximum moves, the row of O at t_o is rescaled (no product into it is
-// under way).  half_done() is called once the first half of the weights has been
+// One thread's row and COLS keys: the scores at t_s become weights at t_p (bf16 or f16),
+// which may lie over them.  When the maximum moves, the row of O at t_o is rescaled
+// (no product into it is under way).  half_done() is called once the first half of the weights has been
 // stored.  Sums and maxima run in chains of 32 columns and of pairs, so that
 // no chain of dependent operations is longer than 16.
 template <int D, bool E4M3, int COLS, class HalfDone>
-__device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_t t_lo, uint32_t t_o, float c, bool part,
+__device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_t t_o, float c, bool part,
                                              const uint32_t* vis, bool have_o, HalfDone half_done, float& mc, float& l) {
-    constexpr bool P8 = E4M3 && D == 128 && COLS < 128;       // two e4m3 terms
-    constexpr float LAZY = P8 ? 3.f : 8.f;
+    constexpr float LAZY = 8.f;
     constexpr int N = COLS / 32;
     float s[N][32], tops[2 * N];
 #pragma unroll
@@ -350,23 +354,10 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
             s[k][x] = a;
             s[k][x + 1] = b;
         }
-        if (P8) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                uint32_t h0, h1, l0, l1;
-                ptx::split_e4m3x2(s[k][4 * x], s[k][4 * x + 1], h0, l0);
-                ptx::split_e4m3x2(s[k][4 * x + 2], s[k][4 * x + 3], h1, l1);
-                u[x] = h0 | h1 << 16;
-                u[8 + x] = l0 | l1 << 16;
-            }
-            ptx::tmem_st8(t_p + 8 * k, u);
-            ptx::tmem_st8(t_lo + 8 * k, u + 8);
-        } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-                u[x] = E4M3 ? ptx::cvt_f16x2(s[k][2 * x], s[k][2 * x + 1]) : ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
-            ptx::tmem_st16(t_p + 16 * k, u);
-        }
+        for (int x = 0; x < 16; ++x)
+            u[x] = E4M3 ? ptx::cvt_f16x2(s[k][2 * x], s[k][2 * x + 1]) : ptx::cvt_bf16x2(s[k][2 * x], s[k][2 * x + 1]);
+        ptx::tmem_st16(t_p + 16 * k, u);
         if (N == 4 && k == 1) half_done();
     }
     uint64_t all = sum[0];
@@ -377,41 +368,54 @@ __device__ __forceinline__ void softmax_cols(uint32_t t_s, uint32_t t_p, uint32_
     l += a + b;
 }
 
-// A tile of V's e4m3 codes as f16, which holds every one of them: its rows of D
-// bytes become rows of 2 D, both swizzled (a row's 16-byte
-// pieces, by its number).  A warp's reads are 512 bytes in a row, four under way
-// together; of its writes, eight lanes' pieces lie in different banks (D = 128: the
-// second block's pieces go the other way round).
-template <int D>
-__device__ __forceinline__ void v_to_f16(uint8_t* slot, int lane) {
+// ROWS rows of a tile of V's e4m3 codes, from row0 (a multiple of 8) on, as f16, which
+// holds every one of them: rows of D bytes become rows of 2 D, both swizzled (a row's
+// 16-byte pieces, by its number).  A lane takes one piece of every STEP-th row; where it goes to
+// is the same place in every second (D = 64: every) one of them, so the loop only adds to
+// addresses.  A warp's reads are 512 bytes in a row, eight under way together; of its writes,
+// eight lanes' pieces lie in different banks (D = 128: the second block's pieces go the
+// other way round).
+template <int D, int ROWS>
+__device__ __forceinline__ void v_to_f16(uint8_t* slot, int row0, int lane) {
     constexpr int PIECES = D / 16, STEP = 32 / PIECES;        // 16-byte pieces a row of codes, rows a warp's reads
-    constexpr int BATCH = 4;
-    const int p = lane % PIECES;                              // where the read's piece lies in its row
+    constexpr int BATCH = 8;
+    static_assert(ROWS % (BATCH * STEP) == 0, "whole batches");
+    const int p = lane % PIECES, r0 = lane / PIECES;          // where the piece lies in its row; the first row
+    const uint8_t* from = slot + ACfg<D, true>::RAW + row0 * D + lane * 16;
+    // D = 128: in rows r0 + 8 i the pieces p >= 4 belong to the second block, in rows r0 + 4 + 8 i the others
+    const bool second = D == 128 && p >= 4;
+    const int x = D == 128 ? (p ^ r0) & 3 : p ^ (r0 >> 1);    // the piece's number in its block
+    int to[2];                                                // bytes from the slot's begin
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int block = D == 128 ? second ^ q : 0;
+        to[q] = block * (KT * 128) + (row0 + r0) * 128 + 16 * ((2 * x ^ r0 ^ (D == 128 ? 4 * q : 0)) ^ block);
+    }
 #pragma unroll 1
-    for (int r = lane / PIECES; r < KT; r += BATCH * STEP) {
+    for (int i = 0; i < ROWS / STEP; i += BATCH) {
         uint4 u[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            u[k] = *reinterpret_cast<const uint4*>(slot + ACfg<D, true>::RAW + (r + k * STEP) * D + p * 16);
+        for (int k = 0; k < BATCH; ++k) u[k] = *reinterpret_cast<const uint4*>(from + k * 512);
         __syncwarp();                                         // (their places are written now)
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int rk = (r + k * STEP) & 7;                // the row's number in its swizzle
-            const int x = p ^ (D == 128 ? rk : rk >> 1);      // the piece
-            const int block = D == 128 ? x / 4 : 0;
-            const uint32_t in[4] = {block ? u[k].z : u[k].x, block ? u[k].w : u[k].y, block ? u[k].x : u[k].z,
-                                    block ? u[k].y : u[k].w};
+            const int q = D == 128 ? k & 1 : 0;
+            const bool turn = D == 128 && second != (q != 0); // the second block's: upper half first
+            const uint32_t in[4] = {turn ? u[k].z : u[k].x, turn ? u[k].w : u[k].y, turn ? u[k].x : u[k].z,
+                                    turn ? u[k].y : u[k].w};
             uint32_t h[8];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 h[2 * y] = ptx::f16x2_of_e4m3(in[y] & 0xFFFF);
                 h[2 * y + 1] = ptx::f16x2_of_e4m3(in[y] >> 16);
             }
-            uint8_t* const row = slot + block * (KT * 128) + (r + k * STEP) * 128;
-            const int at = (2 * (x % 4) ^ rk) ^ block;
-            *reinterpret_cast<uint4*>(row + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + 16 * (at ^ 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            uint8_t* const rows = slot + k * (STEP * 128);
+            *reinterpret_cast<uint4*>(rows + to[q]) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(rows + (to[q] ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
+        from += BATCH * 512;
+        to[0] += BATCH * STEP * 128;
+        to[1] += BATCH * STEP * 128;
     }
 }
 
@@ -968,7 +972,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
             for (; ok && in.next(m, w); ++n_seg) {
                 const int mt = w.k1 - w.k0;
-                const bool two = w.ntok > t.tpt, narrow = copies<C::ROWB>(w.ntok, t) > 1, f16 = E4M3 && (D == 64 || !narrow);
+                const bool two = w.ntok > t.tpt, narrow = copies<C::ROWB>(w.ntok, t) > 1;
                 const int step = two ? 1 : 2, first = two ? 0 : s;             // own tiles: first, first + step, ...
                 const uint32_t nq_s = nq + (two ? s : 0), qb = same(nq_s & 1);
                 const uint32_t qd = ptx::smem_desc_lo(sm0 + qb * C::QT, 16);
@@ -986,7 +990,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         ok = wait(&m->o_free, (n_seg - 1) & 1, m, 8);
                         o_free = true;
                     }
-                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::VSLOT + (f16 ? 0 : C::RAW), f16 ? KT * 128 : KT * C::SW);
+                    const uint32_t vd = ptx::smem_desc_lo(v0 + vs * C::VSLOT, KT * 128);
                     const uint32_t kd = ptx::smem_desc_lo(k0 + ks * C::SLOT, 16);
 #pragma unroll 1
                     for (uint32_t half = j < 0 ? 1 : 0; half < 2 && ok; ++half) {
@@ -1002,25 +1006,11 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         const uint32_t more_o = same(add);
                         if (ptx::elect_one()) {
                             if (j >= 0) {   // O += P V, 64 keys
-                                if (f16) {
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        ptx::mma_ts<false>(t_o, t_s + half * 32 + e * 8,
-                                                           ptx::smem_desc<128>(vd + (half * 64 + e * 16) * 128 / 16), id_o,
-                                                           e ? 1u : more_o);
-                                } else {
-                                    constexpr int E = KT / 2 / C::KSTEP;
-                                    const uint32_t vh = vd + half * (KT / 2 * C::SW >> 4);
-                                    const uint32_t pa = t_s + half * (8 * E);
-#pragma unroll
-                                    for (int part = 0; part < (E4M3 ? 2 : 1); ++part) {
-#pragma unroll
-                                        for (int e = 0; e < E; ++e)
-                                            ptx::mma_ts<E4M3>(t_o, pa + part * 32 + e * 8,
-                                                              ptx::smem_desc<C::SW>(vh + (e * C::KSTEP * C::SW >> 4)), id_o,
-                                                              (part | e) ? 1u : more_o);
-                                    }
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    ptx::mma_ts(t_o, t_s + half * 32 + e * 8,
+                                                ptx::smem_desc<128>(vd + (half * 64 + e * 16) * 128 / 16), id_o,
+                                                e ? 1u : more_o);
                                 if (half) {
                                     ptx::mma_commit(&m->v_empty[vs]);
                                     if (!two) ptx::mma_commit(&m->v_empty[vs]);
@@ -1084,7 +1074,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
 #pragma unroll 1
             for (int seg = 0; ok && in.next(m, w); ++seg) {
                 const int mt = w.k1 - w.k0, total = w.c + w.n, see = all_see(d, w);
-                const bool f16 = E4M3 && (D == 64 || copies<C::ROWB>(w.ntok, t) == 1);
+                const bool convert = E4M3 && !softmax_converts<D, E4M3>(copies<C::ROWB>(w.ntok, t) > 1);
 #pragma unroll 1
                 for (int j = 0; j < mt; ++j, vr.next()) {
                     const int key0 = (w.k0 + j) * KT;
@@ -1121,8 +1111,8 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         if (bad && lane == 0) *(volatile int*)&m->nan_seg[seg % NAN_SLOTS] = seg + 1;
                         __syncwarp();
                     }
-                    if (f16) {
-                        v_to_f16<D>(v_ring + vr.slot * C::VSLOT, lane);
+                    if (convert) {
+                        v_to_f16<D, KT>(v_ring + vr.slot * C::VSLOT, 0, lane);
                         ptx::fence_proxy_async_shared();
                         __syncwarp();
                     }
@@ -1155,6 +1145,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t t_s = tmem + lanes + C::T_S + g * 128, t_o = tmem + lanes + C::T_O + g * 128;
         uint32_t n_s = 0, nq = 0, n_seg = 0, n_ml = 0, n_wg = 0, n_qs = 0, n_turn = 0;
+        uint32_t base = 0;                                               // the segment's first tile in the rings
         bool ok = true;
 #pragma unroll 1
         for (; ok && in.next(m, w); ++n_seg) {
@@ -1246,33 +1237,20 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
                 };
-                constexpr bool P8 = E4M3 && D == 128;
                 if (nc == 4) {
                     // this warp's quarter of the keys; the other quarters' weights are 0 in its rows
                     const uint32_t v = cp == 0 ? vis[0] : cp == 1 ? vis[1] : cp == 2 ? vis[2] : vis[3];
-                    constexpr int PC = P8 ? 8 : 16;                  // columns of 32 keys' weights
-                    softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, &v, have_o,
-                                              nothing, mc, l);
+                    softmax_cols<D, E4M3, 32>(t_s + 32 * cp, t_s + 16 * cp, t_o, c, part, &v, have_o, nothing, mc, l);
                     hand_over();
 #pragma unroll 1
-                    for (int k = 1; k < 4; ++k) {
-                        const uint32_t other = t_s + PC * ((cp + k) & 3);
-                        if (P8) {
-                            ptx::tmem_st8_rep(other, 0);
-                            ptx::tmem_st8_rep(other + 32, 0);
-                        } else {
-                            ptx::tmem_st16_rep(other, 0);
-                        }
-                    }
+                    for (int k = 1; k < 4; ++k) ptx::tmem_st16_rep(t_s + 16 * ((cp + k) & 3), 0);
                 } else if (nc == 2) {
-                    constexpr int PC = P8 ? 16 : 32;
                     const uint32_t v[2] = {cp ? vis[2] : vis[0], cp ? vis[3] : vis[1]};
-                    softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + PC * cp, t_s + 32 + PC * cp, t_o, c, part, v, have_o,
-                                              nothing, mc, l);
+                    softmax_cols<D, E4M3, 64>(t_s + 64 * cp, t_s + 32 * cp, t_o, c, part, v, have_o, nothing, mc, l);
                     hand_over();
-                    const uint32_t other = t_s + PC * (cp ^ 1);
+                    const uint32_t other = t_s + 32 * (cp ^ 1);
                     ptx::tmem_st16_rep(other, 0);
-                    ptx::tmem_st16_rep(other + (P8 ? 32 : 16), 0);
+                    ptx::tmem_st16_rep(other + 16, 0);
                 } else {
                     last_half = 1;
                     auto half_done = [&] {
@@ -1280,9 +1258,19 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         if (lane == 0) ptx::mbar_arrive(&m->turn[g ^ 1]);
                     };
                     if (live)
-                        softmax_cols<D, E4M3, 128>(t_s, t_s, t_s + 32, t_o, c, part, vis, have_o, half_done, mc, l);
+                        softmax_cols<D, E4M3, 128>(t_s, t_s, t_o, c, part, vis, have_o, half_done, mc, l);
                     else
                         half_done();
+                }
+                if constexpr (softmax_converts<D, E4M3>(true)) {
+                    if (nc > 1) {
+                        // this warp's quarter of V's tile, handed over with the weights
+                        ok = wait_landed(&m->landed[1], base + j, m, 22);
+                        if (!ok) break;
+                        v_to_f16<D, KT / 4>(v_ring + (base + j) % C::NV * C::VSLOT, 32 * wq, lane);
+                        ptx::fence_proxy_async_shared();
+                        __syncwarp();
+                    }
                 }
                 stored(last_half);
             }
@@ -1294,6 +1282,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (lane == 0) ptx::mbar_arrive(&m->turn[0]);
             }
             nq += two ? 2 : 1;
+            base += mt;
             ok = wait(&m->o_full, n_seg & 1, m, 17);
             if (!ok) break;
             ptx::tc_fence_after();
