@@ -374,7 +374,10 @@ int moe_kv_workspace_bytes(const moe_kv_shape* shape, size_t* bytes);
  *   parents   [T]            int32, or NULL (chains; W must be 0): the row of
  *                            its request a drafted token follows, an earlier
  *                            one, or -1 (it follows token c_b - 1)
- *   free_pages [n_free]      int32 page ids (may be NULL when n_free is 0)
+ *   free_pages [n_free]      int32 page ids; a negative entry ends the list (may be
+ *                            NULL when n_free is 0).  n_free is fixed in a captured
+ *                            graph: the list itself then says how many there are,
+ *                            with -1 in the places behind the last
  *   block_table [B, max_pages]  int32, in and out: entries ceil(c_b / page) ..
  *                            ceil((c_b + n_b) / page) - 1 are written
  *   row_start [B + 1]        int32 out
@@ -390,7 +393,7 @@ int moe_kv_workspace_bytes(const moe_kv_shape* shape, size_t* bytes);
  * gets no rows; detail B: more than T rows, the last are cut off),
  * MOE_ERR_NO_PAGES (detail: pages missing; entries and slots are -1),
  * MOE_ERR_BAD_PARENT (detail: the row; its walk ends there), MOE_ERR_BAD_PAGE (detail:
- * the id; slots in that page are -1).
+ * the id; slots in that page are -1; also a negative entry of the list before a page id).
  */
 int moe_kv_plan(const moe_kv_shape* shape, const int32_t* ctx_len, const int32_t* n_new,
                 const int32_t* parents, const int32_t* free_pages, int32_t n_free,

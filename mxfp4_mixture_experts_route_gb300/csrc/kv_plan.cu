@@ -3,7 +3,8 @@
 // With c_b cached and n_b new tokens of request b and pages of P tokens:
 //   row_start_b = sum_{a<b} n_a
 //   old_b = ceil(c_b / P), new_b = ceil((c_b + n_b) / P)
-//   entry j in [old_b, new_b) of row b = free[sum_{a<b} (new_a - old_a) + j - old_b]
+//   entry j in [old_b, new_b) of row b = free[sum_{a<b} (new_a - old_a) + j - old_b],
+//   the list of free pages ending at its length or its first negative entry
 //   slot of row i = entry((c_b + i) / P) * P + (c_b + i) % P
 //   mask row i = {i} + its ancestors, position c_b + (ancestors of i)
 //
@@ -11,8 +12,8 @@
 // launch in which no CTA waits for another: every CTA scans all the lengths
 // itself (two counts packed into one 64-bit word, one block scan per 256
 // requests) and then writes its own share, taking a fresh page's id from the
-// free list rather than from the table entry another CTA writes.  Measured: 3.2 us
-// for 8 requests of 8 drafted tokens, 6.2 us for 512 of 64, 5.8 us for 64 prompts of
+// free list rather than from the table entry another CTA writes.  Measured: 3.3 us
+// for 8 requests of 8 drafted tokens, 6.5 us for 512 of 64, 5.9 us for 64 prompts of
 // up to 4096, of which the launch and the scan are 2.5 to 3.
 #include "kv.cuh"
 
@@ -58,6 +59,7 @@ __device__ __forceinline__ int page_of(const KvDims& d, const PlanArgs& a, const
         const int64_t f = (int64_t)taken + (j - r.old_pages);
         if (f >= a.n_free) return -1;
         id = ld_dep(a.free_pages + f);
+        if (id < 0) return -1;               // the list's end
     }
     if (id < 0 || id >= d.n_pages) {
         latch_status(a.sb, MOE_ERR_BAD_PAGE, id);
@@ -109,20 +111,28 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(const KvDims d, const 
     const int total = rows < (unsigned long long)d.T ? (int)rows : d.T;
     if (tid == 0) sh.row[d.B] = total;
     __syncthreads();
+    const int listed = pages < a.n_free ? pages : a.n_free;   // entries of the free list that are taken, if it has them
+    const bool reports = blockIdx.x == 0 && tid == PLAN_THREADS - 1;   // (of the warp with the fewest rows)
+    // (looked at when the rows are done)
+    const int last = reports && listed > 0 ? ld_dep(a.free_pages + listed - 1) : 0;
     if (blockIdx.x == 0) {
         for (int b = tid; b <= d.B; b += PLAN_THREADS) a.row_start[b] = sh.row[b];
-        if (tid == 0) {
+        if (reports) {
             a.used[0] = total;
-            a.used[1] = pages < a.n_free ? pages : a.n_free;
             if (rows > (unsigned long long)d.T) latch_status(a.sb, MOE_ERR_BAD_LENGTHS, d.B);
-            if (pages > a.n_free) latch_status(a.sb, MOE_ERR_NO_PAGES, pages - a.n_free);
         }
     }
     // fresh table entries, a request a CTA at a time
     for (int b = blockIdx.x; b < d.B; b += gridDim.x) {
         const PlanReq r = plan_request(d, a, b, false);
-        for (int j = r.old_pages + tid; j < r.new_pages; j += PLAN_THREADS)
-            a.block_table[(int64_t)b * d.max_pages + j] = page_of(d, a, r, b, sh.page[b], j);
+        for (int j = r.old_pages + tid; j < r.new_pages; j += PLAN_THREADS) {
+            const int id = page_of(d, a, r, b, sh.page[b], j);
+            a.block_table[(int64_t)b * d.max_pages + j] = id;
+            const int f = sh.page[b] + (j - r.old_pages);
+            // a negative entry with a page behind it: not the list's end
+            if (id < 0 && f + 1 < listed && ld_dep(a.free_pages + f) < 0 && ld_dep(a.free_pages + f + 1) >= 0)
+                latch_status(a.sb, MOE_ERR_BAD_PAGE, ld_dep(a.free_pages + f));
+        }
         if (TREE) {
             // the rows of this request: the walk up from each, parents in shared memory
             const int r0 = sh.row[b], n = sh.row[b + 1] - r0;
@@ -172,6 +182,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_kv_plan(const KvDims d, const 
         const int pg = page_of(d, a, r, lo, sh.page[lo], at / d.page);
         a.slots[t] = pg < 0 ? -1 : (int64_t)pg * d.page + at % d.page;
         a.positions[t] = at;
+    }
+    if (reports) {
+        int taken = listed;
+        if (last < 0) {   // the list ends before: entries below lo are pages, hi is none
+            int lo = 0, hi = listed - 1;
+            while (lo < hi) {
+                const int m = (lo + hi) >> 1;
+                if (ld_dep(a.free_pages + m) < 0) hi = m; else lo = m + 1;
+            }
+            taken = hi;
+        }
+        a.used[1] = taken;
+        if (pages > taken) latch_status(a.sb, MOE_ERR_NO_PAGES, pages - taken);
     }
     KT_MARK(K_KV_PLAN, 2);
 }

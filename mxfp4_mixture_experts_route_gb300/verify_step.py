@@ -83,7 +83,8 @@ class VerifyStep:
         self.ctx.copy_(torch.tensor(self.lens))
         self.new.copy_(torch.tensor(news))
         self.parents[:len(flat)] = torch.tensor(flat, dtype=torch.int32)
-        self.free[:len(self.free_pages)] = torch.tensor(self.free_pages, dtype=torch.int32)
+        # (-1 ends the list: the graph was captured with the length of the whole tensor)
+        self.free.copy_(torch.tensor(self.free_pages + [-1] * (len(self.free) - len(self.free_pages)), dtype=torch.int32))
         for x in (*self.q, *(t for kv in self.kv_new for t in kv)):
             x.normal_(generator=self.gen)
         if self.graph is None:
