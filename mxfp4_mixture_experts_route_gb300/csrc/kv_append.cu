@@ -112,9 +112,11 @@ cudaError_t launch_kv_append(const KvDims& d, const AppendArgs& a, cudaStream_t 
     const int64_t n = (int64_t)d.T * d.Hkv * d.D / (d.e4m3 ? 16 : 8);
     // one piece a thread while that is at most one round of the SMs' threads
     // (shortest path), two otherwise; every piece has its thread: no loop to run dry
+    // (but for the largest calls, whose pieces' numbers pass 31 bits)
     const int64_t one = (n + APPEND_THREADS - 1) / APPEND_THREADS;
     const bool few = one <= 8 * num_sms();
-    const dim3 grid((unsigned)(few ? one : (one + 1) / 2), 2), block(APPEND_THREADS);
+    const int64_t want = few ? one : (one + 1) / 2, most = ((int64_t)1 << 30) / APPEND_THREADS;
+    const dim3 grid((unsigned)(want < most ? want : most), 2), block(APPEND_THREADS);
     cudaError_t e;
     if (d.e4m3)
         e = few ? launch_pdl(k_kv_append<true, 1>, grid, block, 0, st, d, a)
