@@ -89,10 +89,11 @@ struct ACfg {
 struct Seg {
     int b, h, c, n;             // request, K/V head, its cached and new tokens
     int row0, tok0, ntok, kt;   // first row of the batch and token of the request, tokens, key tiles of the whole
-    int k0, k1, flags, parts;   // this part's key tiles; SEG_*; first CTA << 16 | CTAs that hold parts
+    int k0, k1, flags, parts;   // this part's key tiles; SEG_*, SEG_TILES; first CTA << 16 | CTAs that hold parts
 };
 constexpr int SEG_VALID = 1;    // (0: the share is done)
 constexpr int SEG_ONCE = 2;     // the request's only pair: its K and V are read once
+constexpr uint32_t SEG_TILES = 4;   // times the tiles of the share before the part's first
 
 // The line that shares are cut on: units a key tile with few rows (tokens up to few_tok,
 // which stand in copies), with one and with two query tiles, and a segment's own.
@@ -419,34 +420,64 @@ __device__ __forceinline__ void v_to_f16(uint8_t* slot, int row0, int lane) {
     }
 }
 
-// The sum of a V column's infinities and NaN over the keys [k0, k1) that row i
-// (row `row` of the batch) sees: what the products, which meet 0 * NaN there,
-// cannot give.  0 when there are none.
+// What infinities and NaN 16 bytes of V's columns hold over the keys [k0, k1) that
+// row i (row `row` of the batch) sees: what the products, which meet 0 * NaN there,
+// cannot give.  Two bits a column: 1 an infinity, 2 a negative one, 3 a NaN (or both
+// infinities, whose sum it is).  Page by page, four keys' loads under way together: a
+// long cache is looked through in milliseconds.
 struct VColumn {                // everything by value: the kernel's parameters stay in constant memory
-    const void* v;              // the K/V head's column in page 0
+    const void* v;              // the K/V head's columns in page 0
     const int32_t* pages;       // the request's row of the block table
     const uint32_t* mask;       // the row's mask words (chains: null)
     int64_t page_stride, token_stride;
     int page, n_pages, c, i;    // cached tokens, the row's number in its request
 };
 template <bool E4M3>
-__device__ __forceinline__ float v_specials(VColumn x, int k0, int k1) {
-    float sum = 0.f;
+__device__ __forceinline__ uint32_t v_specials(VColumn x, int k0, int k1) {
+    constexpr int EL = E4M3 ? 16 : 8, AT_ONCE = 4;
+    const int64_t token = x.token_stride * (E4M3 ? 1 : 2);
+    // all ones in the elements of a word that are not finite
+    auto odd = [](uint32_t v) {
+        return E4M3 ? __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu) : __vcmpeq2(v & 0x7F807F80u, 0x7F807F80u);
+    };
+    uint32_t found = 0;
 #pragma unroll 1
-    for (int key = k0; key < k1; ++key) {
-        const int j = key - x.c;
-        if (j >= 0 && !(x.mask ? (ld_dep(x.mask + (j >> 5)) >> (j & 31)) & 1 : j <= x.i)) continue;
-        const int pg = ld_dep(x.pages + key / x.page);
-        if (pg < 0 || pg >= x.n_pages) continue;
-        const int64_t at = pg * x.page_stride + (key % x.page) * x.token_stride;
-        float v;
-        if (E4M3)
-            v = (ld_dep(reinterpret_cast<const unsigned char*>(x.v) + at) & 0x7F) == 0x7F ? CUDART_NAN_F : 0.f;
-        else
-            v = __uint_as_float((uint32_t)ld_dep(reinterpret_cast<const unsigned short*>(x.v) + at) << 16);
-        if (!isfinite(v)) sum += v;
+    for (int key = k0; key < k1;) {
+        const int p = key / x.page, end = (p + 1) * x.page < k1 ? (p + 1) * x.page : k1;
+        const int pg = ld_dep(x.pages + p);
+        const uint8_t* at = reinterpret_cast<const uint8_t*>(x.v) + pg * x.page_stride * (E4M3 ? 1 : 2) +
+                            (key - p * x.page) * token;
+        if (pg < 0 || pg >= x.n_pages) key = end;
+#pragma unroll 1
+        for (; key < end; key += AT_ONCE, at += AT_ONCE * token) {
+            uint4 u[AT_ONCE];
+            uint32_t hit = 0;
+#pragma unroll
+            for (int y = 0; y < AT_ONCE; ++y)
+                u[y] = ld_dep(reinterpret_cast<const uint4*>(at + (key + y < end ? y : 0) * token));
+#pragma unroll
+            for (int y = 0; y < AT_ONCE; ++y) hit |= odd(u[y].x) | odd(u[y].y) | odd(u[y].z) | odd(u[y].w);
+            if (!hit) continue;
+#pragma unroll 1
+            for (int y = 0; y < AT_ONCE && key + y < end; ++y) {
+                const int j = key + y - x.c;
+                if (j >= 0 && !(x.mask ? (ld_dep(x.mask + (j >> 5)) >> (j & 31)) & 1 : j <= x.i)) continue;
+#pragma unroll 1
+                for (int e = 0; e < EL; ++e) {
+                    uint32_t bits;
+                    if (E4M3) {
+                        bits = (ld_dep(at + y * token + e) & 0x7F) == 0x7F ? 3 : 0;
+                    } else {
+                        const uint32_t v = ld_dep(reinterpret_cast<const unsigned short*>(at + y * token) + e);
+                        bits = (v & 0x7F80) != 0x7F80 ? 0 : v & 0x7F ? 3 : v >> 15 ? 2 : 1;
+                    }
+                    found |= bits << (2 * e);
+                }
+            }
+        }
+        key = end;
     }
-    return sum;
+    return found;
 }
 
 // Some of a divided segment's output, from its parts: the running maximum moves
@@ -752,7 +783,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (off > u.over) k0 = (int)((uint32_t)(off - u.over + per_tile - 1) / (uint32_t)per_tile);
             }
 #pragma unroll 1
-            for (uint32_t i = 0;;) {
+            for (uint32_t i = 0, tiles = 0;;) {
                 const long long left = end - at - u.over;   // units from the segment's first tile to the share's end
                 const bool more = begin < end && left > 0;
                 const int ntok = r.n - p * pt < pt ? r.n - p * pt : pt;
@@ -775,18 +806,19 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         s->kt = kt;
                         s->k0 = k0;
                         s->k1 = k1;
-                        s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0);
+                        s->flags = (more ? SEG_VALID : 0) | (np == 1 ? SEG_ONCE : 0) | (int)(tiles * SEG_TILES);
                         s->parts = 0;
                         if (more && (k0 > 0 || k1 < kt)) {   // divided: where its first and last tile are
-                            const long long tiles = at + u.over;
-                            const int c0 = share_of(total, tiles + cuts.low * per_tile);
+                            const long long first = at + u.over;
+                            const int c0 = share_of(total, first + cuts.low * per_tile);
                             s->parts =
-                                c0 << 16 | (share_of(total, tiles + (long long)(kt - 1 - cuts.high) * per_tile) - c0 + 1);
+                                c0 << 16 | (share_of(total, first + (long long)(kt - 1 - cuts.high) * per_tile) - c0 + 1);
                         }
                         ptx::mbar_arrive(&m->seg_full[i % SEGS]);
                     }
                     __syncwarp();
                     ++i;
+                    tiles += k1 - k0;
                     if (!more) break;
                 }
                 // (no tiles: the share begins or ends so that they are another's)
@@ -1145,7 +1177,6 @@ __global__ void __launch_bounds__(A_THREADS, 1)
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t t_s = tmem + lanes + C::T_S + g * 128, t_o = tmem + lanes + C::T_O + g * 128;
         uint32_t n_s = 0, nq = 0, n_seg = 0, n_ml = 0, n_wg = 0, n_qs = 0, n_turn = 0;
-        uint32_t base = 0;                                               // the segment's first tile in the rings
         bool ok = true;
 #pragma unroll 1
         for (; ok && in.next(m, w); ++n_seg) {
@@ -1265,9 +1296,10 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if constexpr (softmax_converts<D, E4M3>(true)) {
                     if (nc > 1) {
                         // this warp's quarter of V's tile, handed over with the weights
-                        ok = wait_landed(&m->landed[1], base + j, m, 22);
+                        const uint32_t tile = (uint32_t)w.flags / SEG_TILES + j;
+                        ok = wait_landed(&m->landed[1], tile, m, 22);
                         if (!ok) break;
-                        v_to_f16<D, KT / 4>(v_ring + (base + j) % C::NV * C::VSLOT, 32 * wq, lane);
+                        v_to_f16<D, KT / 4>(v_ring + tile % C::NV * C::VSLOT, 32 * wq, lane);
                         ptx::fence_proxy_async_shared();
                         __syncwarp();
                     }
@@ -1282,7 +1314,6 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                 if (lane == 0) ptx::mbar_arrive(&m->turn[0]);
             }
             nq += two ? 2 : 1;
-            base += mt;
             ok = wait(&m->o_full, n_seg & 1, m, 17);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -1321,32 +1352,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     a.lse[out_at(tk, r, 0) / D] =
                         sum == 0.f ? -CUDART_INF_F : (zero - p_base<E4M3>() + log2f(sum)) * 0.69314718055994531f;
             };
-            // Infinities and NaN of V that row r sees in columns [x, x + n), put over
-            // what is there: from the first cleaned key on, or (all) from the part's first.
-            auto specials = [&](int tk, int r, int x, int n, bool all) {
-                const int key0 = w.k0 * KT, total = w.c + w.n, key1 = total < w.k1 * KT ? total : w.k1 * KT;
-                VColumn col;
-                col.v = reinterpret_cast<const uint8_t*>(a.v_cache) + w.h * d.head_stride * (E4M3 ? 1 : 2);
-                col.pages = a.block_table + (int64_t)w.b * d.max_pages;
-                col.mask = d.W ? a.mask + (int64_t)(w.row0 + tk) * d.W : nullptr;
-                col.page_stride = d.page_stride;
-                col.token_stride = d.token_stride;
-                col.page = d.page;
-                col.n_pages = d.n_pages;
-                col.c = w.c;
-                col.i = w.tok0 + tk;
-#pragma unroll 1
-                for (int y = x; y < x + n; ++y) {
-                    VColumn one = col;
-                    one.v = reinterpret_cast<const uint8_t*>(col.v) + y * (E4M3 ? 1 : 2);
-                    const float e = v_specials<E4M3>(one, all || see < key0 ? key0 : see, key1);
-                    if (e == 0.f) continue;
-                    if (whole)
-                        reinterpret_cast<__nv_bfloat16*>(a.out)[out_at(tk, r, y)] = __float2bfloat16_rn(e);
-                    else
-                        part_at(r, y)[y % 4] = e;
-                }
-            };
+            uint32_t odd = 0;                                            // copies: pieces that are not finite
             if (nc == 1) {
                 // one query tile: both streams' O of a row, half its columns a warpgroup
                 float2 x0 = make_float2(mc, l), x1 = make_float2(-CUDART_INF_F, 0.f);
@@ -1387,7 +1393,6 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                         }
                     }
                     if (row < rows && (two || g == 0)) put_ml(tok, row, top, zero, sum);
-                    if (flagged && row < rows && !(sum != sum)) specials(tok, row, c0, c1 - c0, false);
                 }
             } else {
                 // few rows: the copies' and streams' O of a row are added through the
@@ -1443,7 +1448,7 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                     if (!ok) break;
                     const int next = passes == 1 ? rows : rs, sh = passes == 1 ? (D == 128 ? 4 : 3) : (D == 128 ? 3 : 2);
 #pragma unroll 1
-                    for (int i = row; i < rows << sh; i += 128) {
+                    for (int i = row, item = 1 << 4 * pass; i < rows << sh; i += 128, item <<= 1) {
                         const int r = i >> sh, k = i & (w4 - 1), x = x0 + 4 * k, tk = by_g(r, t);
                         float4 z = stage[piece(r, k)];
 #pragma unroll 1
@@ -1456,20 +1461,72 @@ __global__ void __launch_bounds__(A_THREADS, 1)
                                 make_uint2(ptx::cvt_bf16x2(z.x, z.y), ptx::cvt_bf16x2(z.z, z.w));
                         else
                             *reinterpret_cast<float4*>(part_at(r, x)) = z;
-                        // (a copy's weights of 0 make NaN of a seen infinity; a row whose own
-                        // scores are NaN has a NaN sum)
-                        const bool bad = !isfinite(z.x + z.y + z.z + z.w);
-                        if (bad || flagged) {
-                            float l_all = 0.f;
-                            for (int e = 0; e < nc; ++e) l_all += m->ml[0][e * rs + r].y + m->ml[1][e * rs + r].y;
-                            if (!(l_all != l_all)) specials(tk, r, x, 4, bad);
-                        }
+                        if (!E4M3 && !isfinite(z.x + z.y + z.z + z.w)) odd |= item;
                     }
                 }
                 if (!ok) break;
                 ptx::fence_proxy_async_shared();                         // Q's next tile comes by TMA
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&m->q_empty[qb]);
+            }
+            // Entries of V that were cleaned and are seen; and, with copies, whose weights of 0 make NaN of
+            // a seen infinity, all that are not finite.  (e4m3 has no infinity, and a NaN that every row
+            // sees is right as it is.)  This warp's pieces of four columns one after the other, the keys
+            // shared among the lanes.
+            if (flagged || (!E4M3 && C::ROWB <= 128 && __any_sync(0xffffffffu, odd != 0))) {
+                constexpr int EL = E4M3 ? 16 : 8;
+                const int key_0 = w.k0 * KT, key_1 = w.c + w.n < w.k1 * KT ? w.c + w.n : w.k1 * KT;
+                const int cleaned = see < key_0 ? key_0 : see;           // the first key that was cleaned
+                const int passes = nc * rows > 64 ? 2 : 1, sh = (D == 128 ? 5 : 4) - passes;
+                const int items = nc > 1 ? 8 : two ? D / 4 : D / 8;
+#pragma unroll 1
+                for (int item = 0; item < items; ++item) {
+                    int r = row, x = (two ? 0 : g * (D / 2)) + 4 * item;
+                    bool special = row < rows;
+                    if (nc > 1) {                                        // as the loop above goes
+                        const int i = row + 128 * (item & 3), pass = item >> 2;
+                        r = i >> sh;
+                        x = g * (D / 2) + pass * (D / 4) + 4 * (i & ((1 << sh) - 1));
+                        special = r < rows && pass < passes && (flagged || (odd >> item & 1));
+                    }
+                    if (special) {                                       // (scores that are NaN have a NaN sum)
+                        float sum = two ? l : 0.f;
+                        for (int e = 0; !two && e < nc; ++e) sum += m->ml[0][e * rs + r].y + m->ml[1][e * rs + r].y;
+                        special = !(sum != sum);
+                    }
+                    const int tk = nc > 1 ? by_g(r, t) : tok;
+#pragma unroll 1
+                    for (uint32_t left = __ballot_sync(0xffffffffu, special); left; left &= left - 1) {
+                        const int from = __ffs(left) - 1;
+                        const int sx = __shfl_sync(0xffffffffu, x, from), stk = __shfl_sync(0xffffffffu, tk, from);
+                        const int first = __shfl_sync(0xffffffffu, odd >> item & 1, from) ? key_0 : cleaned;
+                        const int each = (key_1 - first + 31) / 32, mine = first + lane * each;
+                        VColumn col;
+                        col.v = reinterpret_cast<const uint8_t*>(a.v_cache) +
+                                (w.h * d.head_stride + sx / EL * EL) * (E4M3 ? 1 : 2);
+                        col.pages = a.block_table + (int64_t)w.b * d.max_pages;
+                        col.mask = d.W ? a.mask + (int64_t)(w.row0 + stk) * d.W : nullptr;
+                        col.page_stride = d.page_stride;
+                        col.token_stride = d.token_stride;
+                        col.page = d.page;
+                        col.n_pages = d.n_pages;
+                        col.c = w.c;
+                        col.i = w.tok0 + stk;
+                        const uint32_t found = __reduce_or_sync(
+                            0xffffffffu, v_specials<E4M3>(col, mine, mine + each < key_1 ? mine + each : key_1));
+                        if (lane != from) continue;
+#pragma unroll 1
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t bits = found >> (2 * (x % EL + y)) & 3;
+                            if (bits == 0) continue;
+                            const float e = bits == 3 ? CUDART_NAN_F : bits == 2 ? -CUDART_INF_F : CUDART_INF_F;
+                            if (whole)
+                                reinterpret_cast<__nv_bfloat16*>(a.out)[out_at(tk, r, x + y)] = __float2bfloat16_rn(e);
+                            else
+                                part_at(r, x)[y] = e;
+                        }
+                    }
+                }
             }
             ptx::tc_fence_before();
             __syncwarp();
