@@ -89,7 +89,7 @@ extern "C" {
 #define MOE_ERR_TIMEOUT           -6  /* device: a bounded wait ran out */
 #define MOE_ERR_BAD_IDS           -7  /* device: an expert id outside [0, E) */
 #define MOE_ERR_BAD_SCALE         -8  /* device: an e8m0 scale byte of 255 (NaN) */
-#define MOE_ERR_NO_DEVICE         -9  /* current device is not sm_103 (GB300) */
+#define MOE_ERR_NO_DEVICE         -9  /* current device is not sm_103 (GB300), or has too few SMs (moe_tree_attention) */
 #define MOE_ERR_BAD_LENGTHS      -10  /* device: a request's length is negative or does not fit */
 #define MOE_ERR_NO_PAGES         -11  /* device: the list of free pages is too short */
 #define MOE_ERR_BAD_PARENT       -12  /* device: a drafted token's parent is not an earlier one */
@@ -429,6 +429,8 @@ int moe_kv_append(const moe_kv_shape* shape, const void* k_new, const void* v_ne
  *   ctx_len [B], row_start [B + 1], mask [T, W] (NULL when W is 0) as
  *   moe_kv_plan leaves them; k_scale, v_scale [Hkv] with MOE_KV_E4M3 (else
  *   NULL); out [T, Hq, D] bf16; lse [T, Hq] fp32 or NULL.
+ * The launch's CTAs wait for one another: it needs the 152 SMs of a GB300, and
+ * a device or context with fewer gets MOE_ERR_NO_DEVICE, with nothing enqueued.
  * Device errors: MOE_ERR_BAD_LENGTHS (detail: the request, which gets no
  * output), MOE_ERR_BAD_PAGE (detail: the id; that request's output is
  * unspecified), MOE_ERR_TIMEOUT.

@@ -134,7 +134,13 @@ int moe_tree_attention(const moe_kv_shape* shape, const void* q, const void* k_c
     if (!rc) rc = check_device();
     if (rc) return rc;
     const AttnArgs a{q, k_cache, v_cache, block_table, ctx_len, row_start, mask, k_scale, v_scale, out, lse, (char*)ws};
-    return cuda_rc(launch_tree_attn(d, a, (cudaStream_t)stream));
+    const cudaError_t e = launch_tree_attn(d, a, (cudaStream_t)stream);
+    // too few SMs for the launch, whose CTAs wait for one another: nothing was enqueued
+    if (e == cudaErrorNotSupported || e == cudaErrorCooperativeLaunchTooLarge) {
+        cudaGetLastError();
+        return MOE_ERR_NO_DEVICE;
+    }
+    return cuda_rc(e);
 }
 
 }  // extern "C"
