@@ -386,9 +386,6 @@ __device__ __forceinline__ uint32_t ld_acquire_cta(const uint32_t* p) {
     asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
     return v;
 }
-__device__ __forceinline__ void red_release_cta_add(uint32_t* p, uint32_t v) {   // shared memory
-    asm volatile("red.release.cta.shared::cta.add.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
-}
 __device__ __forceinline__ void st_release_cta(uint32_t* p, uint32_t v) {
     asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }

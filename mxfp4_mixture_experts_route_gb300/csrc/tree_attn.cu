@@ -117,7 +117,6 @@ struct AMisc {
     Units units;
     int first_c, first_n, first_r0;
     Seg join[2];                // the divided segments: one that began elsewhere, one that ends elsewhere
-    unsigned warp_sum[A_THREADS / 32];
     float2 ml[2][128];
 };
 static_assert(sizeof(AMisc) <= A_MISC, "misc");
