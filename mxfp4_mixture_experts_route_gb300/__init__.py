@@ -270,6 +270,7 @@ def new_kv_workspace(shape: KVShape, device="cuda", stream=None):
 # their marshalling is kept short: tensors that are always there are not asked for None.
 def kv_plan(shape, ctx_len, n_new, parents, free_pages, block_table, row_start, slots, positions, mask, used, ws,
             stream=None) -> None:
+    """Block tables, slots, positions and masks.  A negative entry ends free_pages, whose length a captured graph keeps."""
     rc = (_lib or lib()).moe_kv_plan(
         ctypes.byref(shape), ctx_len.data_ptr(), n_new.data_ptr(), _ptr(parents), _ptr(free_pages),
         0 if free_pages is None else free_pages.numel(), block_table.data_ptr(), row_start.data_ptr(), slots.data_ptr(),

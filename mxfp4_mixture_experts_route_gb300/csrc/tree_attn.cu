@@ -28,15 +28,17 @@
 // the softmax warps do) and counts them, 15 counts K tiles, 14 finds the CTA's segments
 // and hands them to the others, 4-7 and 8-11 the softmax.
 //
-// What bounds it.  With few rows the bytes of K and V: 128 requests of one token,
-// e4m3, contexts to 16384: 555 to 590 us, 0.77 to 0.82 of the measured copy bandwidth;
-// 16 requests of 8, bf16: 70.5 us, 0.73.  With full tiles a stream's chain: 1,960 cycles
+// What bounds it.  With few rows the bytes of K and V: 16 requests of 8, bf16: 70 us
+// (73 launched from the host), 0.73 of the measured copy bandwidth.  With an e4m3 cache
+// and D = 128 a stream's chain comes close to them, and V's codes are a part of it: 128
+// requests of one token, contexts to 16384: 625 to 655 us, 0.69 to 0.73, the tensor core
+// 57% busy.  With full tiles the chain alone: 1,960 cycles
 // of softmax, 910 for the products that follow it (12 MMAs of 128 x 128 x 16), 500 from
-// their ends to the next step's start; two such chains keep the tensor core at 53% and
-// the exponentials at 27% (prompts of up to 2000 tokens: 432 us, 0.64 of the measured
-// bf16 rate).  S and O leave no room in TMEM for a third chain; S in halves of 64 keys,
+// their ends to the next step's start; two such chains keep the tensor core at 54% and
+// the exponentials at 27% (prompts of up to 2000 tokens: 435 to 450 us, 0.61 to 0.63 of the
+// measured bf16 rate).  S and O leave no room in TMEM for a third chain; S in halves of 64 keys,
 // the first made early, was slower (508 us against 442), since an MMA of N = 64 takes as long as
-// one of 128.  A call of few tiles is latency, 12.4 us: 2.5 before the first load, 1.5
+// one of 128.  A call of few tiles is latency, 12.5 us: 2.5 before the first load, 1.5
 // a load, then each step of the chain once, at the speed at which code is first
 // fetched, which is why what runs once a segment is written as loops.
 #include "kv.cuh"
@@ -69,7 +71,7 @@ struct ACfg {
     // V's slots.  e4m3 codes are made f16 for the second product, and the weights are one
     // f16 term.  (e4m3 terms of the weights have no room for small ones beside a large one;
     // with three e5m2 terms 16 requests of 8 rows take 61 us against 58, 128 of one token
-    // 617 against 622.)  Warp 2 makes them, but for copies of few rows with D = 128: there K
+    // 612 to 622 against 622 to 630.)  Warp 2 makes them, but for copies of few rows with D = 128: there K
     // and V come faster than one warp converts (128 requests of one token: 655 us), and the
     // softmax warps make a quarter of a tile each, after their weights (before them: 638).
     // The codes land at RAW in a slot, the f16 rows stand from its begin on, in blocks of
@@ -252,9 +254,11 @@ __device__ __forceinline__ int all_see(const KvDims& d, const Seg& s) { return d
 // a quarter (half) of the keys of its copy, instead of one warp those of all.
 // The others' weights in its copy are 0; the copies' O are added at the end.
 // That pays where a tile's K and V, 32 KB or less, come faster than one warp makes
-// its weights: 128 requests of one token, e4m3, D = 128: 555 us against 724 without,
-// D = 64: 417 against 526, and bf16 450 against 477.  Tiles of 64 KB do not (904 us and
-// 906), and the sum at the end costs a call of few tiles a microsecond (15.4 us and 14.5).
+// its weights: 128 requests of one token, D = 64: e4m3 412 us against 525 without, bf16 443
+// against 476.  Tiles of 64 KB do not (904 us and 906), and the sum at the end costs a
+// call of few tiles a microsecond (15.4 us and 14.5).  With e4m3 and D = 128 V's codes weigh
+// more: 628 us against 643, 64 requests of 32 heads a group 295 against 313; 48 heads, in two
+// copies, 334 against 319, and 16 requests of 8 rows 58.5 to 60 against 56.5.
 template <int ROWB>
 __device__ __forceinline__ int copies(int ntok, const ATabs& t) {
     const int rows = ntok * t.G;
