@@ -476,6 +476,7 @@ __device__ __forceinline__ uint32_t v_specials(VColumn x, int k0, int k1) {
                     }
                     found |= bits << (2 * e);
                 }
+                if (found == (E4M3 ? 0xFFFFFFFFu : 0xFFFFu)) return found;   // (NaN in all of them: no more to learn)
             }
         }
         key = end;
