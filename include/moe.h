@@ -441,6 +441,113 @@ int moe_tree_attention(const moe_kv_shape* shape, const void* q, const void* k_c
                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * What stands between a fused query, key and value projection and the cache, in
+ * one pass: an RMSNorm of each query and key head, the rotation by position,
+ * and the append of K and V.  With x one head's row of D elements:
+ *   y    = x * rsqrt(mean(x^2) + eps) * w          (w NULL: y = x)
+ *   z_i  = y_i cos_i - y_j sin_i,  z_j = y_j cos_i + y_i sin_i
+ * for the pairs (i, j) of the first R elements, i = 0 .. R/2 - 1: (i, i + R/2), or with
+ * MOE_ROPE_INTERLEAVED elements 2i and 2i + 1; elements from R on are left as
+ * they are.  cos_i and sin_i are entries i and R/2 + i of the table's row
+ * positions[t].  Everything is fp32 and rounded once: q to bf16, K and V to the
+ * cache's type as moe_kv_append does (V is neither normalised nor rotated).
+ */
+#define MOE_ROPE_INTERLEAVED 1u /* moe_rope.flags */
+
+/*
+ * Supported: R a multiple of 16, 0 (no rotation) to D; max_pos >= 1 when R > 0; eps
+ * finite and >= 0; q_in_stride as q_stride of moe_kv_shape (0: packed).
+ */
+typedef struct moe_rope {
+    int32_t R;             /* elements of a head that are rotated */
+    int32_t max_pos;       /* rows of the table */
+    uint32_t flags;        /* MOE_ROPE_INTERLEAVED */
+    float eps;
+    int64_t q_in_stride;   /* elements from one row of q_in to the next */
+} moe_rope;
+
+/*
+ *   q_in [T, Hq, D] bf16 (rows q_in_stride apart); k_new, v_new [T, Hkv, D]
+ *   bf16 (rows kv_stride apart): the three parts of a projection's rows, for
+ *   instance.  positions [T] int32 and slots [T] int64 as moe_kv_plan leaves them.
+ *   q_norm, k_norm [D] fp32, each may be NULL; cos_sin [max_pos, R] fp32
+ *   (NULL when R is 0); k_scale, v_scale as for moe_kv_append.
+ *   q [T, Hq, D] bf16 out (rows q_stride apart): q_in itself (then the
+ *   strides have to be equal, else MOE_ERR_INVALID_ARG) or memory apart from it.
+ * A row with a negative position is skipped; a row with a negative slot gets its
+ * q but is not appended; slots are distinct.  Device errors: MOE_ERR_BAD_LENGTHS (detail:
+ * the row; a position past the table, the row is skipped), MOE_ERR_BAD_PAGE
+ * (detail: the page; a slot past the cache, the row is not appended).
+ */
+int moe_qkv_append(const moe_kv_shape* shape, const moe_rope* rope, const void* q_in, const void* k_new,
+                   const void* v_new, const int32_t* positions, const int64_t* slots, const float* q_norm,
+                   const float* k_norm, const float* cos_sin, const float* k_scale, const float* v_scale,
+                   void* q, void* k_cache, void* v_cache, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dense MXFP4: a layer's projections in the experts' weight format.  Rows are
+ * packed as w13 and w2 are (see the top): codes [rows, K/2] and scale bytes [rows, K/32].
+ */
+#define MOE_BF16 0
+#define MOE_F16  1
+#define MOE_F32  2
+
+/*
+ * Rows to MXFP4 (OCP Microscaling v1.0): for every 32 elements of a row, with M the
+ * largest magnitude, the scale is 2^(floor(log2 M) - 2), at least 2^-127 (byte 0,
+ * also where M is 0); a code is x / scale rounded to nearest even and
+ * saturated at +-6.  A block that holds a NaN or an infinity gets scale byte
+ * 255 and codes 0: it reads back as NaN.
+ *   x [rows, K] of type dtype (MOE_BF16, MOE_F16, MOE_F32), rows x_stride elements apart
+ *   (0: K; rows multiples of 16 bytes apart); codes and scales out, packed.
+ * K a multiple of 32 up to 1<<20; 1 <= rows, rows * K < 1<<44.  No workspace.
+ */
+int moe_mx_quantize(int64_t rows, int32_t K, int dtype, const void* x, int64_t x_stride, uint8_t* codes,
+                    uint8_t* scales, void* stream);
+
+/*
+ * MXFP4 rows to y [rows, K] of type dtype, rows y_stride elements apart (as
+ * above): code * scale, exact in fp32 and rounded to the type (to nearest even).
+ */
+int moe_mx_dequantize(int64_t rows, int32_t K, int dtype, const uint8_t* codes, const uint8_t* scales, void* y,
+                      int64_t y_stride, void* stream);
+
+#define MOE_MX_X_MXFP4 1u /* moe_mx_shape.flags: x is MXFP4 too */
+
+/*
+ * out = x . w^T.  Supported: 1 <= T <= 1<<20; N a multiple of 8, 8 <= N <= 1<<20; K a
+ * multiple of 128, 128 <= K <= 65536.  A stride of 0 is the packed one; others
+ * cover a row and are multiples of 8 elements (x_stride: bf16 x only).
+ */
+typedef struct moe_mx_shape {
+    int32_t T;           /* rows of x */
+    int32_t N;           /* rows of w: columns of out */
+    int32_t K;           /* length of the sums */
+    uint32_t flags;      /* MOE_MX_X_MXFP4 */
+    int64_t x_stride;    /* elements from one row of x to the next */
+    int64_t out_stride;  /* ... of out */
+} moe_mx_shape;
+
+/* Workspace size of moe_mx_linear in *bytes (pure host function); moe_workspace_init prepares it once. */
+int moe_mx_workspace_bytes(const moe_mx_shape* shape, size_t* bytes);
+
+/*
+ *   out[t, n] = sum_k x[t, k] * w[n, k], summed in fp32, rounded to bf16
+ *   x [T, K] bf16, or with MOE_MX_X_MXFP4 codes [T, K/2] and xs [T, K/32]
+ *   (xs NULL otherwise); w [N, K/2] codes (32-byte aligned), w_scales [N, K/32];
+ *   out [T, N] bf16
+ * The products are exact in fp32 but for a bf16 x, whose elements enter as two
+ * e4m3 terms under a power of two a block of 32 (see the top): exact down to
+ * 2^-9 of the block's largest magnitude, below that within 2^-17 of it.  A row of x
+ * with a NaN or an infinity (MXFP4: a scale byte of 255) gives a row of NaN.
+ * Device errors: MOE_ERR_BAD_SCALE (a scale byte of 255 in w: its column of out
+ * is NaN), MOE_ERR_TIMEOUT (the workspace is then prepared again).
+ * Calls that share a workspace must be ordered, as for the block's calls.
+ */
+int moe_mx_linear(const moe_mx_shape* shape, const void* x, const uint8_t* xs, const uint8_t* w,
+                  const uint8_t* w_scales, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Synchronises `stream`, returns the status latched in the workspace by the
  * device since the last call (MOE_OK, MOE_ERR_BAD_IDS, MOE_ERR_BAD_SCALE,
  * MOE_ERR_TIMEOUT or what the cache calls name; MOE_ERR_CUDA if the synchronisation itself failed) and

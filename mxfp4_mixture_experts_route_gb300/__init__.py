@@ -32,13 +32,17 @@ MOE_ERR_BAD_PAGE = -13
 MOE_POST_NORM = 1
 MOE_LOGIT_OFFSET = 2
 MOE_KV_E4M3 = 1
+MOE_ROPE_INTERLEAVED = 1
+MOE_MX_X_MXFP4 = 1
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_abi_version", "moe_strerror", "moe_workspace_bytes", "moe_workspace_init",
            "moe_route", "moe_experts", "moe_forward", "moe_forward_host", "moe_device_status",
            "moe_timing_enable", "moe_timing_collect", "moe_kernel_name", "moe_forward_noalloc",
            "moe_workspace_region", "moe_latent_workspace_bytes", "moe_latent_forward",
-           "moe_kv_workspace_bytes", "moe_kv_plan", "moe_kv_append", "moe_tree_attention")
+           "moe_kv_workspace_bytes", "moe_kv_plan", "moe_kv_append", "moe_tree_attention", "moe_qkv_append",
+           "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_workspace_bytes", "moe_mx_linear")
 
 # workspace regions (moe_workspace_region)
 MOE_WS_STATUS, MOE_WS_POS, MOE_WS_TILES, MOE_WS_XQ, MOE_WS_XS, MOE_WS_HQ, MOE_WS_HS, MOE_WS_Y, MOE_WS_LOGITS = range(9)
@@ -80,6 +84,26 @@ class KVShape(ctypes.Structure):
            head_stride=0, token_stride=0, q_stride=0, kv_stride=0):
         return cls(B, T, Hq, Hkv, D, page, n_pages, max_pages, mask_words, MOE_KV_E4M3 if e4m3 else 0,
                    D ** -0.5 if scale is None else scale, page_stride, head_stride, token_stride, q_stride, kv_stride)
+
+
+class Rope(ctypes.Structure):
+    """moe_rope: the heads' norms and the rotation of qkv_append."""
+    _fields_ = [("R", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("q_in_stride", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, R, max_pos=0, eps=1e-6, interleaved=False, q_in_stride=0):
+        return cls(R, max_pos, MOE_ROPE_INTERLEAVED if interleaved else 0, eps, q_in_stride)
+
+
+class MXShape(ctypes.Structure):
+    """moe_mx_shape: a product of x [T, K] with MXFP4 weights [N, K]."""
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, T, N, K, x_mxfp4=False, x_stride=0, out_stride=0):
+        return cls(T, N, K, MOE_MX_X_MXFP4 if x_mxfp4 else 0, x_stride, out_stride)
 
 
 class MoEError(RuntimeError):
@@ -134,6 +158,12 @@ def load_library(path: str) -> ctypes.CDLL:
     L.moe_kv_plan.argtypes = [_KSP] + [_P] * 4 + [ctypes.c_int32] + [_P] * 7 + [ctypes.c_size_t, _P]
     L.moe_kv_append.argtypes = [_KSP] + [_P] * 8 + [ctypes.c_size_t, _P]
     L.moe_tree_attention.argtypes = [_KSP] + [_P] * 12 + [ctypes.c_size_t, _P]
+    L.moe_qkv_append.argtypes = [_KSP, ctypes.POINTER(Rope)] + [_P] * 14 + [ctypes.c_size_t, _P]
+    L.moe_mx_quantize.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int, _P, ctypes.c_int64, _P, _P, _P]
+    L.moe_mx_dequantize.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int, _P, _P, _P, ctypes.c_int64, _P]
+    _MSP = ctypes.POINTER(MXShape)
+    L.moe_mx_workspace_bytes.argtypes = [_MSP, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_mx_linear.argtypes = [_MSP] + [_P] * 6 + [ctypes.c_size_t, _P]
     L.moe_timing_enable.argtypes = [ctypes.c_int]
     L.moe_timing_collect.argtypes = [_P, _P, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     L.moe_kernel_name.argtypes = [ctypes.c_int]
@@ -296,6 +326,90 @@ def tree_attention(shape, q, k_cache, v_cache, block_table, ctx_len, row_start, 
         ws.data_ptr(), ws.numel(), _stream(stream))
     if rc:
         raise MoEError(rc, "moe_tree_attention")
+
+
+def rope_table(max_pos, R, base=10000.0, device="cuda"):
+    """qkv_append's table: cos, then sin, of position * base^(-2 i / R), i = 0 .. R/2 - 1.  [max_pos, R] fp32, from
+    angles in 64 bits."""
+    import torch
+    i = torch.arange(R // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * base ** (-2 * i / R)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def qkv_append(shape, rope, q_in, k_new, v_new, positions, slots, q_norm, k_norm, cos_sin, k_scale, v_scale, q, k_cache,
+               v_cache, ws, stream=None) -> None:
+    """Norms and rotation of query and key heads, and the append of K and V; q may be q_in, norms may be None."""
+    rc = (_lib or lib()).moe_qkv_append(
+        ctypes.byref(shape), ctypes.byref(rope), q_in.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), _ptr(q_norm), _ptr(k_norm), _ptr(cos_sin), _ptr(k_scale), _ptr(v_scale),
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_qkv_append")
+
+
+_mx_types = {}
+
+
+def _mx_rows(t):
+    """(rows, K, MOE_* type, stride from row to row) of a tensor whose last dimension is K and whose others are rows."""
+    if not _mx_types:
+        import torch
+        _mx_types.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
+    dt = _mx_types.get(t.dtype)
+    if dt is None or t.dim() < 1:
+        raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (bf16, fp16 or fp32)")
+    if t.dim() != 2:
+        t = t.view(-1, t.shape[-1])        # (raises if the rows are not evenly apart)
+    rows, K = t.shape
+    if (K > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < K):
+        raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (elements of a row side by side, rows apart)")
+    return rows, K, dt, t.stride(0) if rows > 1 else 0
+
+
+def _mx_packed(rows, K, codes, scales):
+    if (codes.numel() * 2 != rows * K or scales.numel() * 32 != rows * K or not codes.is_contiguous()
+            or not scales.is_contiguous() or codes.element_size() != 1 or scales.element_size() != 1):
+        raise MoEError(MOE_ERR_INVALID_ARG, "mx codes [rows, K/2] and scales [rows, K/32] (packed bytes)")
+
+
+def mx_quantize(x, codes, scales, stream=None) -> None:
+    """Rows x [..., K] (bf16, fp16 or fp32) to MXFP4 codes [..., K/2] and scales [..., K/32] (uint8)."""
+    rows, K, dt, stride = _mx_rows(x)
+    _mx_packed(rows, K, codes, scales)
+    rc = (_lib or lib()).moe_mx_quantize(rows, K, dt, x.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(),
+                                         _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_mx_quantize")
+
+
+def mx_dequantize(codes, scales, y, stream=None) -> None:
+    """MXFP4 rows read back into y [..., K] (bf16, fp16 or fp32)."""
+    rows, K, dt, stride = _mx_rows(y)
+    _mx_packed(rows, K, codes, scales)
+    rc = (_lib or lib()).moe_mx_dequantize(rows, K, dt, codes.data_ptr(), scales.data_ptr(), y.data_ptr(), stride,
+                                           _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_mx_dequantize")
+
+
+def mx_workspace_bytes(shape: MXShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_mx_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "moe_mx_workspace_bytes")
+    return n.value
+
+
+def new_mx_workspace(shape: MXShape, device="cuda", stream=None):
+    """A device workspace (uint8 tensor, 256-byte aligned) of mx_linear, prepared by moe_workspace_init."""
+    return _workspace(mx_workspace_bytes(shape), device, stream)
+
+
+def mx_linear(shape, x, xs, w, w_scales, out, ws, stream=None) -> None:
+    """out = x . w^T with MXFP4 w; x bf16 (xs None) or MXFP4 codes with scales xs; out bf16."""
+    rc = (_lib or lib()).moe_mx_linear(ctypes.byref(shape), x.data_ptr(), _ptr(xs), w.data_ptr(), w_scales.data_ptr(),
+                                       out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if rc:
+        raise MoEError(rc, "moe_mx_linear")
 
 
 def device_status(ws, stream=None) -> tuple[int, int]:

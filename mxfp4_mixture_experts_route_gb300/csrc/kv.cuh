@@ -60,6 +60,20 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const KvDims& d, const AppendArgs& a, cudaStream_t st);
 
+struct QkvArgs {
+    const void *q_in, *k_new, *v_new;
+    const int32_t* positions;
+    const int64_t* slots;
+    const float *q_norm, *k_norm, *cos_sin, *k_scale, *v_scale;
+    void *q, *k_cache, *v_cache;
+    StatusBlock* sb;
+    int R, max_pos;
+    bool interleaved;
+    float eps;
+    int64_t q_in_stride;
+};
+cudaError_t launch_qkv_append(const KvDims& d, const QkvArgs& a, cudaStream_t st);
+
 struct AttnArgs {
     const void *q, *k_cache, *v_cache;
     const int32_t *block_table, *ctx_len, *row_start;

@@ -4,40 +4,16 @@
 //
 // Bound: HBM (each row read once, written once) for prompts, latency for a
 // step's few rows.  A thread moves 16-byte pieces, blockIdx.y picks K or V.
-#include "kv.cuh"
-#include "tc_ptx.cuh"
-
-#include <math_constants.h>
+#include "kv_codes.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int APPEND_THREADS = 256;
 
-// The code of x / s is that of the division's correctly rounded quotient, not of
-// a product with the reciprocal, so that a code is the one the formula gives.  The
-// product is off by less than 2^-22 of itself, so where a little more and a little
-// less than it give the same code, that is the quotient's code too (rounding
-// is monotonic); only next to a tie between two codes the division is made.
-struct Scale {
-    float s, lo, hi;
-    __device__ __forceinline__ explicit Scale(float v) : s(v) {
-        const float r = __fdiv_rn(1.f, v);
-        // (a scale whose reciprocal is not an ordinary number: always by division)
-        const bool fine = v > 0x1p-120f && v < 0x1p120f;
-        lo = fine ? r * (1.f - 0x1p-21f) : 1.f;
-        hi = fine ? r * (1.f + 0x1p-21f) : CUDART_NAN_F;
-    }
-};
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float e) {
-    return ptx::cvt_e4m3x2(a, b) | ptx::cvt_e4m3x2(c, e) << 16;   // saturates at +-448
-}
-__device__ __forceinline__ uint32_t quant4(uint32_t lo, uint32_t hi, const Scale& k) {
-    const float a = __uint_as_float(lo << 16), b = __uint_as_float(lo & 0xFFFF0000u);
-    const float c = __uint_as_float(hi << 16), e = __uint_as_float(hi & 0xFFFF0000u);
-    const uint32_t u = codes4(a * k.lo, b * k.lo, c * k.lo, e * k.lo), v = codes4(a * k.hi, b * k.hi, c * k.hi, e * k.hi);
-    if (u == v) return u;
-    return codes4(__fdiv_rn(a, k.s), __fdiv_rn(b, k.s), __fdiv_rn(c, k.s), __fdiv_rn(e, k.s));
+__device__ __forceinline__ uint32_t quant4(uint32_t lo, uint32_t hi, const KvScale& k) {
+    return kv_codes4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
+                     __uint_as_float(hi & 0xFFFF0000u), k);
 }
 
 // U pieces a thread at once, their loads under way together.  Measured: 16,411 rows of
@@ -93,7 +69,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) k_kv_append(const KvDims d, co
         for (int u = 0; u < U; ++u) {
             if (to[u] < 0) continue;
             if (E4M3) {
-                const Scale k(s[u]);
+                const KvScale k(s[u]);
                 *reinterpret_cast<uint4*>(dst + to[u]) = make_uint4(quant4(x[u].x, x[u].y, k), quant4(x[u].z, x[u].w, k),
                                                                     quant4(y[u].x, y[u].y, k), quant4(y[u].z, y[u].w, k));
             } else {

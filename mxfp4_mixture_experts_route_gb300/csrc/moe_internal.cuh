@@ -130,7 +130,8 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // ---------------------------------------------------------------------------
 enum KernelId {
     K_ROUTER = 0, K_TOPK, K_SORT, K_GATHER, K_EXPERTS, K_COMBINE, K_ROUTE_GATHER,
-    K_LATENT_DOWN, K_LATENT_MID, K_LATENT_UP, K_KV_PLAN, K_KV_APPEND, K_TREE_ATTN, K_NUM
+    K_LATENT_DOWN, K_LATENT_MID, K_LATENT_UP, K_KV_PLAN, K_KV_APPEND, K_TREE_ATTN, K_QKV_APPEND, K_MX_QUANT,
+    K_MX_DEQUANT, K_MX_SPLIT, K_MX_LINEAR, K_NUM
 };
 void timing_begin(int kernel_id, cudaStream_t st);
 void timing_end(cudaStream_t st);

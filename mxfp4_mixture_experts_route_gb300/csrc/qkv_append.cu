@@ -1,0 +1,167 @@
+// Norms and rotation of query and key heads, and the append of K and V.
+//
+//   y = x rsqrt(mean x^2 + eps) w;   z_i = y_i cos_i - y_j sin_i,  z_j = y_j cos_i + y_i sin_i
+//
+// Bound: HBM (each row read once, written once) for prompts, latency for a
+// step's few rows.  D / 8 lanes hold a head, 8 elements each, and take
+// some heads of one token: the angles and weights are the same for all of
+// them, so a lane keeps w cos and w' sin of its elements in registers
+// (z = r (x (w cos) + x' (w' sin)), x' the pair's other element, r the head's rsqrt) and a
+// head costs it one load, one sum over the lanes, four shuffles and one store.
+#include "kv_codes.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int QKV_THREADS = 128;
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// eight fp32 of a table or weight row an earlier kernel may have written
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = ld_dep(reinterpret_cast<const float4*>(p)), b = ld_dep(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// LPH lanes a head, HPG heads a group of lanes.
+template <int LPH, int HPG, bool E4M3, bool INTER>
+__global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, const QkvArgs a) {
+    constexpr int D = LPH * 8;
+    const int qc = (d.Hq + HPG - 1) / HPG, kc = (d.Hkv + HPG - 1) / HPG, chunks = qc + 2 * kc;
+    const int t = blockIdx.x;
+    int c = blockIdx.y * (blockDim.x / LPH) + threadIdx.x / LPH;
+    const int p = threadIdx.x % LPH;                 // the lane's piece of the head
+    const uint32_t lanes = LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1) << (threadIdx.x % 32 / LPH * LPH);
+    KT_MARK(K_QKV_APPEND, 0);
+    pdl_wait();
+    KT_MARK(K_QKV_APPEND, 1);
+    if (c >= chunks) return;                         // (whole groups: the lanes of a head stay together)
+    const int pos = ld_dep(a.positions + t);
+    const int64_t slot = ld_dep(reinterpret_cast<const long long*>(a.slots) + t);
+    const int what = c < qc ? 0 : c < qc + kc ? 1 : 2;   // q, K, V
+    c -= what == 0 ? 0 : what == 1 ? qc : qc + kc;
+    const int heads = what == 0 ? d.Hq : d.Hkv, h0 = c * HPG;
+    if (pos < 0) return;
+    if (a.R > 0 && pos >= a.max_pos) {
+        latch_status(a.sb, MOE_ERR_BAD_LENGTHS, t);
+        return;
+    }
+    int64_t to = 0;
+    if (what != 0) {
+        if (slot >= (int64_t)d.n_pages * d.page) {
+            latch_status(a.sb, MOE_ERR_BAD_PAGE, (int)(slot / d.page));
+            return;
+        }
+        if (slot < 0) return;
+        const int pg = (int)slot / d.page, o = (int)slot - pg * d.page;
+        to = pg * d.page_stride + o * d.token_stride + 8 * p;
+    }
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(what == 0 ? a.q_in : what == 1 ? a.k_new : a.v_new) +
+                          t * (what == 0 ? a.q_in_stride : d.kv_stride) + (int64_t)h0 * D + 8 * p;
+    uint4 x[HPG];
+#pragma unroll
+    for (int i = 0; i < HPG; ++i)
+        if (h0 + i < heads) x[i] = ld_dep(reinterpret_cast<const uint4*>(src + i * D));
+
+    const float* w = what == 0 ? a.q_norm : a.k_norm;
+    // own[j] = w cos, other[j] = +- w' sin of the lane's element j; partner: the piece that holds x'
+    float own[8], other[8];
+    const bool turned = what != 2 && 8 * p < a.R;
+    const int half = a.R / 16;                       // pieces of half the rotated part
+    const int partner = INTER || !turned ? p : p < half ? p + half : p - half;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) own[j] = 1.f, other[j] = 0.f;
+    if (what != 2 && w) load8(w + 8 * p, own);
+    if (turned) {
+        const float* row = a.cos_sin + (int64_t)pos * a.R;
+        float cs[8], sn[8], wp[8];
+        if (INTER) {
+            const float4 u = ld_dep(reinterpret_cast<const float4*>(row + 4 * p));
+            const float4 v = ld_dep(reinterpret_cast<const float4*>(row + a.R / 2 + 4 * p));
+            cs[0] = cs[1] = u.x, cs[2] = cs[3] = u.y, cs[4] = cs[5] = u.z, cs[6] = cs[7] = u.w;
+            sn[1] = v.x, sn[3] = v.y, sn[5] = v.z, sn[7] = v.w;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) sn[j] = -sn[j + 1], wp[j] = own[j + 1], wp[j + 1] = own[j];
+        } else {
+            const int i = 8 * (p < half ? p : p - half);
+            load8(row + i, cs);
+            load8(row + a.R / 2 + i, sn);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wp[j] = 1.f, sn[j] = p < half ? -sn[j] : sn[j];
+            if (w) load8(w + 8 * partner, wp);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) other[j] = wp[j] * sn[j], own[j] *= cs[j];
+    }
+    const bool norm = what != 2 && w;
+    const float* scale = what == 1 ? a.k_scale : a.v_scale;
+#pragma unroll
+    for (int i = 0; i < HPG; ++i) {
+        if (h0 + i >= heads) break;
+        const int h = h0 + i;
+        const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[2 * j] = lo_f(v[j]), f[2 * j + 1] = hi_f(v[j]);
+        float r = 1.f;
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o /= 2) ss += __shfl_xor_sync(lanes, ss, o);
+            r = rsqrtf(ss * (1.f / D) + a.eps);
+        }
+        if (what != 2) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t o = INTER ? __byte_perm(v[j], 0, 0x1032) : __shfl_sync(lanes, v[j], partner, LPH);
+                // (no product with the other element where nothing turns: it may be an infinity)
+                float a0 = f[2 * j] * own[2 * j], a1 = f[2 * j + 1] * own[2 * j + 1];
+                if (turned) a0 = fmaf(lo_f(o), other[2 * j], a0), a1 = fmaf(hi_f(o), other[2 * j + 1], a1);
+                f[2 * j] = a0 * r, f[2 * j + 1] = a1 * r;
+            }
+        }
+        if (what == 0 || !E4M3) {
+            const uint4 y = make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]),
+                                       ptx::cvt_bf16x2(f[4], f[5]), ptx::cvt_bf16x2(f[6], f[7]));
+            uint16_t* dst = what == 0 ? reinterpret_cast<uint16_t*>(a.q) + t * d.q_stride + (int64_t)h * D + 8 * p
+                                      : reinterpret_cast<uint16_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
+            *reinterpret_cast<uint4*>(dst) = y;
+        } else {
+            const KvScale k(ld_dep(scale + h));
+            uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(kv_codes4(f[0], f[1], f[2], f[3], k), kv_codes4(f[4], f[5], f[6], f[7], k));
+        }
+    }
+    KT_MARK(K_QKV_APPEND, 2);
+}
+
+template <int LPH, int HPG>
+cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
+    // a token's groups in equal blocks
+    const int chunks = (d.Hq + HPG - 1) / HPG + 2 * ((d.Hkv + HPG - 1) / HPG);
+    const int ny = (chunks * LPH + QKV_THREADS - 1) / QKV_THREADS;
+    const dim3 grid(d.T, ny), block((chunks + ny - 1) / ny * LPH);
+    if (d.e4m3)
+        return a.interleaved ? launch_pdl(k_qkv_append<LPH, HPG, true, true>, grid, block, 0, st, d, a)
+                             : launch_pdl(k_qkv_append<LPH, HPG, true, false>, grid, block, 0, st, d, a);
+    return a.interleaved ? launch_pdl(k_qkv_append<LPH, HPG, false, true>, grid, block, 0, st, d, a)
+                         : launch_pdl(k_qkv_append<LPH, HPG, false, false>, grid, block, 0, st, d, a);
+}
+
+}  // namespace
+
+cudaError_t launch_qkv_append(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
+    KT_BIND();
+    timing_begin(K_QKV_APPEND, st);
+    // one head a group while those groups fit one round of the SMs' threads (shortest path), four otherwise
+    const bool few = (int64_t)d.T * (d.Hq + 2 * d.Hkv) * (d.D / 8) <= (int64_t)num_sms() * 2048;
+    const cudaError_t e = d.D == 128 ? few ? launch_heads<16, 1>(d, a, st) : launch_heads<16, 4>(d, a, st)
+                                     : few ? launch_heads<8, 1>(d, a, st) : launch_heads<8, 4>(d, a, st);
+    timing_end(st);
+    return e;
+}
+
+}  // namespace moe

@@ -22,6 +22,7 @@ namespace moe {
 struct QuantChunk {
     uint2 hi, lo;
     int e;
+    uint32_t amax;   // bits of the block's largest magnitude
 };
 
 // Eight bf16 elements v of one row (a thread's chunk).  All 32 lanes of the
@@ -58,6 +59,7 @@ __device__ __forceinline__ QuantChunk quantize_vals(const uint4 v) {
     q.hi = make_uint2(hw[0], hw[1]);
     q.lo = make_uint2(lw[0], lw[1]);
     q.e = e;
+    q.amax = amax;
     return q;
 }
 

@@ -324,6 +324,33 @@ __host__ __device__ constexpr uint32_t idesc_mx_e2m1_e4m3(int m, int n, int asf,
            ((uint32_t)(m >> 4) << 24) | ((uint32_t)asf << 29);
 }
 
+// Block-scaled MMA, kind::mxf4 with one e8m0 scale per 32 K (scale_vec 2X): A and B
+// are packed e2m1 (K = 64 an instruction, 32 bytes of a row).  The scales stand
+// as for mma_mx_ss, two bytes of a cell an instruction: those at the instruction
+// descriptor's scale-factor id (0 or 2) and behind it.
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t sfa_tmem, uint32_t sfb_tmem) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+// Instruction descriptor, kind::mxf4 block-scaled: A and B e2m1, e8m0 scales, fp32 accumulator, K = 64.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int asf, int bsf) {
+    return ((uint32_t)bsf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(m >> 4) << 24) | ((uint32_t)asf << 29);
+}
+
+// 32 lanes x 8 consecutive 32-bit TMEM columns (taddr's column a multiple of 8)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // 32 lanes x 2 consecutive 32-bit TMEM columns (taddr's column a multiple of 2)
 __device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t v0, uint32_t v1) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(v0), "r"(v1) : "memory");

@@ -18,7 +18,8 @@ int g_used = 0;            // pairs recorded since the last collect
 int g_open = -1;           // pair started by timing_begin, not yet ended
 
 const char* const kNames[K_NUM] = {"router_logits", "topk", "sort", "gather", "experts", "combine", "topk_sort_gather",
-                                   "latent_down", "latent_mid", "latent_up", "kv_plan", "kv_append", "tree_attn"};
+                                   "latent_down", "latent_mid", "latent_up", "kv_plan", "kv_append", "tree_attn", "qkv_append",
+                                   "mx_quantize", "mx_dequantize", "mx_split", "mx_linear"};
 
 void free_all() {
     for (auto& r : g_recs) {
