@@ -404,11 +404,32 @@ __global__ void __launch_bounds__(L_THREADS, 1)
             }
             ptx::named_bar_sync(2, 128);
             if (!last_flag[0]) continue;
-            for (int t = 0; t < n_tok; ++t) {
-                float y = 0.f;
-                for (int c = c0; c <= c1; ++c)
-                    y += ld_dep(a.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * NT * LM + t * LM + r);
-                if (row < a.N) a.out[(t0 + t) * a.out_stride + row] = __float2bfloat16_rn(y);
+            // four rows a lane, a token a warp at a time; J tokens' loads under way together
+            constexpr int J = NT / 4 < 8 ? NT / 4 : 8;
+            const int row4 = (int)(g.tile / a.tt) * LM + 4 * lane;
+            const float* p = a.parts + ((int64_t)c0 * 2 + 1) * NT * LM + 4 * lane;
+#pragma unroll 1
+            for (int tb = warp - 6; tb < n_tok; tb += 4 * J) {
+                float4 y[J];
+#pragma unroll
+                for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int c = c0; c <= c1; ++c) {
+                    const float* from = c == c0 ? p : p + ((int64_t)(c - c0) * 2 - 1) * NT * LM;
+                    float4 v[J];
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        v[j] = tb + 4 * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + 4 * j) * LM))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        y[j].x += v[j].x, y[j].y += v[j].y, y[j].z += v[j].z, y[j].w += v[j].w;
+                }
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (tb + 4 * j < n_tok && row4 < a.N)
+                        *reinterpret_cast<uint2*>(a.out + (t0 + tb + 4 * j) * a.out_stride + row4) =
+                            make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
             }
             ptx::named_bar_sync(2, 128);   // the flag is written again
         }
