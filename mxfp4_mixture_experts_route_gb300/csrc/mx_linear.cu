@@ -4,17 +4,22 @@
 // both stay packed (tcgen05.mma kind::mxf4, K = 64).  A bf16 x enters as
 // in the experts' kernel (experts_mx.cu): as two e4m3 terms a row, hi and lo, under
 // a power of two a block of 32, which a small kernel (k_mx_split) writes first; the TMA
-// unpacks the weights' codes for kind::mxf8f6f4 and a token takes two columns of the
-// MMA, added at the end.  Either way the tensor core applies the block scales.
+// unpacks the weights' codes for kind::mxf8f6f4.  Either way the tensor core applies the
+// block scales.
 //
-// All tiles (128 weight rows x NT tokens) stand one after the other on a line, cut into
-// stages of 256 K; each of the persistent CTAs takes an equal share of the line.
-// A tile that a cut divides is joined without waiting: every CTA writes its
+// Few tokens: one CTA a tile of 128 weight rows x NT tokens; a token of a bf16 x takes
+// two columns of the MMA, added at the end.  Many: a pair of CTAs (cta_group::2) a tile of
+// 256 weight rows x 256 tokens, of which each holds half of either operand; the terms of
+// a bf16 x are two MMAs into one accumulator.
+//
+// All tiles stand one after the other on a line, cut into
+// stages of KS elements of K; each of the persistent CTAs (pairs) takes an equal share of
+// the line.  A tile that a cut divides is joined without waiting: every CTA writes its
 // part to the workspace and counts itself, and the one that comes last adds the
 // parts in the order of the line (so the sum does not depend on who came last).
 //
 // Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> TMEM, 1024 K ahead in
-// registers), 6-9 the accumulators' way out.
+// registers), 6 on the accumulators' way out: four, or eight of a pair's CTA.
 #include "mx.cuh"
 #include "quant.cuh"
 #include "tc_ptx.cuh"
@@ -22,21 +27,30 @@
 namespace moe {
 namespace {
 
-constexpr int LM = 128;                       // weight rows a tile
-constexpr int LKS = 256;                      // K a stage
-constexpr int L_THREADS = 320;
-constexpr int SF_SLOT = 64;                   // TMEM columns of a stage's scales
-constexpr int SF_A1 = 16, SF_B0 = 32, SF_B1 = 48;
+constexpr int LM = 128;                       // weight rows a CTA
 constexpr uint64_t L_WAIT_NS = 2000000000ull;
 constexpr int L_SITE = 300;                   // detail of MOE_ERR_TIMEOUT: site of the wait
 
-template <bool XMX, int NT>
+// NT tokens a tile, CG CTAs a tile.
+template <bool XMX, int NT, int CG>
 struct LCfg {
-    static constexpr int NB = XMX ? NT : 2 * NT;                  // MMA N
-    static constexpr int A_BYTES = XMX ? LM * 128 : LM * 256;     // a stage's weights in shared memory
-    static constexpr int B_BYTES = XMX ? NB * 128 : NB * 256;
+    static constexpr int TERMS = !XMX && CG == 2 ? 2 : 1;         // MMAs of a K step
+    static constexpr int PER = !XMX && CG == 1 ? 2 : 1;           // accumulator columns a token
+    static constexpr int NB = PER * NT;                           // MMA N
+    static constexpr int KS = TERMS == 2 ? 128 : 256;             // K a stage
+    static constexpr int WORDS = KS / 128;                        // 32-bit words of scale bytes a row and stage
+    static constexpr int B_ROWS = NB / CG;                        // rows of one term of x in this CTA
+    static constexpr int A_BYTES = XMX ? LM * KS / 2 : LM * KS;   // a stage's weights in shared memory
+    static constexpr int B_BYTES = XMX ? B_ROWS * KS / 2 : TERMS * B_ROWS * KS;
+    static constexpr int EW = CG == 2 ? 8 : 4;                    // warps of the way out, and tokens of each
+    static constexpr int EN = NT / (EW / 4);
+    static constexpr int THREADS = 32 * (6 + EW);
     static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int TX = CG * (LM * KS / 2 + B_BYTES);       // bytes of a stage that its barrier counts
     static constexpr int ACC = NB <= 128 ? 2 : 1;                 // accumulators
+    // a stage's scales in TMEM: weight words of 128 K each at SF_A, SF_A + 16, the token words behind them
+    // (every scale address is a multiple of 16 columns)
+    static constexpr int SF_SLOT = WORDS * 32, SF_B = WORDS * 16;
     static constexpr int SF_COL0 = (ACC * NB + 63) / 64 * 64;
     static constexpr int S_TMEM = (512 - SF_COL0) / SF_SLOT;
     static constexpr bool XCH = NB > 32;                          // token scales exchanged through shared memory
@@ -45,6 +59,7 @@ struct LCfg {
     static constexpr int S = S_FIT < S_TMEM ? S_FIT : S_TMEM;
     static constexpr int SMEM = 1024 + S * STAGE + XCH_BYTES + 512;
     static_assert(S >= 2 && SMEM <= 232448, "stages");
+    static_assert(CG == 1 || NT == 256, "a pair's tile is 256 x 256");
 };
 
 struct LArgs {
@@ -61,25 +76,34 @@ struct LArgs {
     int w_once;
 };
 
-// [first, last) of CTA c's share of the line, and the CTA that holds stage p
+// the first stage of worker c's share of the line (of n), and the worker that holds stage p
 __device__ __forceinline__ int64_t share(int64_t total, int c, int n) { return total * c / n; }
 __device__ __forceinline__ int holder_of(int64_t p, int64_t total, int n) { return (int)(((p + 1) * n - 1) / total); }
 
-// A CTA's segments: stages [k0, k1) of a tile, one tile after the other.
+// A worker's segments: stages [k0, k1) of tile (m, t), one tile after the other (token tiles fastest).
+template <int CG>
 struct Segment {
-    int64_t at, end, tile;
-    int k0, k1, nk;
-    __device__ __forceinline__ Segment(const LArgs& a)
-        : at(share(a.total, blockIdx.x, gridDim.x)), end(share(a.total, blockIdx.x + 1, gridDim.x)), nk(a.nk) {
-        tile = at / nk;
-        k0 = (int)(at - tile * nk);
+    int64_t left;
+    int tile, m, t, k0, k1, nk, tt;
+    __device__ __forceinline__ explicit Segment(const LArgs& a) : nk(a.nk), tt(a.tt) {
+        const int c = blockIdx.x / CG, n = gridDim.x / CG;
+        const int64_t at = share(a.total, c, n);
+        left = share(a.total, c + 1, n) - at;
+        tile = (int)(at / nk);
+        m = tile / tt;
+        t = tile - m * tt;
+        k0 = (int)(at - (int64_t)tile * nk);
         cut();
     }
-    __device__ __forceinline__ void cut() { k1 = (int)min((int64_t)nk, k0 + (end - at)); }
-    __device__ __forceinline__ bool more() const { return at < end; }
+    __device__ __forceinline__ void cut() { k1 = (int)min((int64_t)nk, k0 + left); }
+    __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next() {
-        at += k1 - k0;
+        left -= k1 - k0;
         ++tile;
+        if (++t == tt) {
+            t = 0;
+            ++m;
+        }
         k0 = 0;
         cut();
     }
@@ -106,14 +130,16 @@ __device__ __forceinline__ void load_scales(const uint8_t* row, int g, int kb, b
     }
 }
 
-template <bool XMX, int NT>
-__global__ void __launch_bounds__(L_THREADS, 1)
+template <bool XMX, int NT, int CG>
+__global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     k_mx_linear(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const LArgs a) {
-    using C = LCfg<XMX, NT>;
-    constexpr int S = C::S, NB = C::NB, ACC = C::ACC;
+    using C = LCfg<XMX, NT, CG>;
+    constexpr int S = C::S, NB = C::NB, ACC = C::ACC, WORDS = C::WORDS;
+    constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t* xch = reinterpret_cast<uint32_t*>(sm + S * C::STAGE);     // [2][8 words][NT] token scales
+    // a pair's stages are counted on the even CTA's `full`, and its MMAs' ends on both CTAs' barriers
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S * C::STAGE + C::XCH_BYTES);
     uint64_t* empty = full + S;          // the stage's MMAs are done
     uint64_t* acc_full = empty + S;
@@ -124,15 +150,16 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     volatile int* last_flag = abort_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? blockIdx.x & 1 : 0;
     KT_MARK(K_MX_LINEAR, 0);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            ptx::mbar_init(&full[i], 1 + 4);      // TMA, the four scale warps
+            ptx::mbar_init(&full[i], 1 + 4 * CG);      // TMA, the scale warps
             ptx::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < ACC; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 4);
+            ptx::mbar_init(&acc_empty[i], C::EW * CG);
         }
         ptx::mbar_init(fin, 1);
         *abort_flag = 0;
@@ -140,9 +167,13 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         ptx::prefetch_tensormap(&tm_w);
         ptx::prefetch_tensormap(&tm_x);
     }
-    if (warp == 1) ptx::tmem_alloc(holder, 512);
+    if (warp == 1) {
+        if (PAIR) ptx::tmem2_alloc(holder, 512);
+        else ptx::tmem_alloc(holder, 512);
+    }
     ptx::tc_fence_before();
     __syncthreads();
+    if (PAIR) ptx::cluster_sync_all();   // both CTAs' barriers exist
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
     // with MXFP4 x this is the call's first kernel: it reads nothing before its wait
@@ -156,126 +187,155 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         // ------------------------------------------------------------ TMA
         const uint64_t pol_w = a.w_once ? ptx::policy_evict_first() : ptx::policy_evict_last();
         const uint64_t pol_x = ptx::policy_evict_last();
-        auto weights = [&](int64_t tile, int k, int s) {
+        const uint32_t full0 = PAIR ? ptx::map_cluster(full, 0) : 0;
+        auto weights = [&](const Segment<CG>& g, int k, int s) {
             uint8_t* st = sm + s * C::STAGE;
-            const int row = (int)(tile / a.tt) * LM;
-            ptx::mbar_arrive_expect_tx(&full[s], LM * 128 + C::B_BYTES);
-            if (XMX)
-                ptx::tma_load_2d(st, &tm_w, 128 * k, row, &full[s], pol_w);
-            else
-                ptx::tma_load_3d(st, &tm_w, 0, row, 2 * k, &full[s], pol_w);
+            const int row = (g.m * CG + rank) * LM;
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], C::TX);
+            if (PAIR) {
+                if (XMX) ptx::tma2_load_2d(st, &tm_w, 128 * k, row, full0 + 8 * s, pol_w);
+                else ptx::tma2_load_3d(st, &tm_w, 0, row, WORDS * k, full0 + 8 * s, pol_w);
+            } else {
+                if (XMX) ptx::tma_load_2d(st, &tm_w, 128 * k, row, &full[s], pol_w);
+                else ptx::tma_load_3d(st, &tm_w, 0, row, WORDS * k, &full[s], pol_w);
+            }
         };
-        auto tokens = [&](int64_t tile, int k, int s) {
+        auto tokens = [&](const Segment<CG>& g, int k, int s) {
             uint8_t* st = sm + s * C::STAGE + C::A_BYTES;
-            const int row = (int)(tile % a.tt) * NB;
-            if (XMX)
-                ptx::tma_load_2d(st, &tm_x, 128 * k, row, &full[s], pol_x);
-            else
-                ptx::tma_load_3d(st, &tm_x, 0, row, 2 * k, &full[s], pol_x);
+            const int row = g.t * NB + rank * C::B_ROWS;
+            if (PAIR) {
+                if (XMX) ptx::tma2_load_2d(st, &tm_x, 128 * k, row, full0 + 8 * s, pol_x);
+                else ptx::tma2_load_4d(st, &tm_x, 0, row, 0, k, full0 + 8 * s, pol_x);
+            } else {
+                if (XMX) ptx::tma_load_2d(st, &tm_x, 128 * k, row, &full[s], pol_x);
+                else ptx::tma_load_3d(st, &tm_x, 0, row, 2 * k, &full[s], pol_x);
+            }
         };
         if (lane == 0) {
             int pre = 0;
             if (!XMX) {
                 // the first stages' weights, inputs of the call, before the wait for the tokens' terms
                 int i = 0;
-                for (Segment g(a); g.more() && i < S; g.next())
-                    for (int k = g.k0; k < g.k1 && i < S; ++k, ++i) weights(g.tile, k, i);
+                for (Segment<CG> g(a); g.more() && i < S; g.next())
+                    for (int k = g.k0; k < g.k1 && i < S; ++k, ++i) weights(g, k, i);
                 pre = i;
                 pdl_wait();
             }
             bool ok = true;
-            int it = 0;
-            for (Segment g(a); ok && g.more(); g.next()) {
+            int it = 0, s = 0;
+            uint32_t par = 1;
+            for (Segment<CG> g(a); ok && g.more(); g.next()) {
                 for (int k = g.k0; k < g.k1; ++k, ++it) {
-                    const int s = it % S;
                     if (it >= pre) {
-                        if (!ptx::mbar_wait(&empty[s], ((it / S) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
+                        if (!ptx::mbar_wait(&empty[s], par, abort_flag, L_WAIT_NS)) {
                             fail(1);
                             ok = false;
                             break;
                         }
-                        weights(g.tile, k, s);
+                        weights(g, k, s);
                     }
-                    tokens(g.tile, k, s);
+                    tokens(g, k, s);
+                    if (++s == S) s = 0, par ^= 1;
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        int it = 0, seg = 0;
-        bool ok = true;
-        for (Segment g(a); ok && g.more(); g.next(), ++seg) {
-            const int ab = seg % ACC;
-            if (!ptx::mbar_wait_warp(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
-                if (lane == 0) fail(2);
-                ok = false;
-            }
-            const uint32_t d_tmem = tmem + ab * NB;
-            for (int k = g.k0; ok && k < g.k1; ++k, ++it) {
-                const int s = it % S;
-                if (!ptx::mbar_wait_warp(&full[s], (it / S) & 1, abort_flag, L_WAIT_NS)) {
-                    if (lane == 0) fail(3);
+        if (rank == 0) {
+            int s = 0, seg = 0;
+            uint32_t par = 0;
+            bool ok = true;
+            for (Segment<CG> g(a); ok && g.more(); g.next(), ++seg) {
+                const int ab = seg % ACC;
+                if (!ptx::mbar_wait_all<PAIR>(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
+                    if (lane == 0) fail(2);
                     ok = false;
-                    break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t a0 = ptx::smem_u32(sm + s * C::STAGE), b0 = a0 + C::A_BYTES;
-                const uint32_t col = tmem + C::SF_COL0 + s * SF_SLOT;
-                if (ptx::elect_one()) {
-                    if constexpr (XMX) {
+                const uint32_t d_tmem = tmem + ab * NB;
+                for (int k = g.k0; ok && k < g.k1; ++k) {
+                    if (!ptx::mbar_wait_all<PAIR>(&full[s], par, abort_flag, L_WAIT_NS)) {
+                        if (lane == 0) fail(3);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a0 = ptx::smem_u32(sm + s * C::STAGE), b0 = a0 + C::A_BYTES;
+                    const uint32_t sfa = tmem + C::SF_COL0 + s * C::SF_SLOT, sfb = sfa + C::SF_B;
+                    if (ptx::elect_one()) {
+                        if constexpr (XMX) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            ptx::mma_mxf4_ss(d_tmem, ptx::smem_desc_sw128(a0 + 32 * j), ptx::smem_desc_sw128(b0 + 32 * j),
-                                             ptx::idesc_mxf4(LM, NB, 2 * (j & 1), 2 * (j & 1)), k > g.k0 || j > 0,
-                                             col + SF_A1 * (j >> 1), col + SF_B0 + (SF_B1 - SF_B0) * (j >> 1));
-                    } else {
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t ad = ptx::smem_desc_sw128(a0 + 32 * j), bd = ptx::smem_desc_sw128(b0 + 32 * j);
+                                const uint32_t id = ptx::idesc_mxf4(LM * CG, NB, 2 * (j & 1), 2 * (j & 1));
+                                const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * (j >> 1), fb = sfb + 16 * (j >> 1);
+                                if (PAIR) ptx::mma2_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                                else ptx::mma_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                            }
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int h = j >> 2, q = j & 3;   // 128-K slab, K step within it
-                            ptx::mma_mx_ss(d_tmem, ptx::smem_desc_sw128(a0 + h * LM * 128 + 32 * q),
-                                           ptx::smem_desc_sw128(b0 + h * NB * 128 + 32 * q),
-                                           ptx::idesc_mx_e2m1_e4m3(LM, NB, q, q), k > g.k0 || j > 0,
-                                           col + SF_A1 * h, col + SF_B0 + (SF_B1 - SF_B0) * h);
+                            for (int j = 0; j < 4 * WORDS * C::TERMS; ++j) {
+                                // 128-K slab, K step within it, term
+                                const int h = WORDS == 2 ? j >> 2 : 0, q = j & 3, e = C::TERMS == 2 ? j >> 2 : 0;
+                                const uint64_t ad = ptx::smem_desc_sw128(a0 + h * LM * 128 + 32 * q);
+                                const uint64_t bd = ptx::smem_desc_sw128(b0 + (h + e) * C::B_ROWS * 128 + 32 * q);
+                                const uint32_t id = ptx::idesc_mx_e2m1_e4m3(LM * CG, NB, q, q);
+                                const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * h, fb = sfb + 16 * h;
+                                if (PAIR) ptx::mma2_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                                else ptx::mma_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                            }
+                        }
+                        if (PAIR) {
+                            ptx::mma2_commit(&empty[s]);
+                            if (k + 1 == g.k1) ptx::mma2_commit(&acc_full[ab]);
+                        } else {
+                            ptx::mma_commit(&empty[s]);
+                            if (k + 1 == g.k1) ptx::mma_commit(&acc_full[ab]);
                         }
                     }
-                    ptx::mma_commit(&empty[s]);
-                    if (k + 1 == g.k1) ptx::mma_commit(&acc_full[ab]);
+                    __syncwarp();
+                    if (++s == S) s = 0, par ^= 1;
                 }
-                __syncwarp();
             }
+            // every MMA issued above has completed before TMEM is released
+            if (ptx::elect_one()) {
+                if (PAIR) ptx::mma2_commit(fin);
+                else ptx::mma_commit(fin);
+            }
+            __syncwarp();
         }
-        // every MMA issued above has completed before TMEM is released
-        if (ptx::elect_one()) ptx::mma_commit(fin);
-        __syncwarp();
-        ptx::mbar_wait(fin, 0, abort_flag, L_WAIT_NS);
+        ptx::mbar_wait_all<PAIR>(fin, 0, abort_flag, L_WAIT_NS);
     } else if (warp < 6) {
         // ------------------------------------------------------------ scales
         const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row of this thread
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int kb = a.K / 32;
+        constexpr int PG = 8 / WORDS;                                 // stages of a group of 1024 K
         constexpr int OWN = !C::XCH ? 1 : NT > 128 ? NT / 128 : 1;    // tokens whose scales this thread loads
+        const uint32_t full0 = PAIR ? ptx::map_cluster(full, 0) : 0;
         uint32_t wa[8], wb[OWN][8], na[8], nb[OWN][8];
-        auto load_a = [&](int64_t tile, int grp) {
-            const int64_t row = tile / a.tt * LM + r;
-            load_scales(row < a.N ? a.w_scales + row * kb : nullptr, grp, kb, a.vec, na);
+        auto load_a = [&](const Segment<CG>& g, int grp) {
+            const int row = (g.m * CG + rank) * LM + r;
+            load_scales(row < a.N ? a.w_scales + (int64_t)row * kb : nullptr, grp, kb, a.vec, na);
         };
-        auto load_b = [&](int64_t tile, int grp) {
+        auto load_b = [&](const Segment<CG>& g, int grp) {
 #pragma unroll
             for (int u = 0; u < OWN; ++u) {
                 const int j = !C::XCH ? (XMX ? lane : lane >> 1) % NT : r + 128 * u;
-                const int64_t t = tile % a.tt * NT + j;
-                load_scales(j < NT && t < a.T ? a.xs + t * kb : nullptr, grp, kb, a.vec, nb[u]);
+                const int t = g.t * NT + j;
+                load_scales(j < NT && t < a.T ? a.xs + (int64_t)t * kb : nullptr, grp, kb, a.vec, nb[u]);
             }
         };
-        Segment g(a);
-        if (g.more()) load_a(g.tile, g.k0 >> 2);
+        Segment<CG> g(a);
+        if (g.more()) load_a(g, g.k0 / PG);
         if (!XMX) pdl_wait();
-        if (g.more()) load_b(g.tile, g.k0 >> 2);
+        if (g.more()) load_b(g, g.k0 / PG);
         // a warp whose wait gave up goes on without waiting: the four share the barrier below
-        int it = 0, buf = 0;
+        int s = 0, buf = 0;
+        uint32_t par = 1;
         bool ok = true;
         for (; g.more(); g.next()) {
-            for (int grp = g.k0 >> 2; 4 * grp < g.k1; ++grp) {
+            for (int grp = g.k0 / PG; PG * grp < g.k1; ++grp) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     wa[i] = na[i];
@@ -283,17 +343,21 @@ __global__ void __launch_bounds__(L_THREADS, 1)
                     for (int u = 0; u < OWN; ++u) wb[u][i] = nb[u][i];
                 }
                 // the next group's, under way while this one's stages go through
-                if (4 * (grp + 1) < g.k1) {
-                    load_a(g.tile, grp + 1);
-                    load_b(g.tile, grp + 1);
+                if (PG * (grp + 1) < g.k1) {
+                    load_a(g, grp + 1);
+                    load_b(g, grp + 1);
                 } else {
-                    Segment n = g;
+                    Segment<CG> n = g;
                     n.next();
                     if (n.more()) {
-                        load_a(n.tile, 0);
-                        load_b(n.tile, 0);
+                        load_a(n, 0);
+                        load_b(n, 0);
                     }
                 }
+                uint32_t nan = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) nan |= __vcmpeq4(wa[i], 0xFFFFFFFFu);
+                if (nan) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 uint32_t* xb = xch + buf * 8 * NT;
                 if constexpr (C::XCH) {
 #pragma unroll
@@ -306,33 +370,31 @@ __global__ void __launch_bounds__(L_THREADS, 1)
                     buf ^= 1;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = 4 * grp + i;
+                for (int i = 0; i < PG; ++i) {
+                    const int k = PG * grp + i;
                     if (!ok || k < g.k0 || k >= g.k1) continue;
-                    const int s = it % S;
-                    if (!ptx::mbar_wait_warp(&empty[s], ((it / S) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
+                    if (!ptx::mbar_wait_all<PAIR>(&empty[s], par, abort_flag, L_WAIT_NS)) {
                         if (lane == 0) fail(4);
                         ok = false;
                         continue;
                     }
-                    if (__vcmpeq4(wa[2 * i], 0xFFFFFFFFu) | __vcmpeq4(wa[2 * i + 1], 0xFFFFFFFFu))
-                        latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
-                    const uint32_t col = tmem + lane_base + C::SF_COL0 + s * SF_SLOT;
-                    // row r is read at lane r mod 32 of this quarter, column col + q (a warp writes
-                    // its word into all four columns; the other quarters' are never read)
-                    ptx::tmem_st4_rep(col, wa[2 * i]);
-                    ptx::tmem_st4_rep(col + SF_A1, wa[2 * i + 1]);
-                    // column n of B: lane n mod 32 of every quarter, column + n / 32
+                    ptx::tc_fence_after();
+                    const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t to = col + SF_B0 + (SF_B1 - SF_B0) * h;
+                    for (int h = 0; h < WORDS; ++h) {
+                        const int w = WORDS * i + h;
+                        // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
+                        // word into all four columns; the other quarters' are never read)
+                        ptx::tmem_st4_rep(col + 16 * h, wa[w]);
+                        // column n of B: lane n mod 32 of every quarter, column + n / 32
+                        const uint32_t to = col + C::SF_B + 16 * h;
                         if constexpr (!C::XCH) {
-                            ptx::tmem_st4_rep(to, wb[0][2 * i + h]);
+                            ptx::tmem_st4_rep(to, wb[0][w]);
                         } else {
                             uint32_t v[NB / 32];
 #pragma unroll
                             for (int c = 0; c < NB / 32; ++c)
-                                v[c] = xb[(2 * i + h) * NT + (XMX ? 32 * c + lane : 16 * c + (lane >> 1))];
+                                v[c] = xb[w * NT + (C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1))];
                             if constexpr (NB == 64)
                                 ptx::tmem_st2(to, v[0], v[1]);
                             else if constexpr (NB == 128)
@@ -344,8 +406,11 @@ __global__ void __launch_bounds__(L_THREADS, 1)
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&full[s]);
-                    ++it;
+                    if (lane == 0) {
+                        if (PAIR) ptx::mbar_arrive_cluster(full0 + 8 * s);
+                        else ptx::mbar_arrive(&full[s]);
+                    }
+                    if (++s == S) s = 0, par ^= 1;
                 }
             }
         }
@@ -353,73 +418,118 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         // ------------------------------------------------------------ accumulators
         const int q = warp & 3, r = 32 * q + lane;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        const uint32_t acc_empty0 = PAIR ? ptx::map_cluster(acc_empty, 0) : 0;
         if (!XMX) pdl_wait();   // (the workspace's parts: an earlier call may still read its own)
         pdl_trigger();
-        int seg = 0;
-        for (Segment g(a); g.more(); g.next(), ++seg) {
-            const int ab = seg % ACC;
-            const bool got = ptx::mbar_wait_warp(&acc_full[ab], (seg / ACC) & 1, abort_flag, L_WAIT_NS);
-            if (!got && lane == 0) fail(5);
-            // the four warps decide together (they share barriers below)
-            if (threadIdx.x == 6 * 32) last_flag[1 + (seg & 1)] = *abort_flag;
-            ptx::named_bar_sync(2, 128);
-            if (last_flag[1 + (seg & 1)]) break;
-            ptx::tc_fence_after();
-            const int row = (int)(g.tile / a.tt) * LM + r, t0 = (int)(g.tile % a.tt) * NT;
-            const bool whole = g.k0 == 0 && g.k1 == g.nk;
-            float* part = a.parts + ((int64_t)blockIdx.x * 2 + (g.k0 == 0 ? 1 : 0)) * NT * LM + r;
-            const int n_tok = min(NT, a.T - t0);
-#pragma unroll 1
-            for (int c = 0; c < NB; c += 16) {
+        // G tokens' sums, a token's columns added
+        constexpr int G = C::EN < 32 ? C::EN : 32;
+        const int first = (warp - 6) / 4 * C::EN;       // this warp's tokens: EN from here
+        auto read = [&](int ab, int t, float (&y)[G]) {
+            const uint32_t from = tmem + lane_base + ab * NB + C::PER * t;
+            if constexpr (C::PER * G == 16) {
                 uint32_t v[16];
-                ptx::tmem_ld16(tmem + lane_base + ab * NB + c, v);
+                ptx::tmem_ld16(from, v);
                 ptx::tmem_ld_wait16(v);
 #pragma unroll
-                for (int j = 0; j < (XMX ? 16 : 8); ++j) {
-                    const int t = (XMX ? c : c / 2) + j;
-                    const float y = XMX ? __uint_as_float(v[j])
-                                        : __uint_as_float(v[2 * j]) + __uint_as_float(v[2 * j + 1]);
-                    if (t >= n_tok) continue;
-                    if (!whole)
-                        part[t * LM] = y;
-                    else if (row < a.N)
-                        a.out[(t0 + t) * a.out_stride + row] = __float2bfloat16_rn(y);
+                for (int j = 0; j < G; ++j)
+                    y[j] = C::PER == 1 ? __uint_as_float(v[j]) : __uint_as_float(v[2 * j]) + __uint_as_float(v[2 * j + 1]);
+            } else if constexpr (C::PER == 1) {
+                ptx::tmem_ld32(from, y);
+                ptx::tmem_ld_wait32(y);
+            } else {
+#pragma unroll
+                for (int b = 0; b < C::PER * G / 32; ++b) {
+                    float v[32];
+                    ptx::tmem_ld32(from + 32 * b, v);
+                    ptx::tmem_ld_wait32(v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[16 * b + j] = v[2 * j] + v[2 * j + 1];
                 }
             }
+        };
+        auto release = [&](int ab) {
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&acc_empty[ab]);
-            if (whole) continue;
-            // the tile's parts: those of CTAs c0 .. c1
-            const int64_t p0 = g.tile * g.nk;
-            const int c0 = holder_of(p0, a.total, gridDim.x), c1 = holder_of(p0 + g.nk - 1, a.total, gridDim.x);
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_cluster(acc_empty0 + 8 * ab);
+                else ptx::mbar_arrive(&acc_empty[ab]);
+            }
+        };
+        const int me = blockIdx.x / CG, workers = gridDim.x / CG;
+        int seg = 0;
+        for (Segment<CG> g(a); g.more(); g.next(), ++seg) {
+            const int ab = seg % ACC;
+            if (!ptx::mbar_wait_all<PAIR>(&acc_full[ab], (seg / ACC) & 1, abort_flag, L_WAIT_NS) && lane == 0) fail(5);
+            // the warps decide together (they share barriers below)
+            if (threadIdx.x == 6 * 32) last_flag[1 + (seg & 1)] = *abort_flag;
+            ptx::named_bar_sync(2, 32 * C::EW);
+            if (last_flag[1 + (seg & 1)]) break;
+            ptx::tc_fence_after();
+            const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * NT;
+            const int n_tok = min(NT, a.T - t0), mine = min(first + C::EN, n_tok);
+            if (g.k0 == 0 && g.k1 == g.nk) {
+                // out of TMEM first, so that the next tile's MMAs may begin
+                uint32_t y2[C::EN / 2];
+#pragma unroll
+                for (int t = 0; t < C::EN; t += G) {
+                    float y[G];
+                    read(ab, first + t, y);
+#pragma unroll
+                    for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
+                }
+                release(ab);
+                if (row < a.N) {
+                    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (t0 + first) * a.out_stride + row;
+#pragma unroll
+                    for (int t = 0; t < C::EN; t += 2) {
+                        if (first + t < mine) *to = (uint16_t)y2[t / 2];
+                        if (first + t + 1 < mine) to[a.out_stride] = (uint16_t)(y2[t / 2] >> 16);
+                        to += 2 * a.out_stride;
+                    }
+                }
+                continue;
+            }
+            constexpr int64_t PART = (int64_t)NT * LM;
+            auto part_of = [&](int c, int slot) { return a.parts + (((int64_t)c * CG + rank) * 2 + slot) * PART; };
+            float* part = part_of(me, g.k0 == 0) + r;
+#pragma unroll 1
+            for (int t = first; t < mine; t += G) {
+                float y[G];
+                read(ab, t, y);
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    if (t + j < mine) part[(t + j) * LM] = y[j];
+            }
+            release(ab);
+            // the tile's parts: those of workers c0 .. c1
+            const int64_t p0 = (int64_t)g.tile * g.nk;
+            const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + g.nk - 1, a.total, workers);
             __threadfence();
-            ptx::named_bar_sync(2, 128);
+            ptx::named_bar_sync(2, 32 * C::EW);
             if (threadIdx.x == 6 * 32) {
-                const uint32_t was = atomicAdd(&a.count[c0], 1u);
-                const bool last = was == (uint32_t)(c1 - c0);
-                if (last) a.count[c0] = 0;
+                uint32_t* count = a.count + c0 * CG + rank;
+                const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
+                if (last) *count = 0;
                 __threadfence();
                 last_flag[0] = last;
             }
-            ptx::named_bar_sync(2, 128);
+            ptx::named_bar_sync(2, 32 * C::EW);
             if (!last_flag[0]) continue;
             // four rows a lane, a token a warp at a time; J tokens' loads under way together
-            constexpr int J = NT / 4 < 8 ? NT / 4 : 8;
-            const int row4 = (int)(g.tile / a.tt) * LM + 4 * lane;
-            const float* p = a.parts + ((int64_t)c0 * 2 + 1) * NT * LM + 4 * lane;
+            constexpr int J = PAIR ? 4 : NT / C::EW < 8 ? NT / C::EW : 8;
+            const int row4 = row0 + 4 * lane;
 #pragma unroll 1
-            for (int tb = warp - 6; tb < n_tok; tb += 4 * J) {
+            for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
                 float4 y[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int c = c0; c <= c1; ++c) {
-                    const float* from = c == c0 ? p : p + ((int64_t)(c - c0) * 2 - 1) * NT * LM;
+                    const float* from = part_of(c, c == c0) + 4 * lane;
                     float4 v[J];
 #pragma unroll
                     for (int j = 0; j < J; ++j)
-                        v[j] = tb + 4 * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + 4 * j) * LM))
+                        v[j] = tb + C::EW * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + C::EW * j) * LM))
                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < J; ++j)
@@ -427,11 +537,11 @@ __global__ void __launch_bounds__(L_THREADS, 1)
                 }
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    if (tb + 4 * j < n_tok && row4 < a.N)
-                        *reinterpret_cast<uint2*>(a.out + (t0 + tb + 4 * j) * a.out_stride + row4) =
+                    if (tb + C::EW * j < n_tok && row4 < a.N)
+                        *reinterpret_cast<uint2*>(a.out + (t0 + tb + C::EW * j) * a.out_stride + row4) =
                             make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
             }
-            ptx::named_bar_sync(2, 128);   // the flag is written again
+            ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
         }
     }
     __syncthreads();
@@ -442,8 +552,12 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         while (ptx::globaltimer() - t0 < 200000ull) {
         }
     }
+    if (PAIR) ptx::cluster_sync_all();   // the other CTA reads this one's shared memory and arrives on its barriers
     ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    if (warp == 1) {
+        if (PAIR) ptx::tmem2_dealloc(tmem, 512);
+        else ptx::tmem_dealloc(tmem, 512);
+    }
 }
 
 // A bf16 x as two e4m3 terms a row (rows 2t and 2t + 1 of xq) and a scale byte a
@@ -471,12 +585,16 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16*
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Tokens a tile: the fewest that hold T, up to 256 (MXFP4 x) or 64.
-int tile_tokens(const MxDims& d) {
-    const int most = d.x_mx ? 256 : 64;
+// CTAs a tile, and tokens a tile: a pair and 256 with many tokens; else the fewest that hold T, up to 128 (MXFP4 x) or 64.
+struct Tiling {
+    int cg, nt;
+};
+Tiling tiling(const MxDims& d) {
+    if (d.T > 512) return {2, 256};
+    const int most = d.x_mx ? 128 : 64;
     int n = d.x_mx ? 16 : 8;
     while (n < most && n < d.T) n *= 2;
-    return d.x_mx && n == 32 ? 32 : n;
+    return {1, n};
 }
 
 constexpr int L_CTAS = 160;   // at most as many CTAs as the workspace has parts for
@@ -488,15 +606,15 @@ LLayout layout(const MxDims& d) {
     LLayout L;
     L.count = sizeof(StatusBlock);            // in the zeroed prefix
     L.parts = align256(WS_ZERO_PREFIX);
-    L.xq = L.parts + align256((size_t)L_CTAS * 2 * tile_tokens(d) * LM * 4);
+    L.xq = L.parts + align256((size_t)L_CTAS * 2 * tiling(d).nt * LM * 4);
     L.xs = L.xq + (d.x_mx ? 0 : align256((size_t)2 * d.T * d.K));
     L.total = L.xs + (d.x_mx ? 0 : align256((size_t)d.T * (d.K / 32)));
     return L;
 }
 
-template <bool XMX, int NT>
+template <bool XMX, int NT, int CG>
 cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
-    using C = LCfg<XMX, NT>;
+    using C = LCfg<XMX, NT, CG>;
     const LLayout L = layout(d);
     CUtensorMap tm_w, tm_x;
     const uint64_t N = d.N, T = d.T, K = d.K;
@@ -505,18 +623,21 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     if (XMX) {
         // packed rows of K / 2 bytes, 128 bytes (256 K) a stage
         const uint64_t w_d[2] = {K / 2, N}, x_d[2] = {K / 2, T}, s[1] = {K / 2};
-        const uint32_t w_b[2] = {128, LM}, x_b[2] = {128, (uint32_t)C::NB};
+        const uint32_t w_b[2] = {128, LM}, x_b[2] = {128, (uint32_t)C::B_ROWS};
         ok = make_map(&tm_w, U8, p.w, 2, w_d, s, w_b, CU_TENSOR_MAP_SWIZZLE_128B) &&
              make_map(&tm_x, U8, p.x, 2, x_d, s, x_b, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
-        // codes {128, N rows, K/128 slabs}; xq {128 bytes, 2T rows, K/128 slabs}
+        // codes {128, N rows, K/128 slabs}; xq {128 bytes, 2T rows, K/128 slabs}, or its terms apart
+        // {128 bytes, T rows, 2 terms, K/128 slabs}
         const uint64_t w_d[3] = {128, N, K / 128}, w_s[2] = {K / 2, 64}, x_d[3] = {128, 2 * T, K / 128}, x_s[2] = {K, 128};
-        const uint32_t w_b[3] = {128, LM, 2}, x_b[3] = {128, (uint32_t)C::NB, 2};
+        const uint64_t t_d[4] = {128, T, 2, K / 128}, t_s[3] = {2 * K, K, 128};
+        const uint32_t w_b[3] = {128, LM, C::WORDS}, x_b[3] = {128, (uint32_t)C::NB, 2}, t_b[4] = {128, (uint32_t)C::B_ROWS, 2, 1};
         ok = make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.w, 3, w_d, w_s, w_b, CU_TENSOR_MAP_SWIZZLE_128B) &&
-             make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B);
+             (CG == 2 ? make_map(&tm_x, U8, p.ws + L.xq, 4, t_d, t_s, t_b, CU_TENSOR_MAP_SWIZZLE_128B)
+                      : make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B));
     }
     if (!ok) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(k_mx_linear<XMX, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_mx_linear<XMX, NT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LArgs a;
     a.w_scales = p.w_scales;
@@ -529,9 +650,9 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     a.N = d.N;
     a.K = d.K;
     a.out_stride = d.out_stride;
-    a.nk = (d.K + LKS - 1) / LKS;
+    a.nk = (d.K + C::KS - 1) / C::KS;
     a.tt = (d.T + NT - 1) / NT;
-    a.total = (int64_t)((d.N + LM - 1) / LM) * a.tt * a.nk;
+    a.total = (int64_t)((d.N + CG * LM - 1) / (CG * LM)) * a.tt * a.nk;
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
     if (!XMX) {
@@ -542,10 +663,22 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
         timing_end(st);
         if (e != cudaSuccess) return e;
     }
-    const int sms = num_sms() < L_CTAS ? num_sms() : L_CTAS;
+    const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.total < workers ? a.total : workers) * CG);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
     timing_begin(K_MX_LINEAR, st);
-    e = launch_pdl(k_mx_linear<XMX, NT>, dim3((unsigned)(a.total < sms ? a.total : sms)), dim3(L_THREADS), C::SMEM, st, tm_w,
-                   tm_x, a);
+    e = cudaLaunchKernelEx(&cfg, k_mx_linear<XMX, NT, CG>, tm_w, tm_x, a);
     timing_end(st);
     return e;
 }
@@ -556,21 +689,22 @@ size_t mx_linear_ws_bytes(const MxDims& d) { return layout(d).total; }
 
 cudaError_t launch_mx_linear(const MxDims& d, const MxArgs& a, cudaStream_t st) {
     KT_BIND();
-    const int nt = tile_tokens(d);
+    const Tiling t = tiling(d);
     if (d.x_mx) {
-        switch (nt) {
-            case 16: return launch_tiles<true, 16>(d, a, st);
-            case 32: return launch_tiles<true, 32>(d, a, st);
-            case 64: return launch_tiles<true, 64>(d, a, st);
-            case 128: return launch_tiles<true, 128>(d, a, st);
-            default: return launch_tiles<true, 256>(d, a, st);
+        if (t.cg == 2) return launch_tiles<true, 256, 2>(d, a, st);
+        switch (t.nt) {
+            case 16: return launch_tiles<true, 16, 1>(d, a, st);
+            case 32: return launch_tiles<true, 32, 1>(d, a, st);
+            case 64: return launch_tiles<true, 64, 1>(d, a, st);
+            default: return launch_tiles<true, 128, 1>(d, a, st);
         }
     }
-    switch (nt) {
-        case 8: return launch_tiles<false, 8>(d, a, st);
-        case 16: return launch_tiles<false, 16>(d, a, st);
-        case 32: return launch_tiles<false, 32>(d, a, st);
-        default: return launch_tiles<false, 64>(d, a, st);
+    if (t.cg == 2) return launch_tiles<false, 256, 2>(d, a, st);
+    switch (t.nt) {
+        case 8: return launch_tiles<false, 8, 1>(d, a, st);
+        case 16: return launch_tiles<false, 16, 1>(d, a, st);
+        case 32: return launch_tiles<false, 32, 1>(d, a, st);
+        default: return launch_tiles<false, 64, 1>(d, a, st);
     }
 }
 
