@@ -12,9 +12,8 @@
 // 256 weight rows x 256 tokens, of which each holds half of either operand; the terms of
 // a bf16 x are two MMAs into one accumulator.
 //
-// All tiles stand one after the other on a line, cut into
-// stages of KS elements of K; each of the persistent CTAs (pairs) takes an equal share of
-// the line.  A tile that a cut divides is joined without waiting: every CTA writes its
+// The persistent CTAs (pairs) take whole tiles in turn; the last tiles stand one after the other on a
+// line, cut into stages of KS elements of K, of which each takes an equal share.  A tile that a cut divides is joined without waiting: every CTA writes its
 // part to the workspace and counts itself, and the one that comes last adds the
 // parts in the order of the line (so the sum does not depend on who came last).
 //
@@ -56,6 +55,8 @@ struct LCfg {
     static constexpr bool XCH = NB > 32;                          // token scales exchanged through shared memory
     static constexpr int XCH_BYTES = XCH ? 2 * 8 * NT * 4 : 0;
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
+    // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
+    // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
     static constexpr int S = S_FIT < S_TMEM ? S_FIT : S_TMEM;
     static constexpr int SMEM = 1024 + S * STAGE + XCH_BYTES + 512;
     static_assert(S >= 2 && SMEM <= 232448, "stages");
@@ -70,8 +71,9 @@ struct LArgs {
     StatusBlock* sb;
     int T, N, K;
     int64_t out_stride;
-    int nk, tt;                               // stages a tile, token tiles
-    int64_t total;                            // stages on the line
+    int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
+    int waves;                                // whole tiles that every worker takes first
+    int64_t total;                            // stages on the line, which begins behind those tiles
     int vec;                                  // scale rows are 16-byte aligned
     int w_once;
 };
@@ -80,32 +82,50 @@ struct LArgs {
 __device__ __forceinline__ int64_t share(int64_t total, int c, int n) { return total * c / n; }
 __device__ __forceinline__ int holder_of(int64_t p, int64_t total, int n) { return (int)(((p + 1) * n - 1) / total); }
 
-// A worker's segments: stages [k0, k1) of tile (m, t), one tile after the other (token tiles fastest).
+// A worker's segments: stages [k0, k1) of tile (m, t), one after the other: `waves` whole tiles, then its share
+// of the line.  Tiles are numbered through bands of GM weight tiles, so that those that are worked on at one
+// time share their rows of w and of x.
 template <int CG>
 struct Segment {
-    int64_t left;
-    int tile, m, t, k0, k1, nk, tt;
-    __device__ __forceinline__ explicit Segment(const LArgs& a) : nk(a.nk), tt(a.tt) {
+    static constexpr int GM = 8;
+    int64_t left;                // stages of the share to go
+    int tile, m, t, k0, k1, waves;
+    const LArgs& a;
+    __device__ __forceinline__ explicit Segment(const LArgs& args) : waves(args.waves), a(args) {
         const int c = blockIdx.x / CG, n = gridDim.x / CG;
         const int64_t at = share(a.total, c, n);
         left = share(a.total, c + 1, n) - at;
-        tile = (int)(at / nk);
-        m = tile / tt;
-        t = tile - m * tt;
-        k0 = (int)(at - (int64_t)tile * nk);
-        cut();
-    }
-    __device__ __forceinline__ void cut() { k1 = (int)min((int64_t)nk, k0 + left); }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next() {
-        left -= k1 - k0;
-        ++tile;
-        if (++t == tt) {
-            t = 0;
-            ++m;
-        }
+        tile = c;
         k0 = 0;
-        cut();
+        if (waves == 0) {
+            tile = (int)(at / a.nk);
+            k0 = (int)(at - (int64_t)tile * a.nk);
+        }
+        place();
+    }
+    __device__ __forceinline__ void place() {
+        k1 = waves > 0 ? a.nk : (int)min((int64_t)a.nk, k0 + left);
+        const int band = tile / (GM * a.tt), in = tile - band * GM * a.tt, gm = min(GM, a.mt - band * GM);
+        t = in / gm;
+        m = band * GM + in - t * gm;
+    }
+    __device__ __forceinline__ bool more() const { return waves > 0 || left > 0; }
+    __device__ __forceinline__ void next() {
+        const int n = gridDim.x / CG;
+        if (waves > 0) {
+            tile += n;
+            if (--waves == 0) {
+                const int64_t at = share(a.total, blockIdx.x / CG, n);
+                tile = (int)(at / a.nk);
+                k0 = (int)(at - (int64_t)tile * a.nk);
+                tile += a.waves * n;
+            }
+        } else {
+            left -= k1 - k0;
+            ++tile;
+            k0 = 0;
+        }
+        if (more()) place();
     }
 };
 
@@ -247,14 +267,14 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             bool ok = true;
             for (Segment<CG> g(a); ok && g.more(); g.next(), ++seg) {
                 const int ab = seg % ACC;
-                if (!ptx::mbar_wait_all<PAIR>(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
+                if (!ptx::mbar_wait_all(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
                     if (lane == 0) fail(2);
                     ok = false;
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem + ab * NB;
                 for (int k = g.k0; ok && k < g.k1; ++k) {
-                    if (!ptx::mbar_wait_all<PAIR>(&full[s], par, abort_flag, L_WAIT_NS)) {
+                    if (!ptx::mbar_wait_all(&full[s], par, abort_flag, L_WAIT_NS)) {
                         if (lane == 0) fail(3);
                         ok = false;
                         break;
@@ -304,7 +324,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             }
             __syncwarp();
         }
-        ptx::mbar_wait_all<PAIR>(fin, 0, abort_flag, L_WAIT_NS);
+        ptx::mbar_wait_all(fin, 0, abort_flag, L_WAIT_NS);
     } else if (warp < 6) {
         // ------------------------------------------------------------ scales
         const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row of this thread
@@ -373,7 +393,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 for (int i = 0; i < PG; ++i) {
                     const int k = PG * grp + i;
                     if (!ok || k < g.k0 || k >= g.k1) continue;
-                    if (!ptx::mbar_wait_all<PAIR>(&empty[s], par, abort_flag, L_WAIT_NS)) {
+                    if (!ptx::mbar_wait_all(&empty[s], par, abort_flag, L_WAIT_NS)) {
                         if (lane == 0) fail(4);
                         ok = false;
                         continue;
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         int seg = 0;
         for (Segment<CG> g(a); g.more(); g.next(), ++seg) {
             const int ab = seg % ACC;
-            if (!ptx::mbar_wait_all<PAIR>(&acc_full[ab], (seg / ACC) & 1, abort_flag, L_WAIT_NS) && lane == 0) fail(5);
+            if (!ptx::mbar_wait_all(&acc_full[ab], (seg / ACC) & 1, abort_flag, L_WAIT_NS) && lane == 0) fail(5);
             // the warps decide together (they share barriers below)
             if (threadIdx.x == 6 * 32) last_flag[1 + (seg & 1)] = *abort_flag;
             ptx::named_bar_sync(2, 32 * C::EW);
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::tc_fence_after();
             const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * NT;
             const int n_tok = min(NT, a.T - t0), mine = min(first + C::EN, n_tok);
-            if (g.k0 == 0 && g.k1 == g.nk) {
+            if (g.k0 == 0 && g.k1 == a.nk) {
                 // out of TMEM first, so that the next tile's MMAs may begin
                 uint32_t y2[C::EN / 2];
 #pragma unroll
@@ -478,14 +498,17 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                     for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
                 }
                 release(ab);
-                if (row < a.N) {
-                    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (t0 + first) * a.out_stride + row;
+                // lanes 2i and 2i + 1 exchange, so that each stores both rows of one of two tokens (2-byte
+                // stores: T = 8192, N = 14336, K = 7168 in 311 us against 289; rows of 256 bytes through shared
+                // memory: 330, by TMA: 371)
+                const int odd = lane & 1;
+                uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (t0 + first + odd) * a.out_stride + row - odd;
 #pragma unroll
-                    for (int t = 0; t < C::EN; t += 2) {
-                        if (first + t < mine) *to = (uint16_t)y2[t / 2];
-                        if (first + t + 1 < mine) to[a.out_stride] = (uint16_t)(y2[t / 2] >> 16);
-                        to += 2 * a.out_stride;
-                    }
+                for (int t = 0; t < C::EN; t += 2) {
+                    const uint32_t v = y2[t / 2], u = __shfl_xor_sync(0xffffffffu, v, 1);
+                    if (first + t + odd < mine && row < a.N)
+                        *reinterpret_cast<uint32_t*>(to) = odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
+                    to += 2 * a.out_stride;
                 }
                 continue;
             }
@@ -502,8 +525,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             }
             release(ab);
             // the tile's parts: those of workers c0 .. c1
-            const int64_t p0 = (int64_t)g.tile * g.nk;
-            const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + g.nk - 1, a.total, workers);
+            const int64_t p0 = (int64_t)(g.tile - a.waves * workers) * a.nk;
+            const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + a.nk - 1, a.total, workers);
             __threadfence();
             ptx::named_bar_sync(2, 32 * C::EW);
             if (threadIdx.x == 6 * 32) {
@@ -652,7 +675,15 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     a.out_stride = d.out_stride;
     a.nk = (d.K + C::KS - 1) / C::KS;
     a.tt = (d.T + NT - 1) / NT;
-    a.total = (int64_t)((d.N + CG * LM - 1) / (CG * LM)) * a.tt * a.nk;
+    a.mt = (d.N + CG * LM - 1) / (CG * LM);
+    const int64_t tiles = (int64_t)a.mt * a.tt;
+    int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
+    if (tiles * a.nk < workers) workers = (int)(tiles * a.nk);
+    // whole tiles first; the line takes what is left over and one round more, so that a cut
+    // tile has at most three parts
+    a.waves = (int)(tiles / workers);
+    if (a.waves > 0 && tiles % workers) --a.waves;
+    a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
     if (!XMX) {
@@ -663,9 +694,8 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
         timing_end(st);
         if (e != cudaSuccess) return e;
     }
-    const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.total < workers ? a.total : workers) * CG);
+    cfg.gridDim = dim3((unsigned)(workers * CG));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;

@@ -376,35 +376,23 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// The cluster address of `p`'s place in CTA `rank`, an arrival there, and a wait that sees what
-// another CTA's arrival released (bounded like mbar_wait_warp).
+// The cluster address of `p`'s place in CTA `rank`, and an arrival there.  What the arrivals of a pair's
+// kernel announce are accesses to TMEM that have completed (tcgen05.wait) before it; a release at cluster
+// scope would wait for every load under way as well.
 __device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Warp-uniform wait, the clock read only where the phase is not complete at once.
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_wait_all(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
-    auto test = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (__all_sync(0xffffffffu, test())) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, test())) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if ((it & 15u) == 0u) {
             const bool stop = (*abort != 0) || (globaltimer() - t0 > limit_ns);
             if (__shfl_sync(0xffffffffu, (int)stop, 0)) return false;
