@@ -52,8 +52,10 @@ struct LCfg {
     static constexpr int SF_SLOT = WORDS * 32, SF_B = WORDS * 16;
     static constexpr int SF_COL0 = (ACC * NB + 63) / 64 * 64;
     static constexpr int S_TMEM = (512 - SF_COL0) / SF_SLOT;
-    static constexpr bool XCH = NB > 32;                          // token scales exchanged through shared memory
-    static constexpr int XCH_BYTES = XCH ? 2 * 8 * NT * 4 : 0;
+    // scales on their way to TMEM: a pair's token scales of 1024 K, exchanged between threads, twice; else RING
+    // groups of 512 K, a row of weights or tokens 16 bytes
+    static constexpr int RING = 4;
+    static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16;
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
     // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint32_t* xch = reinterpret_cast<uint32_t*>(sm + S * C::STAGE);     // [2][8 words][NT] token scales
+    uint8_t* xch = sm + S * C::STAGE;    // scales: a pair's [2][8 words][NT] words, else [RING][LM + NT] rows
     // a pair's stages are counted on the even CTA's `full`, and its MMAs' ends on both CTAs' barriers
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S * C::STAGE + C::XCH_BYTES);
     uint64_t* empty = full + S;          // the stage's MMAs are done
@@ -325,14 +327,14 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             __syncwarp();
         }
         ptx::mbar_wait_all(fin, 0, abort_flag, L_WAIT_NS);
-    } else if (warp < 6) {
-        // ------------------------------------------------------------ scales
+    } else if (warp < 6 && PAIR) {
+        // ------------------------------------------------------------ scales, of a pair: a group of 1024 K ahead in registers
         const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row of this thread
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int kb = a.K / 32;
         constexpr int PG = 8 / WORDS;                                 // stages of a group of 1024 K
-        constexpr int OWN = !C::XCH ? 1 : NT > 128 ? NT / 128 : 1;    // tokens whose scales this thread loads
-        const uint32_t full0 = PAIR ? ptx::map_cluster(full, 0) : 0;
+        constexpr int OWN = NT >= 128 ? NT / 128 : 1;                 // tokens whose scales this thread loads
+        const uint32_t full0 = ptx::map_cluster(full, 0);
         uint32_t wa[8], wb[OWN][8], na[8], nb[OWN][8];
         auto load_a = [&](const Segment<CG>& g, int grp) {
             const int row = (g.m * CG + rank) * LM + r;
@@ -341,9 +343,9 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         auto load_b = [&](const Segment<CG>& g, int grp) {
 #pragma unroll
             for (int u = 0; u < OWN; ++u) {
-                const int j = !C::XCH ? (XMX ? lane : lane >> 1) % NT : r + 128 * u;
+                const int j = r + 128 * u;
                 const int t = g.t * NT + j;
-                load_scales(j < NT && t < a.T ? a.xs + (int64_t)t * kb : nullptr, grp, kb, a.vec, nb[u]);
+                load_scales(t < a.T ? a.xs + (int64_t)t * kb : nullptr, grp, kb, a.vec, nb[u]);
             }
         };
         Segment<CG> g(a);
@@ -378,17 +380,14 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) nan |= __vcmpeq4(wa[i], 0xFFFFFFFFu);
                 if (nan) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
-                uint32_t* xb = xch + buf * 8 * NT;
-                if constexpr (C::XCH) {
+                uint32_t* xb = reinterpret_cast<uint32_t*>(xch) + buf * 8 * NT;
 #pragma unroll
-                    for (int u = 0; u < OWN; ++u)
-                        if (r + 128 * u < NT)
+                for (int u = 0; u < OWN; ++u)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) xb[i * NT + r + 128 * u] = wb[u][i];
-                    // (one barrier a group: a buffer is written again two groups later)
-                    ptx::named_bar_sync(1, 128);
-                    buf ^= 1;
-                }
+                    for (int i = 0; i < 8; ++i) xb[i * NT + r + 128 * u] = wb[u][i];
+                // (one barrier a group: a buffer is written again two groups later)
+                ptx::named_bar_sync(1, 128);
+                buf ^= 1;
 #pragma unroll
                 for (int i = 0; i < PG; ++i) {
                     const int k = PG * grp + i;
@@ -408,32 +407,127 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                         ptx::tmem_st4_rep(col + 16 * h, wa[w]);
                         // column n of B: lane n mod 32 of every quarter, column + n / 32
                         const uint32_t to = col + C::SF_B + 16 * h;
-                        if constexpr (!C::XCH) {
-                            ptx::tmem_st4_rep(to, wb[0][w]);
-                        } else {
-                            uint32_t v[NB / 32];
+                        uint32_t v[8];
 #pragma unroll
-                            for (int c = 0; c < NB / 32; ++c)
-                                v[c] = xb[w * NT + (C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1))];
-                            if constexpr (NB == 64)
-                                ptx::tmem_st2(to, v[0], v[1]);
-                            else if constexpr (NB == 128)
-                                ptx::tmem_st4(to, v[0], v[1], v[2], v[3]);
-                            else
-                                ptx::tmem_st8(to, v);
-                        }
+                        for (int c = 0; c < 8; ++c) v[c] = xb[w * NT + 32 * c + lane];
+                        ptx::tmem_st8(to, v);
                     }
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) ptx::mbar_arrive_cluster(full0 + 8 * s);
-                        else ptx::mbar_arrive(&full[s]);
-                    }
+                    if (lane == 0) ptx::mbar_arrive_cluster(full0 + 8 * s);
                     if (++s == S) s = 0, par ^= 1;
                 }
             }
         }
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ scales: RING - 1 groups of 512 K ahead in shared memory
+        const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row and token of this thread
+        const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        const int kb = a.K / 32;
+        constexpr int RING = C::RING;
+        // 16 scale bytes of a row; zeros past the tensor's ends, where the codes are zeros too
+        auto fetch = [&](const uint8_t* src, bool in, int grp, uint8_t* dst) {
+            src += 16 * grp;
+            if (a.vec) {
+                ptx::cp_async_16(dst, src, in ? 16 : 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<uint32_t*>(dst)[i] =
+                        in && 16 * grp + 4 * i < kb ? ld_dep(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+            }
+        };
+        auto fetch_a = [&](const Segment<CG>& g, int grp, int buf) {
+            const int row = g.m * LM + r;
+            fetch(a.w_scales + (int64_t)min(row, a.N - 1) * kb, row < a.N, grp, xch + (buf * (LM + NT) + r) * 16);
+        };
+        auto fetch_b = [&](const Segment<CG>& g, int grp, int buf) {
+            const int t = g.t * NT + r;
+            if (r < NT) fetch(a.xs + (int64_t)min(t, a.T - 1) * kb, t < a.T, grp, xch + (buf * (LM + NT) + LM + r) * 16);
+        };
+        auto advance = [&](Segment<CG>& g, int& grp) {
+            if (2 * ++grp >= g.k1) {
+                g.next();
+                grp = 0;
+            }
+        };
+        Segment<CG> g(a), ahead = g;
+        int grp = g.k0 / 2, agrp = grp;
+        if (!XMX) {
+            // the weights' scales, inputs of the call, before the wait for the tokens'
+            Segment<CG> n = g;
+            int ngrp = grp;
+#pragma unroll 1
+            for (int i = 0; i < RING - 1 && n.more(); ++i, advance(n, ngrp)) fetch_a(n, ngrp, i);
+            pdl_wait();
+        }
+#pragma unroll 1
+        for (int i = 0; i < RING - 1; ++i) {
+            if (ahead.more()) {
+                if (XMX) fetch_a(ahead, agrp, i);
+                fetch_b(ahead, agrp, i);
+                advance(ahead, agrp);
+            }
+            ptx::cp_async_commit();
+        }
+        // a warp whose wait gave up goes on without waiting: the four share the barrier below
+        int s = 0, buf = 0;
+        uint32_t par = 1;
+        bool ok = true;
+#pragma unroll 1
+        for (; g.more(); advance(g, grp), buf = (buf + 1) % RING) {
+            ptx::cp_async_wait<RING - 2>();
+            ptx::named_bar_sync(1, 128);
+            // (behind the barrier every warp is done with the group before this one)
+            if (ahead.more()) {
+                fetch_a(ahead, agrp, (buf + RING - 1) % RING);
+                fetch_b(ahead, agrp, (buf + RING - 1) % RING);
+                advance(ahead, agrp);
+            }
+            ptx::cp_async_commit();
+            const uint8_t* rows = xch + buf * (LM + NT) * 16;
+#pragma unroll 1
+            for (int k = max(2 * grp, g.k0); ok && k < min(2 * grp + 2, g.k1); ++k) {
+                const uint2 w = *reinterpret_cast<const uint2*>(rows + 16 * r + 8 * (k & 1));
+                if (__vcmpeq4(w.x, 0xFFFFFFFFu) | __vcmpeq4(w.y, 0xFFFFFFFFu)) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
+                uint2 v[(NB + 31) / 32];
+#pragma unroll
+                for (int c = 0; c < (NB + 31) / 32; ++c) {
+                    const int t = C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1);
+                    v[c] = *reinterpret_cast<const uint2*>(rows + 16 * (LM + t % NT) + 8 * (k & 1));
+                }
+                if (!ptx::mbar_wait_all(&empty[s], par, abort_flag, L_WAIT_NS)) {
+                    if (lane == 0) fail(4);
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
+                // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
+                // word into all four columns; the other quarters' are never read)
+                ptx::tmem_st4_rep(col, w.x);
+                ptx::tmem_st4_rep(col + 16, w.y);
+                // column n of B: lane n mod 32 of every quarter, column + n / 32
+                const uint32_t to = col + C::SF_B;
+                if constexpr (NB <= 32) {
+                    ptx::tmem_st4_rep(to, v[0].x);
+                    ptx::tmem_st4_rep(to + 16, v[0].y);
+                } else if constexpr (NB == 64) {
+                    ptx::tmem_st2(to, v[0].x, v[1].x);
+                    ptx::tmem_st2(to + 16, v[0].y, v[1].y);
+                } else if constexpr (NB == 128) {
+                    ptx::tmem_st4(to, v[0].x, v[1].x, v[2].x, v[3].x);
+                    ptx::tmem_st4(to + 16, v[0].y, v[1].y, v[2].y, v[3].y);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&full[s]);
+                if (++s == S) s = 0, par ^= 1;
+            }
+        }
+        ptx::cp_async_wait<0>();
     } else {
         // ------------------------------------------------------------ accumulators
         const int q = warp & 3, r = 32 * q + lane;
@@ -488,27 +582,38 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * NT;
             const int n_tok = min(NT, a.T - t0), mine = min(first + C::EN, n_tok);
             if (g.k0 == 0 && g.k1 == a.nk) {
-                // out of TMEM first, so that the next tile's MMAs may begin
-                uint32_t y2[C::EN / 2];
-#pragma unroll
-                for (int t = 0; t < C::EN; t += G) {
-                    float y[G];
-                    read(ab, first + t, y);
-#pragma unroll
-                    for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
-                }
-                release(ab);
                 // lanes 2i and 2i + 1 exchange, so that each stores both rows of one of two tokens (2-byte
                 // stores: T = 8192, N = 14336, K = 7168 in 311 us against 289; rows of 256 bytes through shared
                 // memory: 330, by TMA: 371)
                 const int odd = lane & 1;
-                uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (t0 + first + odd) * a.out_stride + row - odd;
-#pragma unroll
-                for (int t = 0; t < C::EN; t += 2) {
-                    const uint32_t v = y2[t / 2], u = __shfl_xor_sync(0xffffffffu, v, 1);
+                auto store = [&](int t, uint32_t v) {
+                    const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
                     if (first + t + odd < mine && row < a.N)
-                        *reinterpret_cast<uint32_t*>(to) = odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
-                    to += 2 * a.out_stride;
+                        *reinterpret_cast<uint32_t*>(a.out + (t0 + first + t + odd) * a.out_stride + row - odd) =
+                            odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
+                };
+                if constexpr (PAIR) {
+                    // its one accumulator is read out first, so that the next tile's MMAs may begin
+                    uint32_t y2[C::EN / 2];
+#pragma unroll
+                    for (int t = 0; t < C::EN; t += G) {
+                        float y[G];
+                        read(ab, first + t, y);
+#pragma unroll
+                        for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
+                    }
+                    release(ab);
+#pragma unroll
+                    for (int t = 0; t < C::EN; t += 2) store(t, y2[t / 2]);
+                } else {
+#pragma unroll 1
+                    for (int t = 0; t < n_tok; t += G) {
+                        float y[G];
+                        read(ab, t, y);
+#pragma unroll
+                        for (int j = 0; j < G; j += 2) store(t + j, ptx::cvt_bf16x2(y[j], y[j + 1]));
+                    }
+                    release(ab);
                 }
                 continue;
             }
@@ -539,14 +644,14 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::named_bar_sync(2, 32 * C::EW);
             if (!last_flag[0]) continue;
             // four rows a lane, a token a warp at a time; J tokens' loads under way together
-            constexpr int J = PAIR ? 4 : NT / C::EW < 8 ? NT / C::EW : 8;
+            constexpr int J = PAIR ? 4 : NT / C::EW < 16 ? NT / C::EW : 16;
             const int row4 = row0 + 4 * lane;
 #pragma unroll 1
             for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
                 float4 y[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
                 for (int c = c0; c <= c1; ++c) {
                     const float* from = part_of(c, c == c0) + 4 * lane;
                     float4 v[J];
