@@ -12,16 +12,23 @@
 // 256 weight rows x 256 tokens, of which each holds half of either operand; the terms of
 // a bf16 x are two MMAs into one accumulator.
 //
-// The persistent CTAs (pairs) take whole tiles in turn; the last tiles stand one after the other on a
-// line, cut into stages of KS elements of K, of which each takes an equal share.  A tile that a cut divides is joined without waiting: every CTA writes its
-// part to the workspace and counts itself, and the one that comes last adds the
-// parts in the order of the line (so the sum does not depend on who came last).
+// How the tiles' stages (KS elements of K) are shared out:
+//   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; the parts are
+//     added through the cluster's shared memory;
+//   - else the persistent CTAs (pairs) take whole tiles in turn;
+//   - where a last round of them would leave much idle, the last tiles stand one after the other on a
+//     line of which every CTA (pair) takes an equal share.  A tile that a cut divides is
+//     joined without waiting: every CTA writes its part to the workspace and counts itself,
+//     and the one that comes last adds the parts in the order of the line (so the sum does
+//     not depend on who came last).
 //
 // Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> TMEM, 1024 K ahead in
 // registers), 6 on the accumulators' way out: four, or eight of a pair's CTA.
 #include "mx.cuh"
 #include "quant.cuh"
 #include "tc_ptx.cuh"
+
+#include <atomic>
 
 namespace moe {
 namespace {
@@ -74,8 +81,9 @@ struct LArgs {
     int T, N, K;
     int64_t out_stride;
     int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
-    int waves;                                // whole tiles that every worker takes first
-    int64_t total;                            // stages on the line, which begins behind those tiles
+    int split;                                // CTAs of a cluster that share a tile, or 1
+    int tiles, waves;                         // whole tiles that every worker takes first, if there is a line
+    int64_t total;                            // stages on the line, which begins behind those tiles, or 0
     int vec;                                  // scale rows are 16-byte aligned
     int w_once;
 };
@@ -93,17 +101,29 @@ struct Segment {
     int64_t left;                // stages of the share to go
     int tile, m, t, k0, k1, waves;
     const LArgs& a;
-    __device__ __forceinline__ explicit Segment(const LArgs& args) : waves(args.waves), a(args) {
+    __device__ __forceinline__ explicit Segment(const LArgs& args) : left(0), waves(args.waves), a(args) {
         const int c = blockIdx.x / CG, n = gridDim.x / CG;
-        const int64_t at = share(a.total, c, n);
-        left = share(a.total, c + 1, n) - at;
         tile = c;
         k0 = 0;
-        if (waves == 0) {
-            tile = (int)(at / a.nk);
-            k0 = (int)(at - (int64_t)tile * a.nk);
+        if (a.split > 1) {
+            const int part = c % a.split;
+            tile = c / a.split;
+            waves = 0;
+            k0 = a.nk * part / a.split;
+            left = a.nk * (part + 1) / a.split - k0;
+        } else if (a.total == 0) {
+            waves = (a.tiles - c + n - 1) / n;
+        } else {
+            const int64_t at = share(a.total, c, n);
+            left = share(a.total, c + 1, n) - at;
+            if (waves == 0) to_line(at);
         }
         place();
+    }
+    __device__ __forceinline__ void to_line(int64_t at) {
+        tile = (int)(at / a.nk);
+        k0 = (int)(at - (int64_t)tile * a.nk);
+        tile += a.waves * (gridDim.x / CG);
     }
     __device__ __forceinline__ void place() {
         k1 = waves > 0 ? a.nk : (int)min((int64_t)a.nk, k0 + left);
@@ -116,12 +136,7 @@ struct Segment {
         const int n = gridDim.x / CG;
         if (waves > 0) {
             tile += n;
-            if (--waves == 0) {
-                const int64_t at = share(a.total, blockIdx.x / CG, n);
-                tile = (int)(at / a.nk);
-                k0 = (int)(at - (int64_t)tile * a.nk);
-                tile += a.waves * n;
-            }
+            if (--waves == 0 && a.total > 0) to_line(share(a.total, blockIdx.x / CG, n));
         } else {
             left -= k1 - k0;
             ++tile;
@@ -581,6 +596,20 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::tc_fence_after();
             const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * NT;
             const int n_tok = min(NT, a.T - t0), mine = min(first + C::EN, n_tok);
+            if constexpr (!PAIR) {
+                if (a.split > 1) {
+                    // the CTA's part into its own shared memory, whose stages are done with
+                    float* part = reinterpret_cast<float*>(sm) + r;
+#pragma unroll 1
+                    for (int t = 0; t < n_tok; t += G) {
+                        float y[G];
+                        read(ab, t, y);
+#pragma unroll
+                        for (int j = 0; j < G; ++j) part[(t + j) * LM] = y[j];
+                    }
+                    break;
+                }
+            }
             if (g.k0 == 0 && g.k1 == a.nk) {
                 // lanes 2i and 2i + 1 exchange, so that each stores both rows of one of two tokens (2-byte
                 // stores: T = 8192, N = 14336, K = 7168 in 311 us against 289; rows of 256 bytes through shared
@@ -672,6 +701,31 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
         }
     }
+    if constexpr (!PAIR) {
+        if (a.split > 1) {
+            // the cluster's parts, added in the order of K: CTA c of it takes the c-th share of the tokens
+            ptx::cluster_sync_all();
+            const int c = blockIdx.x % a.split;
+            const Segment<CG> g(a);
+            const int row0 = g.m * LM, t0 = g.t * NT, n_tok = min(NT, a.T - t0);
+            const int u0 = n_tok * c / a.split, u1 = n_tok * (c + 1) / a.split;
+            for (int i = threadIdx.x; i < (u1 - u0) * 32; i += C::THREADS) {
+                const int t = u0 + (i >> 5), row = 4 * (i & 31);
+                const float* at = reinterpret_cast<const float*>(sm) + t * LM + row;
+                float4 v[8];
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    v[p] = p < a.split ? ptx::ld_cluster(ptx::map_cluster(at, p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 y = v[0];
+#pragma unroll
+                for (int p = 1; p < 8; ++p) y.x += v[p].x, y.y += v[p].y, y.z += v[p].z, y.w += v[p].w;
+                if (row0 + row < a.N)
+                    *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + row0 + row) =
+                        make_uint2(ptx::cvt_bf16x2(y.x, y.y), ptx::cvt_bf16x2(y.z, y.w));
+            }
+            ptx::cluster_sync_all();   // every CTA keeps its part until the others have read it
+        }
+    }
     __syncthreads();
     KT_MARK(K_MX_LINEAR, 2);
     if (*abort_flag) {
@@ -740,6 +794,34 @@ LLayout layout(const MxDims& d) {
     return L;
 }
 
+// How many clusters of `size` such CTAs (one an SM) run at once on the current device (a GB300: 76 of two, 46 of
+// three, 36 of four, 28 of five, 23 of six, 15 of eight), asked once.
+int clusters_at_once(const void* kernel, int threads, int smem, int size) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev][size];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = -1;
+        }
+        known[dev][size] = n;
+    }
+    return n;
+}
+
 template <bool XMX, int NT, int CG>
 cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     using C = LCfg<XMX, NT, CG>;
@@ -782,13 +864,28 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     a.tt = (d.T + NT - 1) / NT;
     a.mt = (d.N + CG * LM - 1) / (CG * LM);
     const int64_t tiles = (int64_t)a.mt * a.tt;
-    int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
-    if (tiles * a.nk < workers) workers = (int)(tiles * a.nk);
-    // whole tiles first; the line takes what is left over and one round more, so that a cut
-    // tile has at most three parts
-    a.waves = (int)(tiles / workers);
-    if (a.waves > 0 && tiles % workers) --a.waves;
-    a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
+    const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
+    a.tiles = (int)tiles;
+    a.split = 1;
+    a.waves = 0;
+    a.total = 0;
+    int ctas = (int)(tiles < workers ? tiles : workers);
+    if (CG == 1)
+        for (int n = 2; n <= 8 && n <= a.nk && n * tiles <= workers; ++n)
+            if (tiles <= clusters_at_once((const void*)k_mx_linear<XMX, NT, CG>, C::THREADS, C::SMEM, n)) a.split = n;
+    if (a.split > 1) {
+        ctas *= a.split;
+    } else if (tiles % workers) {
+        // a last round of whole tiles, or the line: it takes what is left over and one round more, so that a cut
+        // tile has at most three parts, and its joins take as long as LINE stages
+        constexpr int LINE = 10;
+        const int64_t rounds = tiles / workers + 1;
+        if (rounds * a.nk * workers > tiles * a.nk + (int64_t)LINE * workers) {
+            a.waves = rounds >= 2 ? (int)rounds - 2 : 0;
+            a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
+            ctas = workers;
+        }
+    }
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
     if (!XMX) {
@@ -800,7 +897,7 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(workers * CG));
+    cfg.gridDim = dim3((unsigned)(ctas * CG));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
@@ -808,10 +905,10 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = CG * a.split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
+    cfg.numAttrs = CG * a.split > 1 ? 2 : 1;
     timing_begin(K_MX_LINEAR, st);
     e = cudaLaunchKernelEx(&cfg, k_mx_linear<XMX, NT, CG>, tm_w, tm_x, a);
     timing_end(st);
