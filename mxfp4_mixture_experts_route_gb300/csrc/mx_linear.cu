@@ -29,9 +29,13 @@
 #include "tc_ptx.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace moe {
 namespace {
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 constexpr int LM = 128;                       // weight rows a CTA
 constexpr uint64_t L_WAIT_NS = 2000000000ull;
@@ -60,7 +64,8 @@ struct LCfg {
     static constexpr int SF_COL0 = (ACC * NB + 63) / 64 * 64;
     static constexpr int S_TMEM = (512 - SF_COL0) / SF_SLOT;
     // scales on their way to TMEM: a pair's token scales of 1024 K, exchanged between threads, twice; else RING
-    // groups of 512 K, a row of weights or tokens 16 bytes
+    // groups of 512 K, a row of weights or tokens 16 bytes (or half as many of twice the bytes, where the rows in
+    // memory are not 16-byte aligned: the two aligned pieces that hold them)
     static constexpr int RING = 4;
     static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16;
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
@@ -440,26 +445,32 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row and token of this thread
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int kb = a.K / 32;
-        constexpr int RING = C::RING;
-        // 16 scale bytes of a row; zeros past the tensor's ends, where the codes are zeros too
-        auto fetch = [&](const uint8_t* src, bool in, int grp, uint8_t* dst) {
-            src += 16 * grp;
+        const int ring = a.vec ? C::RING : C::RING / 2, bytes = a.vec ? 16 : 32;
+        // a group's scale bytes of row `n` of `rows`; zeros past the tensor's ends, where the codes are zeros too
+        auto fetch = [&](const uint8_t* src, int n, int rows, int grp, uint8_t* dst) {
+            const int64_t at = (int64_t)min(n, rows - 1) * kb + 16 * grp, end = (int64_t)rows * kb;
             if (a.vec) {
-                ptx::cp_async_16(dst, src, in ? 16 : 0);
+                ptx::cp_async_16(dst, src + at, n < rows ? 16 : 0);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    reinterpret_cast<uint32_t*>(dst)[i] =
-                        in && 16 * grp + 4 * i < kb ? ld_dep(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t p = (at & ~(int64_t)15) + 16 * i;
+                    ptx::cp_async_16(dst + 16 * i, src + min(p, end & ~(int64_t)15),
+                                     n < rows ? (uint32_t)max((int64_t)0, min((int64_t)16, end - p)) : 0u);
+                }
             }
         };
+        // its 8 bytes of stage k; a row's bytes past K (of the next row, or zeros) meet codes that are zeros
+        auto words = [&](const uint8_t* p, int n, int rows, int k) {
+            if (a.vec) return *reinterpret_cast<const uint2*>(p + 8 * (k & 1));
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p + ((int64_t)min(n, rows - 1) * kb & 15) + 8 * (k & 1));
+            return make_uint2(w[0], 8 * k + 4 < kb ? w[1] : 0u);
+        };
         auto fetch_a = [&](const Segment<CG>& g, int grp, int buf) {
-            const int row = g.m * LM + r;
-            fetch(a.w_scales + (int64_t)min(row, a.N - 1) * kb, row < a.N, grp, xch + (buf * (LM + NT) + r) * 16);
+            fetch(a.w_scales, g.m * LM + r, a.N, grp, xch + (buf * (LM + NT) + r) * bytes);
         };
         auto fetch_b = [&](const Segment<CG>& g, int grp, int buf) {
-            const int t = g.t * NT + r;
-            if (r < NT) fetch(a.xs + (int64_t)min(t, a.T - 1) * kb, t < a.T, grp, xch + (buf * (LM + NT) + LM + r) * 16);
+            if (r < NT) fetch(a.xs, g.t * NT + r, a.T, grp, xch + (buf * (LM + NT) + LM + r) * bytes);
         };
         auto advance = [&](Segment<CG>& g, int& grp) {
             if (2 * ++grp >= g.k1) {
@@ -474,11 +485,11 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             Segment<CG> n = g;
             int ngrp = grp;
 #pragma unroll 1
-            for (int i = 0; i < RING - 1 && n.more(); ++i, advance(n, ngrp)) fetch_a(n, ngrp, i);
+            for (int i = 0; i < ring - 1 && n.more(); ++i, advance(n, ngrp)) fetch_a(n, ngrp, i);
             pdl_wait();
         }
 #pragma unroll 1
-        for (int i = 0; i < RING - 1; ++i) {
+        for (int i = 0; i < ring - 1; ++i) {
             if (ahead.more()) {
                 if (XMX) fetch_a(ahead, agrp, i);
                 fetch_b(ahead, agrp, i);
@@ -491,26 +502,28 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         uint32_t par = 1;
         bool ok = true;
 #pragma unroll 1
-        for (; g.more(); advance(g, grp), buf = (buf + 1) % RING) {
-            ptx::cp_async_wait<RING - 2>();
+        for (; g.more(); advance(g, grp), buf = buf + 1 == ring ? 0 : buf + 1) {
+            if (a.vec) ptx::cp_async_wait<C::RING - 2>();
+            else ptx::cp_async_wait<C::RING / 2 - 2>();
             ptx::named_bar_sync(1, 128);
             // (behind the barrier every warp is done with the group before this one)
             if (ahead.more()) {
-                fetch_a(ahead, agrp, (buf + RING - 1) % RING);
-                fetch_b(ahead, agrp, (buf + RING - 1) % RING);
+                const int to = buf == 0 ? ring - 1 : buf - 1;
+                fetch_a(ahead, agrp, to);
+                fetch_b(ahead, agrp, to);
                 advance(ahead, agrp);
             }
             ptx::cp_async_commit();
-            const uint8_t* rows = xch + buf * (LM + NT) * 16;
+            const uint8_t* rows = xch + buf * (LM + NT) * bytes;
 #pragma unroll 1
             for (int k = max(2 * grp, g.k0); ok && k < min(2 * grp + 2, g.k1); ++k) {
-                const uint2 w = *reinterpret_cast<const uint2*>(rows + 16 * r + 8 * (k & 1));
+                const uint2 w = words(rows + bytes * r, g.m * LM + r, a.N, k);
                 if (__vcmpeq4(w.x, 0xFFFFFFFFu) | __vcmpeq4(w.y, 0xFFFFFFFFu)) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 uint2 v[(NB + 31) / 32];
 #pragma unroll
                 for (int c = 0; c < (NB + 31) / 32; ++c) {
-                    const int t = C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1);
-                    v[c] = *reinterpret_cast<const uint2*>(rows + 16 * (LM + t % NT) + 8 * (k & 1));
+                    const int t = (C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1)) % NT;
+                    v[c] = words(rows + bytes * (LM + t), g.t * NT + t, a.T, k);
                 }
                 if (!ptx::mbar_wait_all(&empty[s], par, abort_flag, L_WAIT_NS)) {
                     if (lane == 0) fail(4);
@@ -709,20 +722,36 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             const Segment<CG> g(a);
             const int row0 = g.m * LM, t0 = g.t * NT, n_tok = min(NT, a.T - t0);
             const int u0 = n_tok * c / a.split, u1 = n_tok * (c + 1) / a.split;
-            for (int i = threadIdx.x; i < (u1 - u0) * 32; i += C::THREADS) {
-                const int t = u0 + (i >> 5), row = 4 * (i & 31);
-                const float* at = reinterpret_cast<const float*>(sm) + t * LM + row;
-                float4 v[8];
+            // P parts of U pieces (four rows of a token) a thread, their loads under way together
+            auto add = [&](auto parts, auto pieces) {
+                constexpr int P = decltype(parts)::value, U = decltype(pieces)::value;
+#pragma unroll 1
+                for (int i = threadIdx.x; i < (u1 - u0) * 32; i += U * C::THREADS) {
+                    float4 v[U][P];
 #pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    v[p] = p < a.split ? ptx::ld_cluster(ptx::map_cluster(at, p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                float4 y = v[0];
+                    for (int u = 0; u < U; ++u) {
+                        const int j = i + u * C::THREADS;
+                        const uint32_t at = ptx::smem_u32(sm) + (min(u0 + (j >> 5), u1 - 1) * LM + 4 * (j & 31)) * 4;
 #pragma unroll
-                for (int p = 1; p < 8; ++p) y.x += v[p].x, y.y += v[p].y, y.z += v[p].z, y.w += v[p].w;
-                if (row0 + row < a.N)
-                    *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + row0 + row) =
-                        make_uint2(ptx::cvt_bf16x2(y.x, y.y), ptx::cvt_bf16x2(y.z, y.w));
-            }
+                        for (int p = 0; p < P; ++p)
+                            v[u][p] = p < a.split ? ptx::ld_cluster(ptx::map_cluster(at, p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int j = i + u * C::THREADS, t = u0 + (j >> 5), row = row0 + 4 * (j & 31);
+                        float4 y = v[u][0];
+#pragma unroll
+                        for (int p = 1; p < P; ++p)
+                            y.x += v[u][p].x, y.y += v[u][p].y, y.z += v[u][p].z, y.w += v[u][p].w;
+                        if (t < u1 && row < a.N)
+                            *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + row) =
+                                make_uint2(ptx::cvt_bf16x2(y.x, y.y), ptx::cvt_bf16x2(y.z, y.w));
+                    }
+                }
+            };
+            if (a.split == 2) add(Int<2>(), Int<NT >= 64 ? 7 : 1>());
+            else if (a.split <= 4) add(Int<4>(), Int<NT >= 64 ? 4 : 1>());
+            else add(Int<8>(), Int<NT >= 64 ? 2 : 1>());
             ptx::cluster_sync_all();   // every CTA keeps its part until the others have read it
         }
     }

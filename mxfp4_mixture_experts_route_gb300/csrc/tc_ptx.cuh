@@ -387,11 +387,12 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
 // The cluster address of `p`'s place in CTA `rank`, and an arrival there.  What the arrivals of a pair's
 // kernel announce are accesses to TMEM that have completed (tcgen05.wait) before it; a release at cluster
 // scope would wait for every load under way as well.
-__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
+__device__ __forceinline__ uint32_t map_cluster(uint32_t saddr, uint32_t rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) { return map_cluster(smem_u32(p), rank); }
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
