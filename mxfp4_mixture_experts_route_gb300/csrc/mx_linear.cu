@@ -28,7 +28,6 @@
 #include "quant.cuh"
 #include "tc_ptx.cuh"
 
-#include <atomic>
 #include <type_traits>
 
 namespace moe {
@@ -85,6 +84,7 @@ struct LArgs {
     StatusBlock* sb;
     int T, N, K;
     int64_t out_stride;
+    int nt;                                   // tokens of a pair's tile: a multiple of 32 up to NT
     int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
     int split;                                // CTAs of a cluster that share a tile, or 1
     int tiles, waves;                         // whole tiles that every worker takes first, if there is a line
@@ -230,10 +230,11 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         const uint64_t pol_w = a.w_once ? ptx::policy_evict_first() : ptx::policy_evict_last();
         const uint64_t pol_x = ptx::policy_evict_last();
         const uint32_t full0 = PAIR ? ptx::map_cluster(full, 0) : 0;
+        const uint32_t pair_tx = C::TX - C::B_BYTES / (NT / 2) * (NT - a.nt);
         auto weights = [&](const Segment<CG>& g, int k, int s) {
             uint8_t* st = sm + s * C::STAGE;
             const int row = (g.m * CG + rank) * LM;
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], C::TX);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], PAIR ? pair_tx : C::TX);
             if (PAIR) {
                 if (XMX) ptx::tma2_load_2d(st, &tm_w, 128 * k, row, full0 + 8 * s, pol_w);
                 else ptx::tma2_load_3d(st, &tm_w, 0, row, WORDS * k, full0 + 8 * s, pol_w);
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         };
         auto tokens = [&](const Segment<CG>& g, int k, int s) {
             uint8_t* st = sm + s * C::STAGE + C::A_BYTES;
-            const int row = g.t * NB + rank * C::B_ROWS;
+            const int row = PAIR ? g.t * a.nt + rank * (a.nt / 2) : g.t * NB;
             if (PAIR) {
                 if (XMX) ptx::tma2_load_2d(st, &tm_x, 128 * k, row, full0 + 8 * s, pol_x);
                 else ptx::tma2_load_4d(st, &tm_x, 0, row, 0, k, full0 + 8 * s, pol_x);
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const uint64_t ad = ptx::smem_desc_sw128(a0 + 32 * j), bd = ptx::smem_desc_sw128(b0 + 32 * j);
-                                const uint32_t id = ptx::idesc_mxf4(LM * CG, NB, 2 * (j & 1), 2 * (j & 1));
+                                const uint32_t id = ptx::idesc_mxf4(LM * CG, PAIR ? a.nt : NB, 2 * (j & 1), 2 * (j & 1));
                                 const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * (j >> 1), fb = sfb + 16 * (j >> 1);
                                 if (PAIR) ptx::mma2_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
                                 else ptx::mma_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
@@ -320,8 +321,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                                 // 128-K slab, K step within it, term
                                 const int h = WORDS == 2 ? j >> 2 : 0, q = j & 3, e = C::TERMS == 2 ? j >> 2 : 0;
                                 const uint64_t ad = ptx::smem_desc_sw128(a0 + h * LM * 128 + 32 * q);
-                                const uint64_t bd = ptx::smem_desc_sw128(b0 + (h + e) * C::B_ROWS * 128 + 32 * q);
-                                const uint32_t id = ptx::idesc_mx_e2m1_e4m3(LM * CG, NB, q, q);
+                                const uint64_t bd = ptx::smem_desc_sw128(b0 + (h * C::B_ROWS + e * (a.nt / 2)) * 128 + 32 * q);
+                                const uint32_t id = ptx::idesc_mx_e2m1_e4m3(LM * CG, PAIR ? a.nt : NB, q, q);
                                 const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * h, fb = sfb + 16 * h;
                                 if (PAIR) ptx::mma2_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
                                 else ptx::mma_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 #pragma unroll
             for (int u = 0; u < OWN; ++u) {
                 const int j = r + 128 * u;
-                const int t = g.t * NT + j;
+                const int t = g.t * a.nt + j;
                 load_scales(t < a.T ? a.xs + (int64_t)t * kb : nullptr, grp, kb, a.vec, nb[u]);
             }
         };
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         pdl_trigger();
         // G tokens' sums, a token's columns added
         constexpr int G = C::EN < 32 ? C::EN : 32;
-        const int first = (warp - 6) / 4 * C::EN;       // this warp's tokens: EN from here
+        const int first = PAIR ? (warp - 6) / 4 * (a.nt / 2) : 0;       // this warp's tokens: from here, at most EN
         auto read = [&](int ab, int t, float (&y)[G]) {
             const uint32_t from = tmem + lane_base + ab * NB + C::PER * t;
             if constexpr (C::PER * G == 16) {
@@ -607,8 +608,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::named_bar_sync(2, 32 * C::EW);
             if (last_flag[1 + (seg & 1)]) break;
             ptx::tc_fence_after();
-            const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * NT;
-            const int n_tok = min(NT, a.T - t0), mine = min(first + C::EN, n_tok);
+            const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * (PAIR ? a.nt : NT);
+            const int n_tok = min(PAIR ? a.nt : NT, a.T - t0), mine = PAIR ? min(first + a.nt / 2, n_tok) : n_tok;
             if constexpr (!PAIR) {
                 if (a.split > 1) {
                     // the CTA's part into its own shared memory, whose stages are done with
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                     break;
                 }
             }
-            if (g.k0 == 0 && g.k1 == a.nk) {
+            if (PAIR || (g.k0 == 0 && g.k1 == a.nk)) {
                 // lanes 2i and 2i + 1 exchange, so that each stores both rows of one of two tokens (2-byte
                 // stores: T = 8192, N = 14336, K = 7168 in 311 us against 289; rows of 256 bytes through shared
                 // memory: 330, by TMA: 371)
@@ -659,8 +660,9 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 }
                 continue;
             }
+            if constexpr (!PAIR) {
             constexpr int64_t PART = (int64_t)NT * LM;
-            auto part_of = [&](int c, int slot) { return a.parts + (((int64_t)c * CG + rank) * 2 + slot) * PART; };
+            auto part_of = [&](int c, int slot) { return a.parts + ((int64_t)c * 2 + slot) * PART; };
             float* part = part_of(me, g.k0 == 0) + r;
 #pragma unroll 1
             for (int t = first; t < mine; t += G) {
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             __threadfence();
             ptx::named_bar_sync(2, 32 * C::EW);
             if (threadIdx.x == 6 * 32) {
-                uint32_t* count = a.count + c0 * CG + rank;
+                uint32_t* count = a.count + c0;
                 const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
                 if (last) *count = 0;
                 __threadfence();
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             ptx::named_bar_sync(2, 32 * C::EW);
             if (!last_flag[0]) continue;
             // four rows a lane, a token a warp at a time; J tokens' loads under way together
-            constexpr int J = PAIR ? 4 : NT / C::EW < 16 ? NT / C::EW : 16;
+            constexpr int J = NT / C::EW < 16 ? NT / C::EW : 16;
             const int row4 = row0 + 4 * lane;
 #pragma unroll 1
             for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
@@ -712,6 +714,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                             make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
             }
             ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
+            }
         }
     }
     if constexpr (!PAIR) {
@@ -796,65 +799,75 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16*
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// CTAs a tile, and tokens a tile: a pair and 256 with many tokens; else the fewest that hold T, up to 128 (MXFP4 x) or 64.
+// How a product is cut: CTAs and tokens a tile; CTAs of a cluster that share a tile's K; whether the last tiles go on a line.
 struct Tiling {
-    int cg, nt;
+    int cg, nt, split;
+    bool line;
 };
-Tiling tiling(const MxDims& d) {
-    if (d.T > 512) return {2, 256};
-    const int most = d.x_mx ? 128 : 64;
-    int n = d.x_mx ? 16 : 8;
-    while (n < most && n < d.T) n *= 2;
-    return {1, n};
-}
 
-constexpr int L_CTAS = 160;   // at most as many CTAs as the workspace has parts for
+constexpr int L_CTAS = 152;   // a GB300's SMs: at most as many CTAs as the workspace has parts for
+// How many clusters of 0 .. 8 such CTAs (one an SM) a GB300 runs at once (cudaOccupancyMaxActiveClusters)
+constexpr int CLUSTERS[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+// The line's joins take as long as this many stages.
+constexpr int LINE = 10;
+
+// The cut with the least estimated time: a launch costs `start`, a round of tiles a stage's time for each of its
+// stages, and sharing K `join` (us).  The numbers were fitted to measurements over T = 1 .. 8192, which they
+// meet within 10%: with operands in L2 a single CTA's stage (256 K) takes about the same for 8 tokens as for 128
+// (its copies' latency), a pair's of MXFP4 x too, whatever its tokens; a pair's of a bf16 x (128 K) grows with
+// them.  For instance T = 512, N = 6144, K = 4096, MXFP4 x: tiles of 128 tokens 22.4 us, pairs with 192 13.8,
+// with 256 14.8; T = 128, N = 4096: 64 tokens and two CTAs a tile 8.7 us, 32 tokens and one 10.0; bf16
+// x, T = 4096: pairs with 224 tokens 127 us, with 256 140, with 128 158.
+Tiling tiling(const MxDims& d) {
+    struct Single {
+        int nt;
+        float start, stage, join;
+    };
+    static const Single mx[4] = {{16, 4.0f, 0.31f, 0.3f}, {32, 4.2f, 0.34f, 0.5f}, {64, 4.4f, 0.42f, 0.9f}, {128, 5.2f, 0.465f, 2.f}};
+    static const Single bf[4] = {{8, 6.0f, 0.31f, 0.3f}, {16, 6.2f, 0.35f, 0.4f}, {32, 6.3f, 0.45f, 0.6f}, {64, 7.0f, 0.49f, 1.f}};
+    Tiling best{0, 0, 1, false};
+    float least = 0.f;
+    auto take = [&](float t, const Tiling& c) {
+        if (best.cg == 0 || t < least) best = c, least = t;
+    };
+    const int64_t nk = (d.K + 255) / 256;
+    for (const Single& c : d.x_mx ? mx : bf) {
+        const int64_t tiles = (int64_t)((d.N + LM - 1) / LM) * ((d.T + c.nt - 1) / c.nt);
+        const int64_t rounds = (tiles + L_CTAS - 1) / L_CTAS;
+        for (int n = 2; n <= 8 && n <= nk; ++n)
+            if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), {1, c.nt, n, false});
+        take(c.start + c.stage * (rounds * nk), {1, c.nt, 1, false});
+        take(c.start + c.stage * ((float)(tiles * nk) / L_CTAS + LINE), {1, c.nt, 1, true});
+        if (c.nt >= d.T) break;
+    }
+    for (int nt = 64; nt <= 256; nt += 32) {
+        const int64_t tiles = (int64_t)((d.N + 2 * LM - 1) / (2 * LM)) * ((d.T + nt - 1) / nt);
+        const int64_t rounds = (tiles + L_CTAS / 2 - 1) / (L_CTAS / 2);
+        if (d.x_mx) take(6.6f + 0.45f * (rounds * nk), {2, nt, 1, false});
+        else take(6.5f + (0.235f + 0.00182f * nt) * (rounds * (d.K / 128)), {2, nt, 1, false});
+    }
+    return best;
+}
 
 struct LLayout {
     size_t count, parts, xq, xs, total;
 };
 LLayout layout(const MxDims& d) {
+    const Tiling t = tiling(d);
     LLayout L;
     L.count = sizeof(StatusBlock);            // in the zeroed prefix
     L.parts = align256(WS_ZERO_PREFIX);
-    L.xq = L.parts + align256((size_t)L_CTAS * 2 * tiling(d).nt * LM * 4);
+    L.xq = L.parts + align256(t.line ? (size_t)L_CTAS * 2 * t.nt * LM * 4 : 0);
     L.xs = L.xq + (d.x_mx ? 0 : align256((size_t)2 * d.T * d.K));
     L.total = L.xs + (d.x_mx ? 0 : align256((size_t)d.T * (d.K / 32)));
     return L;
 }
 
-// How many clusters of `size` such CTAs (one an SM) run at once on the current device (a GB300: 76 of two, 46 of
-// three, 36 of four, 28 of five, 23 of six, 15 of eight), asked once.
-int clusters_at_once(const void* kernel, int threads, int smem, int size) {
-    static std::atomic<int> known[64][9];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) dev = 0;
-    int n = known[dev][size];
-    if (n == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(size);
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = size;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            n = -1;
-        }
-        known[dev][size] = n;
-    }
-    return n;
-}
-
 template <bool XMX, int NT, int CG>
-cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
+cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cudaStream_t st) {
     using C = LCfg<XMX, NT, CG>;
     const LLayout L = layout(d);
+    const int nt = cut.nt;
     CUtensorMap tm_w, tm_x;
     const uint64_t N = d.N, T = d.T, K = d.K;
     const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -862,7 +875,7 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     if (XMX) {
         // packed rows of K / 2 bytes, 128 bytes (256 K) a stage
         const uint64_t w_d[2] = {K / 2, N}, x_d[2] = {K / 2, T}, s[1] = {K / 2};
-        const uint32_t w_b[2] = {128, LM}, x_b[2] = {128, (uint32_t)C::B_ROWS};
+        const uint32_t w_b[2] = {128, LM}, x_b[2] = {128, CG == 2 ? (uint32_t)nt / 2 : (uint32_t)NT};
         ok = make_map(&tm_w, U8, p.w, 2, w_d, s, w_b, CU_TENSOR_MAP_SWIZZLE_128B) &&
              make_map(&tm_x, U8, p.x, 2, x_d, s, x_b, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
@@ -870,7 +883,7 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
         // {128 bytes, T rows, 2 terms, K/128 slabs}
         const uint64_t w_d[3] = {128, N, K / 128}, w_s[2] = {K / 2, 64}, x_d[3] = {128, 2 * T, K / 128}, x_s[2] = {K, 128};
         const uint64_t t_d[4] = {128, T, 2, K / 128}, t_s[3] = {2 * K, K, 128};
-        const uint32_t w_b[3] = {128, LM, C::WORDS}, x_b[3] = {128, (uint32_t)C::NB, 2}, t_b[4] = {128, (uint32_t)C::B_ROWS, 2, 1};
+        const uint32_t w_b[3] = {128, LM, C::WORDS}, x_b[3] = {128, (uint32_t)C::NB, 2}, t_b[4] = {128, (uint32_t)nt / 2, 2, 1};
         ok = make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.w, 3, w_d, w_s, w_b, CU_TENSOR_MAP_SWIZZLE_128B) &&
              (CG == 2 ? make_map(&tm_x, U8, p.ws + L.xq, 4, t_d, t_s, t_b, CU_TENSOR_MAP_SWIZZLE_128B)
                       : make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B));
@@ -890,30 +903,24 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     a.K = d.K;
     a.out_stride = d.out_stride;
     a.nk = (d.K + C::KS - 1) / C::KS;
-    a.tt = (d.T + NT - 1) / NT;
     a.mt = (d.N + CG * LM - 1) / (CG * LM);
+    a.nt = nt;
+    a.tt = (d.T + nt - 1) / nt;
     const int64_t tiles = (int64_t)a.mt * a.tt;
     const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
     a.tiles = (int)tiles;
-    a.split = 1;
+    a.split = cut.split;
     a.waves = 0;
     a.total = 0;
     int ctas = (int)(tiles < workers ? tiles : workers);
-    if (CG == 1)
-        for (int n = 2; n <= 8 && n <= a.nk && n * tiles <= workers; ++n)
-            if (tiles <= clusters_at_once((const void*)k_mx_linear<XMX, NT, CG>, C::THREADS, C::SMEM, n)) a.split = n;
-    if (a.split > 1) {
-        ctas *= a.split;
-    } else if (tiles % workers) {
-        // a last round of whole tiles, or the line: it takes what is left over and one round more, so that a cut
-        // tile has at most three parts, and its joins take as long as LINE stages
-        constexpr int LINE = 10;
-        const int64_t rounds = tiles / workers + 1;
-        if (rounds * a.nk * workers > tiles * a.nk + (int64_t)LINE * workers) {
-            a.waves = rounds >= 2 ? (int)rounds - 2 : 0;
-            a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
-            ctas = workers;
-        }
+    if (cut.split > 1) {
+        ctas = (int)tiles * cut.split;
+    } else if (cut.line) {
+        // the line takes what whole rounds leave over and one round more, so that a cut tile has at most three parts
+        const int64_t rounds = tiles / workers;
+        a.waves = rounds >= 1 ? (int)rounds - 1 : 0;
+        a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
+        ctas = (int)(a.total < workers ? a.total : workers);
     }
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
@@ -952,20 +959,20 @@ cudaError_t launch_mx_linear(const MxDims& d, const MxArgs& a, cudaStream_t st) 
     KT_BIND();
     const Tiling t = tiling(d);
     if (d.x_mx) {
-        if (t.cg == 2) return launch_tiles<true, 256, 2>(d, a, st);
+        if (t.cg == 2) return launch_tiles<true, 256, 2>(d, a, t, st);
         switch (t.nt) {
-            case 16: return launch_tiles<true, 16, 1>(d, a, st);
-            case 32: return launch_tiles<true, 32, 1>(d, a, st);
-            case 64: return launch_tiles<true, 64, 1>(d, a, st);
-            default: return launch_tiles<true, 128, 1>(d, a, st);
+            case 16: return launch_tiles<true, 16, 1>(d, a, t, st);
+            case 32: return launch_tiles<true, 32, 1>(d, a, t, st);
+            case 64: return launch_tiles<true, 64, 1>(d, a, t, st);
+            default: return launch_tiles<true, 128, 1>(d, a, t, st);
         }
     }
-    if (t.cg == 2) return launch_tiles<false, 256, 2>(d, a, st);
+    if (t.cg == 2) return launch_tiles<false, 256, 2>(d, a, t, st);
     switch (t.nt) {
-        case 8: return launch_tiles<false, 8, 1>(d, a, st);
-        case 16: return launch_tiles<false, 16, 1>(d, a, st);
-        case 32: return launch_tiles<false, 32, 1>(d, a, st);
-        default: return launch_tiles<false, 64, 1>(d, a, st);
+        case 8: return launch_tiles<false, 8, 1>(d, a, t, st);
+        case 16: return launch_tiles<false, 16, 1>(d, a, t, st);
+        case 32: return launch_tiles<false, 32, 1>(d, a, t, st);
+        default: return launch_tiles<false, 64, 1>(d, a, t, st);
     }
 }
 
