@@ -351,32 +351,35 @@ def qkv_append(shape, rope, q_in, k_new, v_new, positions, slots, q_norm, k_norm
 _mx_types = {}
 
 
-def _mx_rows(t):
-    """(rows, K, MOE_* type, stride from row to row) of a tensor whose last dimension is K and whose others are rows."""
+def _mx_rows(t, codes, scales):
+    """(rows, K, MOE_* type, distance of rows or 0 where they are packed) of a tensor whose last dimension is K and whose
+    others are rows, next to packed codes [rows, K/2] and scales [rows, K/32]."""
     if not _mx_types:
         import torch
         _mx_types.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
     dt = _mx_types.get(t.dtype)
-    if dt is None or t.dim() < 1:
+    n = t.numel()
+    if dt is None or not n:
         raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (bf16, fp16 or fp32)")
-    if t.dim() != 2:
-        t = t.view(-1, t.shape[-1])        # (raises if the rows are not evenly apart)
-    rows, K = t.shape
-    if (K > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < K):
-        raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (elements of a row side by side, rows apart)")
-    return rows, K, dt, t.stride(0) if rows > 1 else 0
-
-
-def _mx_packed(rows, K, codes, scales):
-    if (codes.numel() * 2 != rows * K or scales.numel() * 32 != rows * K or not codes.is_contiguous()
-            or not scales.is_contiguous() or codes.element_size() != 1 or scales.element_size() != 1):
+    K = t.shape[-1]
+    stride = 0
+    if not t.is_contiguous():
+        if t.dim() != 2:
+            t = t.view(-1, K)          # (raises if the rows are not evenly apart)
+        stride = t.stride(0)
+        if (K > 1 and t.stride(1) != 1) or (n > K and stride < K):
+            raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (elements of a row side by side, rows apart)")
+        if n == K:
+            stride = 0
+    if (codes.numel() * 2 != n or scales.numel() * 32 != n or codes.element_size() != 1 or scales.element_size() != 1
+            or not codes.is_contiguous() or not scales.is_contiguous()):
         raise MoEError(MOE_ERR_INVALID_ARG, "mx codes [rows, K/2] and scales [rows, K/32] (packed bytes)")
+    return n // K, K, dt, stride
 
 
 def mx_quantize(x, codes, scales, stream=None) -> None:
     """Rows x [..., K] (bf16, fp16 or fp32) to MXFP4 codes [..., K/2] and scales [..., K/32] (uint8)."""
-    rows, K, dt, stride = _mx_rows(x)
-    _mx_packed(rows, K, codes, scales)
+    rows, K, dt, stride = _mx_rows(x, codes, scales)
     rc = (_lib or lib()).moe_mx_quantize(rows, K, dt, x.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(),
                                          _stream(stream))
     if rc:
@@ -385,8 +388,7 @@ def mx_quantize(x, codes, scales, stream=None) -> None:
 
 def mx_dequantize(codes, scales, y, stream=None) -> None:
     """MXFP4 rows read back into y [..., K] (bf16, fp16 or fp32)."""
-    rows, K, dt, stride = _mx_rows(y)
-    _mx_packed(rows, K, codes, scales)
+    rows, K, dt, stride = _mx_rows(y, codes, scales)
     rc = (_lib or lib()).moe_mx_dequantize(rows, K, dt, codes.data_ptr(), scales.data_ptr(), y.data_ptr(), stride,
                                            _stream(stream))
     if rc:

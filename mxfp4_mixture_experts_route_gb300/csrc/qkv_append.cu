@@ -14,6 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int QKV_THREADS = 128;
+constexpr int QKV_WARPS = 16;                 // warps of an SM that still start at once
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -24,24 +25,25 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// LPH lanes a head, HPG heads a group of lanes.
-template <int LPH, int HPG, bool E4M3, bool INTER>
+// LPH lanes a head; a warp takes CH heads of one kind (query, key or value) of one token, 32 / LPH side by side, U
+// of each group of lanes loaded at a time.
+template <int LPH, int CH, int U, bool E4M3, bool INTER>
 __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, const QkvArgs a) {
-    constexpr int D = LPH * 8;
-    const int qc = (d.Hq + HPG - 1) / HPG, kc = (d.Hkv + HPG - 1) / HPG, chunks = qc + 2 * kc;
+    constexpr int D = LPH * 8, SIDE = 32 / LPH;
+    const int qc = (d.Hq + CH - 1) / CH, kc = (d.Hkv + CH - 1) / CH, chunks = qc + 2 * kc;
     const int t = blockIdx.x;
-    int c = blockIdx.y * (blockDim.x / LPH) + threadIdx.x / LPH;
+    int c = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
     const int p = threadIdx.x % LPH;                 // the lane's piece of the head
-    const uint32_t lanes = LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1) << (threadIdx.x % 32 / LPH * LPH);
     KT_MARK(K_QKV_APPEND, 0);
     pdl_wait();
     KT_MARK(K_QKV_APPEND, 1);
-    if (c >= chunks) return;                         // (whole groups: the lanes of a head stay together)
+    if (c >= chunks) return;
     const int pos = ld_dep(a.positions + t);
     const int64_t slot = ld_dep(reinterpret_cast<const long long*>(a.slots) + t);
-    const int what = c < qc ? 0 : c < qc + kc ? 1 : 2;   // q, K, V
+    const int what = c < qc ? 0 : c < qc + kc ? 1 : 2;   // q, K, V: the same for the warp
     c -= what == 0 ? 0 : what == 1 ? qc : qc + kc;
-    const int heads = what == 0 ? d.Hq : d.Hkv, h0 = c * HPG;
+    const int end = min(what == 0 ? d.Hq : d.Hkv, (c + 1) * CH);   // the warp's heads end here
+    const int h0 = c * CH + threadIdx.x % 32 / LPH;                // this lane's: h0, h0 + SIDE, ...
     if (pos < 0) return;
     if (a.R > 0 && pos >= a.max_pos) {
         latch_status(a.sb, MOE_ERR_BAD_LENGTHS, t);
@@ -58,11 +60,24 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
         to = pg * d.page_stride + o * d.token_stride + 8 * p;
     }
     const uint16_t* src = reinterpret_cast<const uint16_t*>(what == 0 ? a.q_in : what == 1 ? a.k_new : a.v_new) +
-                          t * (what == 0 ? a.q_in_stride : d.kv_stride) + (int64_t)h0 * D + 8 * p;
-    uint4 x[HPG];
+                          t * (what == 0 ? a.q_in_stride : d.kv_stride) + 8 * p;
+    const float* scale = what == 1 ? a.k_scale : a.v_scale;
+    uint4 x[U], ahead[U];
+    float sc[U], sc_ahead[U];
+    auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < HPG; ++i)
-        if (h0 + i < heads) x[i] = ld_dep(reinterpret_cast<const uint4*>(src + i * D));
+        for (int i = 0; i < U; ++i) {
+            const int head = h + i * SIDE;
+            if (head < end) {
+                ahead[i] = ld_dep(reinterpret_cast<const uint4*>(src + (int64_t)head * D));
+                if (E4M3 && what != 0) sc_ahead[i] = ld_dep(scale + head);
+            } else {
+                ahead[i] = make_uint4(0, 0, 0, 0);
+                sc_ahead[i] = 1.f;
+            }
+        }
+    };
+    load(h0);
 
     const float* w = what == 0 ? a.q_norm : a.k_norm;
     // own[j] = w cos, other[j] = +- w' sin of the lane's element j; partner: the piece that holds x'
@@ -95,60 +110,76 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
         for (int j = 0; j < 8; ++j) other[j] = wp[j] * sn[j], own[j] *= cs[j];
     }
     const bool norm = what != 2 && w;
-    const float* scale = what == 1 ? a.k_scale : a.v_scale;
+    // (the same number of rounds for the warp's lanes, which exchange elements)
+#pragma unroll 1
+    for (int hb = h0; hb - h0 < end - c * CH; hb += U * SIDE) {
 #pragma unroll
-    for (int i = 0; i < HPG; ++i) {
-        if (h0 + i >= heads) break;
-        const int h = h0 + i;
-        const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float f[8];
+        for (int i = 0; i < U; ++i) x[i] = ahead[i], sc[i] = sc_ahead[i];
+        if (CH > U * SIDE) load(hb + U * SIDE);      // the next heads' loads under way meanwhile
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[2 * j] = lo_f(v[j]), f[2 * j + 1] = hi_f(v[j]);
-        float r = 1.f;
-        if (norm) {
-            float ss = 0.f;
+        for (int i = 0; i < U; ++i) {
+            const int h = hb + i * SIDE;
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+            for (int j = 0; j < 4; ++j) f[2 * j] = lo_f(v[j]), f[2 * j + 1] = hi_f(v[j]);
+            float r = 1.f;
+            if (norm) {
+                float ss = 0.f;
 #pragma unroll
-            for (int o = LPH / 2; o > 0; o /= 2) ss += __shfl_xor_sync(lanes, ss, o);
-            r = rsqrtf(ss * (1.f / D) + a.eps);
-        }
-        if (what != 2) {
+                for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t o = INTER ? __byte_perm(v[j], 0, 0x1032) : __shfl_sync(lanes, v[j], partner, LPH);
-                // (no product with the other element where nothing turns: it may be an infinity)
-                float a0 = f[2 * j] * own[2 * j], a1 = f[2 * j + 1] * own[2 * j + 1];
-                if (turned) a0 = fmaf(lo_f(o), other[2 * j], a0), a1 = fmaf(hi_f(o), other[2 * j + 1], a1);
-                f[2 * j] = a0 * r, f[2 * j + 1] = a1 * r;
+                for (int o = LPH / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                r = rsqrtf(ss * (1.f / D) + a.eps);
             }
-        }
-        if (what == 0 || !E4M3) {
-            const uint4 y = make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]),
-                                       ptx::cvt_bf16x2(f[4], f[5]), ptx::cvt_bf16x2(f[6], f[7]));
-            uint16_t* dst = what == 0 ? reinterpret_cast<uint16_t*>(a.q) + t * d.q_stride + (int64_t)h * D + 8 * p
-                                      : reinterpret_cast<uint16_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
-            *reinterpret_cast<uint4*>(dst) = y;
-        } else {
-            const KvScale k(ld_dep(scale + h));
-            uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(kv_codes4(f[0], f[1], f[2], f[3], k), kv_codes4(f[4], f[5], f[6], f[7], k));
+            if (what != 2) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t o = INTER ? __byte_perm(v[j], 0, 0x1032) : __shfl_sync(0xffffffffu, v[j], partner, LPH);
+                    // (no product with the other element where nothing turns: it may be an infinity)
+                    float a0 = f[2 * j] * own[2 * j], a1 = f[2 * j + 1] * own[2 * j + 1];
+                    if (turned) a0 = fmaf(lo_f(o), other[2 * j], a0), a1 = fmaf(hi_f(o), other[2 * j + 1], a1);
+                    f[2 * j] = a0 * r, f[2 * j + 1] = a1 * r;
+                }
+            }
+            if (h >= end) continue;
+            if (what == 0 || !E4M3) {
+                uint16_t* dst = what == 0 ? reinterpret_cast<uint16_t*>(a.q) + t * d.q_stride + (int64_t)h * D + 8 * p
+                                          : reinterpret_cast<uint16_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
+                *reinterpret_cast<uint4*>(dst) = make_uint4(ptx::cvt_bf16x2(f[0], f[1]), ptx::cvt_bf16x2(f[2], f[3]),
+                                                            ptx::cvt_bf16x2(f[4], f[5]), ptx::cvt_bf16x2(f[6], f[7]));
+            } else {
+                const KvScale k(sc[i]);
+                uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.k_cache : a.v_cache) + to + h * d.head_stride;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(kv_codes4(f[0], f[1], f[2], f[3], k), kv_codes4(f[4], f[5], f[6], f[7], k));
+            }
         }
     }
     KT_MARK(K_QKV_APPEND, 2);
 }
 
-template <int LPH, int HPG>
+template <int LPH, int CH, int U>
 cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
-    // a token's groups in equal blocks
-    const int chunks = (d.Hq + HPG - 1) / HPG + 2 * ((d.Hkv + HPG - 1) / HPG);
-    const int ny = (chunks * LPH + QKV_THREADS - 1) / QKV_THREADS;
-    const dim3 grid(d.T, ny), block((chunks + ny - 1) / ny * LPH);
+    // a token's warps in equal blocks
+    const int chunks = (d.Hq + CH - 1) / CH + 2 * ((d.Hkv + CH - 1) / CH);
+    const int ny = (chunks * 32 + QKV_THREADS - 1) / QKV_THREADS;
+    const dim3 grid(d.T, ny), block((chunks + ny - 1) / ny * 32);
     if (d.e4m3)
-        return a.interleaved ? launch_pdl(k_qkv_append<LPH, HPG, true, true>, grid, block, 0, st, d, a)
-                             : launch_pdl(k_qkv_append<LPH, HPG, true, false>, grid, block, 0, st, d, a);
-    return a.interleaved ? launch_pdl(k_qkv_append<LPH, HPG, false, true>, grid, block, 0, st, d, a)
-                         : launch_pdl(k_qkv_append<LPH, HPG, false, false>, grid, block, 0, st, d, a);
+        return a.interleaved ? launch_pdl(k_qkv_append<LPH, CH, U, true, true>, grid, block, 0, st, d, a)
+                             : launch_pdl(k_qkv_append<LPH, CH, U, true, false>, grid, block, 0, st, d, a);
+    return a.interleaved ? launch_pdl(k_qkv_append<LPH, CH, U, false, true>, grid, block, 0, st, d, a)
+                         : launch_pdl(k_qkv_append<LPH, CH, U, false, false>, grid, block, 0, st, d, a);
+}
+
+// The heads of a warp: the fewest that keep the warps within one round of the SMs (short chains, and every warp
+// loads the angles and weights anew), up to 32.
+template <int LPH>
+cudaError_t launch_lph(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
+    constexpr int SIDE = 32 / LPH;
+    const int64_t heads = (int64_t)d.T * (d.Hq + 2 * d.Hkv), most = (int64_t)num_sms() * QKV_WARPS;
+    if (heads <= most * SIDE) return launch_heads<LPH, SIDE, 1>(d, a, st);
+    if (heads <= most * 8) return launch_heads<LPH, 8, 2>(d, a, st);
+    return launch_heads<LPH, 32, 2>(d, a, st);
 }
 
 }  // namespace
@@ -156,10 +187,7 @@ cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
 cudaError_t launch_qkv_append(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
     KT_BIND();
     timing_begin(K_QKV_APPEND, st);
-    // one head a group while those groups fit one round of the SMs' threads (shortest path), four otherwise
-    const bool few = (int64_t)d.T * (d.Hq + 2 * d.Hkv) * (d.D / 8) <= (int64_t)num_sms() * 2048;
-    const cudaError_t e = d.D == 128 ? few ? launch_heads<16, 1>(d, a, st) : launch_heads<16, 4>(d, a, st)
-                                     : few ? launch_heads<8, 1>(d, a, st) : launch_heads<8, 4>(d, a, st);
+    const cudaError_t e = d.D == 128 ? launch_lph<16>(d, a, st) : launch_lph<8>(d, a, st);
     timing_end(st);
     return e;
 }
