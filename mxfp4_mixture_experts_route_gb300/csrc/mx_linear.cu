@@ -3,7 +3,8 @@
 // The weights are the MMA's A (M = 128 of their rows), the tokens its B.  With MXFP4 x
 // both stay packed (tcgen05.mma kind::mxf4, K = 64).  A bf16 x enters as
 // in the experts' kernel (experts_mx.cu): as two e4m3 terms a row, hi and lo, under
-// a power of two a block of 32, which a small kernel (k_mx_split) writes first; the TMA
+// a power of two a block of 32, which the scale warps make in shared memory (up to 8 tokens) or a
+// small kernel (k_mx_split) writes first; the TMA
 // unpacks the weights' codes for kind::mxf8f6f4.  Either way the tensor core applies the
 // block scales.
 //
@@ -43,6 +44,8 @@ constexpr int L_SITE = 300;                   // detail of MOE_ERR_TIMEOUT: site
 // NT tokens a tile, CG CTAs a tile.
 template <bool XMX, int NT, int CG>
 struct LCfg {
+    static constexpr bool FUSED = !XMX && CG == 1 && NT == 8;     // the terms of x are made here (K % 512 == 0)
+    static constexpr bool FIRST = XMX || FUSED;                   // the call's first kernel: it reads nothing before its wait
     static constexpr int TERMS = !XMX && CG == 2 ? 2 : 1;         // MMAs of a K step
     static constexpr int PER = !XMX && CG == 1 ? 2 : 1;           // accumulator columns a token
     static constexpr int NB = PER * NT;                           // MMA N
@@ -53,9 +56,10 @@ struct LCfg {
     static constexpr int B_BYTES = XMX ? B_ROWS * KS / 2 : TERMS * B_ROWS * KS;
     static constexpr int EW = CG == 2 ? 8 : 4;                    // warps of the way out, and tokens of each
     static constexpr int EN = NT / (EW / 4);
-    static constexpr int THREADS = 32 * (6 + EW);
+    static constexpr int SETS = FUSED ? 2 : 1;                    // sets of four scale warps: 2-5, and behind the others
+    static constexpr int THREADS = 32 * (2 + 4 * SETS + EW);
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int TX = CG * (LM * KS / 2 + B_BYTES);       // bytes of a stage that its barrier counts
+    static constexpr int TX = CG * (LM * KS / 2 + (FUSED ? 0 : B_BYTES));   // bytes of a stage that its barrier counts
     static constexpr int ACC = NB <= 128 ? 2 : 1;                 // accumulators
     // a stage's scales in TMEM: weight words of 128 K each at SF_A, SF_A + 16, the token words behind them
     // (every scale address is a multiple of 16 columns)
@@ -63,10 +67,10 @@ struct LCfg {
     static constexpr int SF_COL0 = (ACC * NB + 63) / 64 * 64;
     static constexpr int S_TMEM = (512 - SF_COL0) / SF_SLOT;
     // scales on their way to TMEM: a pair's token scales of 1024 K, exchanged between threads, twice; else RING
-    // groups of 512 K, a row of weights or tokens 16 bytes (or half as many of twice the bytes, where the rows in
+    // groups of 512 K (RING / SETS a set), a row of weights or tokens 16 bytes (or half as many of twice the bytes, where the rows in
     // memory are not 16-byte aligned: the two aligned pieces that hold them)
     static constexpr int RING = 4;
-    static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16;
+    static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16 + (FUSED ? SETS * 2 * NT * 8 : 0);
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
     // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
@@ -186,7 +190,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     uint64_t* empty = full + S;          // the stage's MMAs are done
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + ACC;
-    uint64_t* fin = acc_empty + ACC;
+    uint64_t* x_full = acc_empty + ACC;  // FUSED: the stage's rows of x are there
+    uint64_t* fin = x_full + (C::FUSED ? S : 0);
     uint32_t* holder = reinterpret_cast<uint32_t*>(fin + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
     volatile int* last_flag = abort_flag + 1;
@@ -198,6 +203,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         for (int i = 0; i < S; ++i) {
             ptx::mbar_init(&full[i], 1 + 4 * CG);      // TMA, the scale warps
             ptx::mbar_init(&empty[i], 1);
+            if (C::FUSED) ptx::mbar_init(&x_full[i], 1);
         }
         for (int i = 0; i < ACC; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
@@ -218,8 +224,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     if (PAIR) ptx::cluster_sync_all();   // both CTAs' barriers exist
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
-    // with MXFP4 x this is the call's first kernel: it reads nothing before its wait
-    if (XMX) pdl_wait();
+    if (C::FIRST) pdl_wait();
 
     auto fail = [&](int site) {
         latch_status(a.sb, MOE_ERR_TIMEOUT, L_SITE + site);
@@ -250,13 +255,20 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 if (XMX) ptx::tma2_load_2d(st, &tm_x, 128 * k, row, full0 + 8 * s, pol_x);
                 else ptx::tma2_load_4d(st, &tm_x, 0, row, 0, k, full0 + 8 * s, pol_x);
             } else {
-                if (XMX) ptx::tma_load_2d(st, &tm_x, 128 * k, row, &full[s], pol_x);
-                else ptx::tma_load_3d(st, &tm_x, 0, row, 2 * k, &full[s], pol_x);
+                if (C::FUSED) {
+                    // x itself, NT rows of 512 bytes
+                    ptx::mbar_arrive_expect_tx(&x_full[s], C::B_BYTES);
+                    ptx::tma_load_2d(st, &tm_x, 256 * k, g.t * NT, &x_full[s], pol_x);
+                } else if (XMX) {
+                    ptx::tma_load_2d(st, &tm_x, 128 * k, row, &full[s], pol_x);
+                } else {
+                    ptx::tma_load_3d(st, &tm_x, 0, row, 2 * k, &full[s], pol_x);
+                }
             }
         };
         if (lane == 0) {
             int pre = 0;
-            if (!XMX) {
+            if (!C::FIRST) {
                 // the first stages' weights, inputs of the call, before the wait for the tokens' terms
                 int i = 0;
                 for (Segment<CG> g(a); g.more() && i < S; g.next())
@@ -441,12 +453,16 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 }
             }
         }
-    } else if (warp < 6) {
-        // ------------------------------------------------------------ scales: RING - 1 groups of 512 K ahead in shared memory
+    } else if (warp < 6 || warp >= 6 + C::EW) {
+        // ------------------------------------------------------------ scales: groups of 512 K, ahead in shared memory
+        // (a set of four warps takes every SETS-th group, of which it has `ring` - 1 under way)
+        const int set = warp < 6 ? 0 : 1;
         const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row and token of this thread
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int kb = a.K / 32;
-        const int ring = a.vec ? C::RING : C::RING / 2, bytes = a.vec ? 16 : 32;
+        constexpr int RING_BYTES = C::RING * (LM + NT) * 16;
+        const int ring = (a.vec ? C::RING : C::RING / 2) / C::SETS, bytes = a.vec ? 16 : 32;
+        uint8_t* mine = xch + set * (C::RING / C::SETS) * (LM + NT) * 16;
         // a group's scale bytes of row `n` of `rows`; zeros past the tensor's ends, where the codes are zeros too
         auto fetch = [&](const uint8_t* src, int n, int rows, int grp, uint8_t* dst) {
             const int64_t at = (int64_t)min(n, rows - 1) * kb + 16 * grp, end = (int64_t)rows * kb;
@@ -468,10 +484,10 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             return make_uint2(w[0], 8 * k + 4 < kb ? w[1] : 0u);
         };
         auto fetch_a = [&](const Segment<CG>& g, int grp, int buf) {
-            fetch(a.w_scales, g.m * LM + r, a.N, grp, xch + (buf * (LM + NT) + r) * bytes);
+            fetch(a.w_scales, g.m * LM + r, a.N, grp, mine + (buf * (LM + NT) + r) * bytes);
         };
         auto fetch_b = [&](const Segment<CG>& g, int grp, int buf) {
-            if (r < NT) fetch(a.xs, g.t * NT + r, a.T, grp, xch + (buf * (LM + NT) + LM + r) * bytes);
+            if (!C::FUSED && r < NT) fetch(a.xs, g.t * NT + r, a.T, grp, mine + (buf * (LM + NT) + LM + r) * bytes);
         };
         auto advance = [&](Segment<CG>& g, int& grp) {
             if (2 * ++grp >= g.k1) {
@@ -479,9 +495,16 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 grp = 0;
             }
         };
+        // to the set's next group
+        auto skip = [&](Segment<CG>& g, int& grp) {
+#pragma unroll
+            for (int i = 0; i < C::SETS; ++i)
+                if (g.more()) advance(g, grp);
+        };
         Segment<CG> g(a), ahead = g;
         int grp = g.k0 / 2, agrp = grp;
-        if (!XMX) {
+        if (set == 1 && ahead.more()) advance(ahead, agrp);
+        if (!C::FIRST) {
             // the weights' scales, inputs of the call, before the wait for the tokens'
             Segment<CG> n = g;
             int ngrp = grp;
@@ -492,46 +515,96 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 #pragma unroll 1
         for (int i = 0; i < ring - 1; ++i) {
             if (ahead.more()) {
-                if (XMX) fetch_a(ahead, agrp, i);
+                if (C::FIRST) fetch_a(ahead, agrp, i);
                 fetch_b(ahead, agrp, i);
-                advance(ahead, agrp);
+                skip(ahead, agrp);
             }
             ptx::cp_async_commit();
         }
         // a warp whose wait gave up goes on without waiting: the four share the barrier below
-        int s = 0, buf = 0;
-        uint32_t par = 1;
+        int s = 0, buf = 0, turn = 0;
+        uint32_t par = C::FUSED ? 0 : 1;
+        uint2* made = reinterpret_cast<uint2*>(xch + RING_BYTES) + set * 2 * NT;   // FUSED: [2][NT] scale words of the stage's tokens
+        int turn_of = 0;                           // whose group it is
         bool ok = true;
 #pragma unroll 1
-        for (; g.more(); advance(g, grp), buf = buf + 1 == ring ? 0 : buf + 1) {
-            if (a.vec) ptx::cp_async_wait<C::RING - 2>();
-            else ptx::cp_async_wait<C::RING / 2 - 2>();
-            ptx::named_bar_sync(1, 128);
+        for (; g.more(); advance(g, grp)) {
+            const int k0 = max(2 * grp, g.k0), k1 = min(2 * grp + 2, g.k1);
+            if (C::SETS == 2) {
+                const bool other = turn_of != set;
+                turn_of ^= 1;
+                if (other) {
+                    s += k1 - k0;
+                    if (s >= S) s -= S, par ^= 1;
+                    continue;
+                }
+            }
+            if (ring == 4) ptx::cp_async_wait<2>();
+            else ptx::cp_async_wait<0>();
+            ptx::named_bar_sync(1 + 2 * set, 128);
             // (behind the barrier every warp is done with the group before this one)
             if (ahead.more()) {
                 const int to = buf == 0 ? ring - 1 : buf - 1;
                 fetch_a(ahead, agrp, to);
                 fetch_b(ahead, agrp, to);
-                advance(ahead, agrp);
+                skip(ahead, agrp);
             }
             ptx::cp_async_commit();
-            const uint8_t* rows = xch + buf * (LM + NT) * bytes;
+            const uint8_t* rows = mine + buf * (LM + NT) * bytes;
+            buf = buf + 1 == ring ? 0 : buf + 1;
 #pragma unroll 1
-            for (int k = max(2 * grp, g.k0); ok && k < min(2 * grp + 2, g.k1); ++k) {
+            for (int k = k0; k < k1; ++k) {
                 const uint2 w = words(rows + bytes * r, g.m * LM + r, a.N, k);
                 if (__vcmpeq4(w.x, 0xFFFFFFFFu) | __vcmpeq4(w.y, 0xFFFFFFFFu)) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 uint2 v[(NB + 31) / 32];
-#pragma unroll
-                for (int c = 0; c < (NB + 31) / 32; ++c) {
-                    const int t = (C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1)) % NT;
-                    v[c] = words(rows + bytes * (LM + t), g.t * NT + t, a.T, k);
-                }
-                if (!ptx::mbar_wait_all(&empty[s], par, abort_flag, L_WAIT_NS)) {
+                if (ok && !ptx::mbar_wait_all(C::FUSED ? &x_full[s] : &empty[s], par, abort_flag, L_WAIT_NS)) {
                     if (lane == 0) fail(4);
                     ok = false;
-                    break;
                 }
                 ptx::tc_fence_after();
+                if constexpr (C::FUSED) {
+                    // warp q takes tokens q, q + 4, ..., a lane 8 elements of each: x out of the stage, then its
+                    // terms in place of it (row 2t hi, 2t + 1 lo, two slabs of 128 K, 128-byte swizzle)
+                    uint8_t* st = sm + s * C::STAGE + C::A_BYTES;
+                    QuantChunk qc[NT / 4];
+#pragma unroll
+                    for (int i = 0; i < NT / 4; ++i) {
+                        if (g.t * NT + 4 * i + q >= a.T) {      // (the arithmetic is what a stage takes longest for)
+                            qc[i].hi = qc[i].lo = make_uint2(0, 0);
+                            qc[i].e = 1;
+                            qc[i].amax = 0;
+                        } else {
+                            qc[i] = quantize_vals(*reinterpret_cast<const uint4*>(st + (4 * i + q) * 512 + 16 * lane));
+                        }
+                        if (qc[i].amax >= 0x7F800000u) {
+                            qc[i].hi = qc[i].lo = make_uint2(0, 0);
+                            qc[i].e = 255;
+                        }
+                        // lanes 0-15: the scale bytes of the first 128 K, lanes 16-31: of the second
+                        uint32_t e = (uint32_t)qc[i].e << (8 * (lane >> 2 & 3));
+                        e |= __shfl_xor_sync(0xffffffffu, e, 4);
+                        e |= __shfl_xor_sync(0xffffffffu, e, 8);
+                        if ((lane & 15) == 0) reinterpret_cast<uint32_t*>(made + turn * NT + 4 * i + q)[lane >> 4] = e;
+                    }
+                    ptx::named_bar_sync(1 + 2 * set, 128);
+#pragma unroll
+                    for (int i = 0; i < NT / 4; ++i) {
+                        const int row = 2 * (4 * i + q), unit = lane >> 1 & 7;
+                        uint8_t* to = st + (lane >> 4) * NB * 128 + row * 128 + 8 * (lane & 1);
+                        *reinterpret_cast<uint2*>(to + ((unit ^ (row & 7)) << 4)) = qc[i].hi;
+                        *reinterpret_cast<uint2*>(to + 128 + ((unit ^ (row + 1 & 7)) << 4)) = qc[i].lo;
+                    }
+                    ptx::fence_proxy_async_shared();
+                    v[0] = made[turn * NT + (lane >> 1) % NT];
+                    turn ^= 1;                     // (written again only behind the next stage's barrier)
+                } else {
+#pragma unroll
+                    for (int c = 0; c < (NB + 31) / 32; ++c) {
+                        const int t = (C::PER == 1 ? 32 * c + lane : 16 * c + (lane >> 1)) % NT;
+                        v[c] = words(rows + bytes * (LM + t), g.t * NT + t, a.T, k);
+                    }
+                }
+                if (!ok) continue;
                 const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
                 // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
                 // word into all four columns; the other quarters' are never read)
@@ -562,7 +635,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         const int q = warp & 3, r = 32 * q + lane;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const uint32_t acc_empty0 = PAIR ? ptx::map_cluster(acc_empty, 0) : 0;
-        if (!XMX) pdl_wait();   // (the workspace's parts: an earlier call may still read its own)
+        if (!C::FIRST) pdl_wait();   // (the workspace's parts: an earlier call may still read its own)
         pdl_trigger();
         // G tokens' sums, a token's columns added
         constexpr int G = C::EN < 32 ? C::EN : 32;
@@ -755,7 +828,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             if (a.split == 2) add(Int<2>(), Int<NT >= 64 ? 7 : 1>());
             else if (a.split <= 4) add(Int<4>(), Int<NT >= 64 ? 4 : 1>());
             else add(Int<8>(), Int<NT >= 64 ? 2 : 1>());
-            ptx::cluster_sync_all();   // every CTA keeps its part until the others have read it
+            ptx::cluster_sync_relaxed();   // every CTA keeps its part until the others have read it
         }
     }
     __syncthreads();
@@ -823,8 +896,8 @@ Tiling tiling(const MxDims& d) {
         int nt;
         float start, stage, join;
     };
-    static const Single mx[4] = {{16, 4.0f, 0.31f, 0.3f}, {32, 4.2f, 0.34f, 0.5f}, {64, 4.4f, 0.42f, 0.9f}, {128, 5.2f, 0.465f, 2.f}};
-    static const Single bf[4] = {{8, 6.0f, 0.31f, 0.3f}, {16, 6.2f, 0.35f, 0.4f}, {32, 6.3f, 0.45f, 0.6f}, {64, 7.0f, 0.49f, 1.f}};
+    static const Single mx[4] = {{16, 3.2f, 0.40f, 0.5f}, {32, 3.4f, 0.41f, 0.6f}, {64, 4.0f, 0.43f, 0.9f}, {128, 5.0f, 0.465f, 1.6f}};
+    static const Single bf[4] = {{8, 4.4f, 0.47f, 0.3f}, {16, 4.8f, 0.44f, 0.4f}, {32, 5.6f, 0.42f, 0.6f}, {64, 7.0f, 0.49f, 1.f}};
     Tiling best{0, 0, 1, false};
     float least = 0.f;
     auto take = [&](float t, const Tiling& c) {
@@ -832,6 +905,7 @@ Tiling tiling(const MxDims& d) {
     };
     const int64_t nk = (d.K + 255) / 256;
     for (const Single& c : d.x_mx ? mx : bf) {
+        if (c.nt == 8 && d.K % 512) continue;   // its kernel takes the scales by 16 bytes
         const int64_t tiles = (int64_t)((d.N + LM - 1) / LM) * ((d.T + c.nt - 1) / c.nt);
         const int64_t rounds = (tiles + L_CTAS - 1) / L_CTAS;
         for (int n = 2; n <= 8 && n <= nk; ++n)
@@ -858,8 +932,9 @@ LLayout layout(const MxDims& d) {
     L.count = sizeof(StatusBlock);            // in the zeroed prefix
     L.parts = align256(WS_ZERO_PREFIX);
     L.xq = L.parts + align256(t.line ? (size_t)L_CTAS * 2 * t.nt * LM * 4 : 0);
-    L.xs = L.xq + (d.x_mx ? 0 : align256((size_t)2 * d.T * d.K));
-    L.total = L.xs + (d.x_mx ? 0 : align256((size_t)d.T * (d.K / 32)));
+    const bool split_x = !d.x_mx && !(t.cg == 1 && t.nt == 8);   // k_mx_split's terms
+    L.xs = L.xq + (split_x ? align256((size_t)2 * d.T * d.K) : 0);
+    L.total = L.xs + (split_x ? align256((size_t)d.T * (d.K / 32)) : 0);
     return L;
 }
 
@@ -884,9 +959,12 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
         const uint64_t w_d[3] = {128, N, K / 128}, w_s[2] = {K / 2, 64}, x_d[3] = {128, 2 * T, K / 128}, x_s[2] = {K, 128};
         const uint64_t t_d[4] = {128, T, 2, K / 128}, t_s[3] = {2 * K, K, 128};
         const uint32_t w_b[3] = {128, LM, C::WORDS}, x_b[3] = {128, (uint32_t)C::NB, 2}, t_b[4] = {128, (uint32_t)nt / 2, 2, 1};
+        const uint64_t r_d[2] = {K, T}, r_s[1] = {2 * (uint64_t)d.x_stride};
+        const uint32_t r_b[2] = {256, (uint32_t)NT};
         ok = make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, p.w, 3, w_d, w_s, w_b, CU_TENSOR_MAP_SWIZZLE_128B) &&
-             (CG == 2 ? make_map(&tm_x, U8, p.ws + L.xq, 4, t_d, t_s, t_b, CU_TENSOR_MAP_SWIZZLE_128B)
-                      : make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B));
+             (C::FUSED ? make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, 2, r_d, r_s, r_b, CU_TENSOR_MAP_SWIZZLE_NONE)
+              : CG == 2 ? make_map(&tm_x, U8, p.ws + L.xq, 4, t_d, t_s, t_b, CU_TENSOR_MAP_SWIZZLE_128B)
+                        : make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B));
     }
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_mx_linear<XMX, NT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -924,7 +1002,7 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     }
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
-    if (!XMX) {
+    if (!C::FIRST) {
         timing_begin(K_MX_SPLIT, st);
         e = launch_pdl(k_mx_split, dim3(d.T, (d.K / 8 + SPLIT_THREADS - 1) / SPLIT_THREADS), dim3(SPLIT_THREADS), 0, st,
                        reinterpret_cast<const __nv_bfloat16*>(p.x), d.x_stride, d.K,

@@ -216,7 +216,7 @@ def check(out, x64, off, w64):
 SHAPES = [(1, 8, 128), (1, 128, 256), (3, 136, 384), (8, 256, 1024), (5, 6144, 4096), (9, 1000, 640), (16, 512, 4224),
           (17, 264, 2048), (33, 1024, 1152), (64, 128, 7168), (65, 392, 512), (100, 2048, 1536), (128, 1280, 4096),
           (129, 160, 896), (255, 640, 2176), (257, 520, 1280), (300, 4096, 256), (1000, 1000, 1024), (2049, 768, 640),
-          (700, 8, 65536)]
+          (700, 8, 65536), (5, 20000, 4096), (40, 9736, 5120), (3, 19464, 3968), (200, 6152, 16384)]
 
 
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
