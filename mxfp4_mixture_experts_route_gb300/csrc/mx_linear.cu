@@ -56,7 +56,10 @@ struct LCfg {
     static constexpr int B_BYTES = XMX ? B_ROWS * KS / 2 : TERMS * B_ROWS * KS;
     static constexpr int EW = CG == 2 ? 8 : 4;                    // warps of the way out, and tokens of each
     static constexpr int EN = NT / (EW / 4);
-    static constexpr int SETS = FUSED ? 2 : 1;                    // sets of four scale warps: 2-5, and behind the others
+    // sets of four scale warps (2-5, and behind the others), which take turns where a stage has little else: one alone
+    // takes 0.4 us a stage (T = 8, N = 16384, K = 8192, MXFP4 x: 16.1 us, with two 13.8; with wider tiles the
+    // registers of more warps cost more than they gain: T = 128, N = 9216, K = 7168 12.4, with two 13.1)
+    static constexpr int SETS = FUSED || (XMX && NT <= 64) ? 2 : 1;
     static constexpr int THREADS = 32 * (2 + 4 * SETS + EW);
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int TX = CG * (LM * KS / 2 + (FUSED ? 0 : B_BYTES));   // bytes of a stage that its barrier counts
@@ -69,7 +72,7 @@ struct LCfg {
     // scales on their way to TMEM: a pair's token scales of 1024 K, exchanged between threads, twice; else RING
     // groups of 512 K (RING / SETS a set), a row of weights or tokens 16 bytes (or half as many of twice the bytes, where the rows in
     // memory are not 16-byte aligned: the two aligned pieces that hold them)
-    static constexpr int RING = 4;
+    static constexpr int RING = SETS == 2 && !FUSED ? 8 : 4;
     static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16 + (FUSED ? SETS * 2 * NT * 8 : 0);
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
@@ -506,10 +509,10 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         if (set == 1 && ahead.more()) advance(ahead, agrp);
         if (!C::FIRST) {
             // the weights' scales, inputs of the call, before the wait for the tokens'
-            Segment<CG> n = g;
-            int ngrp = grp;
+            Segment<CG> n = ahead;
+            int ngrp = agrp;
 #pragma unroll 1
-            for (int i = 0; i < ring - 1 && n.more(); ++i, advance(n, ngrp)) fetch_a(n, ngrp, i);
+            for (int i = 0; i < ring - 1 && n.more(); ++i, skip(n, ngrp)) fetch_a(n, ngrp, i);
             pdl_wait();
         }
 #pragma unroll 1
@@ -849,22 +852,35 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 
 // A bf16 x as two e4m3 terms a row (rows 2t and 2t + 1 of xq) and a scale byte a
 // block (quant.cuh); a block with a NaN or an infinity has byte 255 and codes 0.
+// PIECES of 16 bytes a thread, their loads under way together: with many rows four (bound by HBM; the product with
+// 4096 rows of 4096 takes 121 us, with one 128), with few one (latency; 128 rows of 7168 21.3 us, with four 22.9).
 constexpr int SPLIT_THREADS = 128;
+template <int PIECES>
 __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16* x, int64_t stride, int K, uint8_t* xq, uint8_t* xs) {
-    const int t = blockIdx.x, c = blockIdx.y * SPLIT_THREADS + threadIdx.x, n = K / 8;
+    const int t = blockIdx.x, first = blockIdx.y * SPLIT_THREADS * PIECES + threadIdx.x, n = K / 8;
+    const uint4* row = reinterpret_cast<const uint4*>(x + t * stride);
     KT_MARK(K_MX_SPLIT, 0);
     pdl_wait();
     pdl_trigger();   // (after the wait: the product reads the weights as soon as it starts)
     KT_MARK(K_MX_SPLIT, 1);
-    QuantChunk q = quantize_chunk_dep(reinterpret_cast<const uint4*>(x + t * stride), c, c < n);
-    if (q.amax >= 0x7F800000u) {
-        q.hi = q.lo = make_uint2(0, 0);
-        q.e = 255;
+    uint4 v[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = first + i * SPLIT_THREADS;
+        v[i] = c < n ? ld_dep(row + c) : make_uint4(0, 0, 0, 0);
     }
-    if (c < n) {
-        uint8_t* row = xq + (size_t)2 * t * K + 8 * c;
-        *reinterpret_cast<uint2*>(row) = q.hi;
-        *reinterpret_cast<uint2*>(row + K) = q.lo;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = first + i * SPLIT_THREADS;
+        QuantChunk q = quantize_vals(v[i]);
+        if (q.amax >= 0x7F800000u) {
+            q.hi = q.lo = make_uint2(0, 0);
+            q.e = 255;
+        }
+        if (c >= n) continue;
+        uint8_t* to = xq + (size_t)2 * t * K + 8 * c;
+        *reinterpret_cast<uint2*>(to) = q.hi;
+        *reinterpret_cast<uint2*>(to + K) = q.lo;
         if ((c & 3) == 0) xs[(size_t)t * (K / 32) + (c >> 2)] = (uint8_t)q.e;
     }
     KT_MARK(K_MX_SPLIT, 2);
@@ -896,7 +912,7 @@ Tiling tiling(const MxDims& d) {
         int nt;
         float start, stage, join;
     };
-    static const Single mx[4] = {{16, 3.2f, 0.40f, 0.5f}, {32, 3.4f, 0.41f, 0.6f}, {64, 4.0f, 0.43f, 0.9f}, {128, 5.0f, 0.465f, 1.6f}};
+    static const Single mx[4] = {{16, 3.7f, 0.31f, 0.5f}, {32, 3.7f, 0.35f, 0.6f}, {64, 4.3f, 0.40f, 1.2f}, {128, 5.0f, 0.465f, 1.6f}};
     static const Single bf[4] = {{8, 4.4f, 0.47f, 0.3f}, {16, 4.8f, 0.44f, 0.4f}, {32, 5.6f, 0.42f, 0.6f}, {64, 7.0f, 0.49f, 1.f}};
     Tiling best{0, 0, 1, false};
     float least = 0.f;
@@ -1004,7 +1020,9 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     a.w_once = a.tt == 1;
     if (!C::FIRST) {
         timing_begin(K_MX_SPLIT, st);
-        e = launch_pdl(k_mx_split, dim3(d.T, (d.K / 8 + SPLIT_THREADS - 1) / SPLIT_THREADS), dim3(SPLIT_THREADS), 0, st,
+        const bool many = (int64_t)d.T * (d.K / 8) > (int64_t)num_sms() * 2048;   // more than one round of the SMs' threads
+        const int per = SPLIT_THREADS * (many ? 4 : 1);
+        e = launch_pdl(many ? k_mx_split<4> : k_mx_split<1>, dim3(d.T, (d.K / 8 + per - 1) / per), dim3(SPLIT_THREADS), 0, st,
                        reinterpret_cast<const __nv_bfloat16*>(p.x), d.x_stride, d.K,
                        reinterpret_cast<uint8_t*>(p.ws + L.xq), reinterpret_cast<uint8_t*>(p.ws + L.xs));
         timing_end(st);
