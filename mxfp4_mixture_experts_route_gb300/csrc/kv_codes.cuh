@@ -10,13 +10,15 @@ namespace moe {
 
 // The code of x / s is that of the division's correctly rounded quotient, not of
 // a product with the reciprocal, so that a code is the one the formula gives.  The
-// product is off by less than 2^-22 of itself, so where a little more and a little
+// product with the approximate reciprocal (off by 2^-23) and a factor next to one (two roundings, 2^-24 each)
+// is off by less than 2^-21 of itself, so where a little more and a little
 // less than it give the same code, that is the quotient's code too (rounding
 // is monotonic); only next to a tie between two codes the division is made.
 struct KvScale {
     float s, lo, hi;
     __device__ __forceinline__ explicit KvScale(float v) : s(v) {
-        const float r = __fdiv_rn(1.f, v);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
         // (a scale whose reciprocal is not an ordinary number: always by division)
         const bool fine = v > 0x1p-120f && v < 0x1p120f;
         lo = fine ? r * (1.f - 0x1p-21f) : 1.f;

@@ -19,9 +19,14 @@ constexpr int QKV_WARPS = 16;                 // warps of an SM that still start
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// eight fp32 of a table or weight row an earlier kernel may have written
+// four and eight fp32 of a table or weight row: in shared memory, or as an earlier kernel may have written it
+template <bool SHARED>
+__device__ __forceinline__ float4 load4(const float* p) {
+    return SHARED ? *reinterpret_cast<const float4*>(p) : ld_dep(reinterpret_cast<const float4*>(p));
+}
+template <bool SHARED>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = ld_dep(reinterpret_cast<const float4*>(p)), b = ld_dep(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = load4<SHARED>(p), b = load4<SHARED>(p + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
@@ -30,6 +35,7 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 template <int LPH, int CH, int U, bool E4M3, bool INTER>
 __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, const QkvArgs a) {
     constexpr int D = LPH * 8, SIDE = 32 / LPH;
+    constexpr bool STAGED = CH == 8 || CH == 16;
     const int qc = (d.Hq + CH - 1) / CH, kc = (d.Hkv + CH - 1) / CH, chunks = qc + 2 * kc;
     const int t = blockIdx.x;
     int c = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
@@ -37,10 +43,10 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
     KT_MARK(K_QKV_APPEND, 0);
     pdl_wait();
     KT_MARK(K_QKV_APPEND, 1);
-    if (c >= chunks) return;
     const int pos = ld_dep(a.positions + t);
     const int64_t slot = ld_dep(reinterpret_cast<const long long*>(a.slots) + t);
     const int what = c < qc ? 0 : c < qc + kc ? 1 : 2;   // q, K, V: the same for the warp
+    bool live = c < chunks;
     c -= what == 0 ? 0 : what == 1 ? qc : qc + kc;
     const int end = min(what == 0 ? d.Hq : d.Hkv, (c + 1) * CH);   // the warp's heads end here
     const int h0 = c * CH + threadIdx.x % 32 / LPH;                // this lane's: h0, h0 + SIDE, ...
@@ -50,14 +56,13 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
         return;
     }
     int64_t to = 0;
-    if (what != 0) {
-        if (slot >= (int64_t)d.n_pages * d.page) {
-            latch_status(a.sb, MOE_ERR_BAD_PAGE, (int)(slot / d.page));
-            return;
+    if (what != 0 && live) {
+        if (slot >= (int64_t)d.n_pages * d.page) latch_status(a.sb, MOE_ERR_BAD_PAGE, (int)(slot / d.page));
+        live = slot >= 0 && slot < (int64_t)d.n_pages * d.page;
+        if (live) {
+            const int pg = (int)slot / d.page, o = (int)slot - pg * d.page;
+            to = pg * d.page_stride + o * d.token_stride + 8 * p;
         }
-        if (slot < 0) return;
-        const int pg = (int)slot / d.page, o = (int)slot - pg * d.page;
-        to = pg * d.page_stride + o * d.token_stride + 8 * p;
     }
     const uint16_t* src = reinterpret_cast<const uint16_t*>(what == 0 ? a.q_in : what == 1 ? a.k_new : a.v_new) +
                           t * (what == 0 ? a.q_in_stride : d.kv_stride) + 8 * p;
@@ -77,9 +82,24 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
             }
         }
     };
-    load(h0);
+    if (live) load(h0);
 
-    const float* w = what == 0 ? a.q_norm : a.k_norm;
+    // the token's angles and the weights: by way of shared memory, once a block instead of once a warp, where a warp has
+    // some heads (500 rows of 56 + 2 x 8: 5.4 us, without 7.3; with fewer heads its latency counts, with more
+    // it gains nothing: 16,411 rows 122 us, without 116)
+    const float *w = what == 0 ? a.q_norm : a.k_norm, *row = a.cos_sin + (int64_t)pos * a.R;
+    if constexpr (STAGED) {
+        __shared__ float4 stage[3][D / 4];
+        for (int i = threadIdx.x; i < 3 * D / 4; i += blockDim.x) {
+            const int n = i / (D / 4), j = i % (D / 4);
+            const float* from = n == 0 ? a.q_norm : n == 1 ? a.k_norm : row;
+            if (n < 2 ? from != nullptr : 4 * j < a.R) stage[n][j] = ld_dep(reinterpret_cast<const float4*>(from) + j);
+        }
+        __syncthreads();
+        if (w) w = reinterpret_cast<const float*>(stage[what == 0 ? 0 : 1]);
+        row = reinterpret_cast<const float*>(stage[2]);
+    }
+    if (!live) return;
     // own[j] = w cos, other[j] = +- w' sin of the lane's element j; partner: the piece that holds x'
     float own[8], other[8];
     const bool turned = what != 2 && 8 * p < a.R;
@@ -87,24 +107,23 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
     const int partner = INTER || !turned ? p : p < half ? p + half : p - half;
 #pragma unroll
     for (int j = 0; j < 8; ++j) own[j] = 1.f, other[j] = 0.f;
-    if (what != 2 && w) load8(w + 8 * p, own);
+    if (what != 2 && w) load8<STAGED>(w + 8 * p, own);
     if (turned) {
-        const float* row = a.cos_sin + (int64_t)pos * a.R;
         float cs[8], sn[8], wp[8];
         if (INTER) {
-            const float4 u = ld_dep(reinterpret_cast<const float4*>(row + 4 * p));
-            const float4 v = ld_dep(reinterpret_cast<const float4*>(row + a.R / 2 + 4 * p));
+            const float4 u = load4<STAGED>(row + 4 * p);
+            const float4 v = load4<STAGED>(row + a.R / 2 + 4 * p);
             cs[0] = cs[1] = u.x, cs[2] = cs[3] = u.y, cs[4] = cs[5] = u.z, cs[6] = cs[7] = u.w;
             sn[1] = v.x, sn[3] = v.y, sn[5] = v.z, sn[7] = v.w;
 #pragma unroll
             for (int j = 0; j < 8; j += 2) sn[j] = -sn[j + 1], wp[j] = own[j + 1], wp[j + 1] = own[j];
         } else {
             const int i = 8 * (p < half ? p : p - half);
-            load8(row + i, cs);
-            load8(row + a.R / 2 + i, sn);
+            load8<STAGED>(row + i, cs);
+            load8<STAGED>(row + a.R / 2 + i, sn);
 #pragma unroll
             for (int j = 0; j < 8; ++j) wp[j] = 1.f, sn[j] = p < half ? -sn[j] : sn[j];
-            if (w) load8(w + 8 * partner, wp);
+            if (w) load8<STAGED>(w + 8 * partner, wp);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) other[j] = wp[j] * sn[j], own[j] *= cs[j];
@@ -171,14 +190,16 @@ cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
                          : launch_pdl(k_qkv_append<LPH, CH, U, false, false>, grid, block, 0, st, d, a);
 }
 
-// The heads of a warp: the fewest that keep the warps within one round of the SMs (short chains, and every warp
-// loads the angles and weights anew), up to 32.
+// The heads of a warp: two to four while the warps fit one round of the SMs (short chains), more where the angles and
+// weights that every warp needs come to count (rows of 56 + 2 x 8 heads to bf16: 32 rows 3.0 us with two, 3.9 with 16; 128
+// rows 3.5 with 8, 4.2 with 4 and with 16; 500 rows 5.4 with 16, 7.0 with 8 and with 32; 16,411 rows 116 with 32, 128 with 16).
 template <int LPH>
 cudaError_t launch_lph(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
     constexpr int SIDE = 32 / LPH;
     const int64_t heads = (int64_t)d.T * (d.Hq + 2 * d.Hkv), most = (int64_t)num_sms() * QKV_WARPS;
     if (heads <= most * SIDE) return launch_heads<LPH, SIDE, 1>(d, a, st);
     if (heads <= most * 8) return launch_heads<LPH, 8, 2>(d, a, st);
+    if (heads <= most * 64) return launch_heads<LPH, 16, 2>(d, a, st);
     return launch_heads<LPH, 32, 2>(d, a, st);
 }
 

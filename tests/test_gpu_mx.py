@@ -373,3 +373,118 @@ def test_linear_extreme_scales(kind, low, high):
     out, work = product(x, xs, w, ws, T, N, K, kind)
     moe.check_device_status(work)
     check(out, x64, off, values(w, ws))
+
+
+@pytest.mark.parametrize("T", [1, 3, 8])
+def test_linear_few_tokens_place_every_element(T):
+    N, K = 136, 1536
+    g = gen(T)
+    for _ in range(6):
+        t, n, k = (int(torch.randint(0, m, (1,), device=DEV, generator=g)) for m in (T, N, K))
+        x = torch.zeros(T, K, device=DEV, dtype=torch.bfloat16)
+        x[t, k] = 3.0
+        w = torch.zeros(N, K, device=DEV)
+        w[n, k] = -0.5
+        codes, scales = torch.empty(N, K // 2, dtype=torch.uint8, device=DEV), torch.empty(N, K // 32, dtype=torch.uint8, device=DEV)
+        moe.mx_quantize(w, codes, scales)
+        out, _ = product(x, None, codes, scales, T, N, K, "bf16")
+        want = torch.zeros(T, N, device=DEV)
+        want[t, n] = -1.5
+        assert torch.equal(out.float(), want)
+
+
+@pytest.mark.parametrize("T,bad", [(1, 0), (6, 2), (8, 7)])
+def test_linear_few_tokens_that_are_not_finite(T, bad):
+    N, K = 200, 2048
+    w, ws = weights(8, N, K)
+    w[0] = 0
+    x, _, x64, off = tokens(9, T, K, "bf16")
+    x[bad, 1000] = float("-inf")
+    out, work = product(x, None, w, ws, T, N, K, "bf16")
+    moe.check_device_status(work)
+    keep = [t for t in range(T) if t != bad]
+    assert out[bad].isnan().all()
+    check(out[keep], x64[keep], off[keep], values(w, ws))
+
+
+@pytest.mark.parametrize("T,N,K,kind", [(1 << 20, 8, 128, "bf16"), (1 << 20, 8, 128, "mxfp4"), (1, 1 << 20, 128, "bf16"),
+                                        (2, 1 << 20, 128, "mxfp4")])
+def test_linear_largest_sides(T, N, K, kind):
+    w, ws = weights(1, N, K)
+    x, xs, x64, off = tokens(2, T, K, kind)
+    out, work = product(x, xs, w, ws, T, N, K, kind)
+    moe.check_device_status(work)
+    check(out, x64, off, values(w, ws))
+
+
+def test_linear_out_rows_past_32_bit_offsets():
+    T, N, K = 5, 136, 256
+    stride = (1 << 29) + 8                              # the last row begins past 2^31 elements
+    w, ws = weights(1, N, K)
+    for kind in ("bf16", "mxfp4"):
+        x, xs, x64, off = tokens(2, T, K, kind)
+        big = torch.full((T * stride,), -77.0, dtype=torch.bfloat16, device=DEV)
+        out = big.as_strided((T, N), (stride, 1))
+        product(x, xs, w, ws, T, N, K, kind, out=out, out_stride=stride)
+        check(out, x64, off, values(w, ws))
+        out.fill_(-77.0)
+        assert (big == -77.0).all()
+
+
+def test_linear_on_two_streams_at_once():
+    # every way of sharing the work out, beside another call on another stream
+    cases = [(8, 7168, 4096, "mxfp4"), (5, 20000, 4096, "bf16"), (600, 2048, 1024, "bf16"), (300, 6144, 2048, "mxfp4"),
+             (100, 1024, 4096, "bf16"), (1000, 1536, 512, "mxfp4")]
+    data = []
+    for i, (T, N, K, kind) in enumerate(cases):
+        w, ws = weights(i, N, K)
+        x, xs, _, _ = tokens(i, T, K, kind)
+        shape = moe.MXShape.of(T, N, K, x_mxfp4=kind == "mxfp4")
+        outs = [torch.empty(T, N, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+        data.append((shape, x, xs, w, ws, outs, [moe.new_mx_workspace(shape) for _ in range(3)]))
+    for shape, x, xs, w, ws, outs, works in data:
+        moe.mx_linear(shape, x, xs, w, ws, outs[2], works[2])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    for _ in range(10):
+        for k, stream in enumerate(streams):
+            for i in range(len(data)):
+                shape, x, xs, w, ws, outs, works = data[(i + 3 * k) % len(data)]
+                moe.mx_linear(shape, x, xs, w, ws, outs[k], works[k], stream)
+        torch.cuda.synchronize()
+        for shape, x, xs, w, ws, outs, works in data:
+            assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+    for d in data:
+        for work in d[-1]:
+            moe.check_device_status(work)
+
+
+def test_two_graphs_share_a_workspace():
+    T1, N1, K1, T2, N2, K2 = 5, 20000, 4096, 40, 1000, 2176
+    a, b = moe.MXShape.of(T1, N1, K1), moe.MXShape.of(T2, N2, K2)
+    work = moe.new_mx_workspace(max((a, b), key=moe.mx_workspace_bytes))
+    (w1, s1), (w2, s2) = weights(1, N1, K1), weights(2, N2, K2)
+    x1, x2 = tokens(1, T1, K1, "bf16")[0], tokens(2, T2, K2, "bf16")[0]
+    o1, o2 = torch.empty(T1, N1, dtype=torch.bfloat16, device=DEV), torch.empty(T2, N2, dtype=torch.bfloat16, device=DEV)
+
+    def first():
+        moe.mx_linear(a, x1, None, w1, s1, o1, work)
+
+    def second():
+        moe.mx_linear(b, x2, None, w2, s2, o2, work)
+
+    graphs = []
+    for call in (first, second):
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    want = o1.clone(), o2.clone()
+    for i in (0, 1, 1, 0, 0, 1):
+        (o1, o2)[i].zero_()
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, want[0]) and torch.equal(o2, want[1])
+    moe.check_device_status(work)
