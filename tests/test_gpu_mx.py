@@ -404,7 +404,8 @@ def test_linear_few_tokens_that_are_not_finite(T, bad):
     moe.check_device_status(work)
     keep = [t for t in range(T) if t != bad]
     assert out[bad].isnan().all()
-    check(out[keep], x64[keep], off[keep], values(w, ws))
+    if keep:
+        check(out[keep], x64[keep], off[keep], values(w, ws))
 
 
 @pytest.mark.parametrize("T,N,K,kind", [(1 << 20, 8, 128, "bf16"), (1 << 20, 8, 128, "mxfp4"), (1, 1 << 20, 128, "bf16"),
