@@ -69,17 +69,18 @@ struct LCfg {
     static constexpr int SF_SLOT = WORDS * 32, SF_B = WORDS * 16;
     static constexpr int SF_COL0 = (ACC * NB + 63) / 64 * 64;
     static constexpr int S_TMEM = (512 - SF_COL0) / SF_SLOT;
-    // scales on their way to TMEM: a pair's token scales of 1024 K, exchanged between threads, twice; else RING
+    // scales on their way to TMEM: a pair's groups of 1024 K, [8 words][rows], twice; else RING
     // groups of 512 K (RING / SETS a set), a row of weights or tokens 16 bytes (or half as many of twice the bytes, where the rows in
     // memory are not 16-byte aligned: the two aligned pieces that hold them)
     static constexpr int RING = SETS == 2 && !FUSED ? 8 : 4;
-    static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * NT * 4 : RING * (LM + NT) * 16 + (FUSED ? SETS * 2 * NT * 8 : 0);
+    static constexpr int XCH_BYTES = CG == 2 ? 2 * 8 * (LM + NT + 8) * 4 : RING * (LM + NT) * 16 + (FUSED ? SETS * 2 * NT * 8 : 0);
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
     // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
-    static constexpr int S = S_FIT < S_TMEM ? S_FIT : S_TMEM;
+    // (nor is a pair with a bf16 x faster with four stages than with three)
+    static constexpr int S = TERMS == 2 ? 3 : S_FIT < S_TMEM ? S_FIT : S_TMEM;
     static constexpr int SMEM = 1024 + S * STAGE + XCH_BYTES + 512;
-    static_assert(S >= 2 && SMEM <= 232448, "stages");
+    static_assert(S >= 2 && S <= S_FIT && SMEM <= 232448, "stages");
     static_assert(CG == 1 || NT == 256, "a pair's tile is 256 x 256");
 };
 
@@ -157,27 +158,6 @@ struct Segment {
         if (more()) place();
     }
 };
-
-// Scale bytes 32 g .. 32 g + 31 of a row (1024 K); past the row's end 127 (its codes are zeros).
-__device__ __forceinline__ void load_scales(const uint8_t* row, int g, int kb, bool vec, uint32_t (&w)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 0x7F7F7F7Fu;
-    if (row == nullptr) return;
-    row += 32 * g;
-    const int n = kb - 32 * g;
-    if (vec) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (16 * i < n) {
-                const uint4 v = ld_dep(reinterpret_cast<const uint4*>(row) + i);
-                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-            }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (4 * i < n) w[i] = ld_dep(reinterpret_cast<const uint32_t*>(row) + i);
-    }
-}
 
 template <bool XMX, int NT, int CG>
 __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
@@ -364,42 +344,52 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         }
         ptx::mbar_wait_all(fin, 0, abort_flag, L_WAIT_NS);
     } else if (warp < 6 && PAIR) {
-        // ------------------------------------------------------------ scales, of a pair: a group of 1024 K ahead in registers
-        const int q = warp & 3, r = 32 * q + lane;      // TMEM lane quarter; weight row of this thread
+        // ------------------------------------------------------------ scales of a pair: groups of 1024 K, the next one ahead
+        // in registers.  Eight lanes load a row's 32 bytes: a lane a row, which takes two to eight requests a
+        // row instead of one, held up the TMA's (T = 4096, N = 6144, K = 4096, MXFP4 x: 51 us against 46)
+        const int q = warp & 3, word = lane & 7, sub = lane >> 3;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const int kb = a.K / 32;
-        constexpr int PG = 8 / WORDS;                                 // stages of a group of 1024 K
-        constexpr int OWN = NT >= 128 ? NT / 128 : 1;                 // tokens whose scales this thread loads
+        constexpr int PG = 8 / WORDS;                                 // stages of a group
+        constexpr int PT = 256;                                       // (NT)
+        constexpr int NA = LM / 16, NR = PT / 16;                     // rows of weights, tokens a thread loads a word of
+        constexpr int SA = LM + 4, SB = PT + 4;                       // (4: the lanes' stores fall into different banks)
         const uint32_t full0 = ptx::map_cluster(full, 0);
-        uint32_t wa[8], wb[OWN][8], na[8], nb[OWN][8];
-        auto load_a = [&](const Segment<CG>& g, int grp) {
-            const int row = (g.m * CG + rank) * LM + r;
-            load_scales(row < a.N ? a.w_scales + (int64_t)row * kb : nullptr, grp, kb, a.vec, na);
-        };
-        auto load_b = [&](const Segment<CG>& g, int grp) {
+        uint32_t na[NA], nb[NR];
+        // bytes 32 grp + 4 word .. + 3 of rows 4 i + sub of this warp's part; past the tensor's ends 127 (its codes are zeros)
+        auto load = [&](const uint8_t* from, int row0, int rows, int grp, auto& to) {
+            const bool in = 32 * grp + 4 * word < kb;
 #pragma unroll
-            for (int u = 0; u < OWN; ++u) {
-                const int j = r + 128 * u;
-                const int t = g.t * a.nt + j;
-                load_scales(t < a.T ? a.xs + (int64_t)t * kb : nullptr, grp, kb, a.vec, nb[u]);
+            for (int i = 0; i < (int)(sizeof(to) / 4); ++i) {
+                const int row = row0 + 4 * i + sub;
+                to[i] = in && row < rows
+                            ? ld_dep(reinterpret_cast<const uint32_t*>(from + (int64_t)row * kb + 32 * grp + 4 * word))
+                            : 0x7F7F7F7Fu;
             }
         };
+        auto load_a = [&](const Segment<CG>& g, int grp) { load(a.w_scales, (g.m * CG + rank) * LM + q * (LM / 4), a.N, grp, na); };
+        auto load_b = [&](const Segment<CG>& g, int grp) { load(a.xs, g.t * a.nt + q * (PT / 4), a.T, grp, nb); };
         Segment<CG> g(a);
-        if (g.more()) load_a(g, g.k0 / PG);
+        if (g.more()) load_a(g, 0);
         if (!XMX) pdl_wait();
-        if (g.more()) load_b(g, g.k0 / PG);
+        if (g.more()) load_b(g, 0);
         // a warp whose wait gave up goes on without waiting: the four share the barrier below
         int s = 0, buf = 0;
         uint32_t par = 1;
         bool ok = true;
         for (; g.more(); g.next()) {
-            for (int grp = g.k0 / PG; PG * grp < g.k1; ++grp) {
+            for (int grp = 0; PG * grp < g.k1; ++grp) {
+                uint32_t* xa = reinterpret_cast<uint32_t*>(xch) + buf * 8 * (SA + SB);
+                uint32_t* xb = xa + 8 * SA;
+                uint32_t nan = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    wa[i] = na[i];
-#pragma unroll
-                    for (int u = 0; u < OWN; ++u) wb[u][i] = nb[u][i];
+                for (int i = 0; i < NA; ++i) {
+                    nan |= __vcmpeq4(na[i], 0xFFFFFFFFu);
+                    xa[word * SA + q * (LM / 4) + 4 * i + sub] = na[i];
                 }
+#pragma unroll
+                for (int i = 0; i < NR; ++i) xb[word * SB + q * (PT / 4) + 4 * i + sub] = nb[i];
+                if (nan) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 // the next group's, under way while this one's stages go through
                 if (PG * (grp + 1) < g.k1) {
                     load_a(g, grp + 1);
@@ -412,41 +402,33 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                         load_b(n, 0);
                     }
                 }
-                uint32_t nan = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) nan |= __vcmpeq4(wa[i], 0xFFFFFFFFu);
-                if (nan) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
-                uint32_t* xb = reinterpret_cast<uint32_t*>(xch) + buf * 8 * NT;
-#pragma unroll
-                for (int u = 0; u < OWN; ++u)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) xb[i * NT + r + 128 * u] = wb[u][i];
                 // (one barrier a group: a buffer is written again two groups later)
                 ptx::named_bar_sync(1, 128);
                 buf ^= 1;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < PG; ++i) {
-                    const int k = PG * grp + i;
-                    if (!ok || k < g.k0 || k >= g.k1) continue;
+                    if (!ok || PG * grp + i >= g.k1) break;
+                    uint32_t w[WORDS], v[WORDS][PT / 32];
+#pragma unroll
+                    for (int h = 0; h < WORDS; ++h) {
+                        w[h] = xa[(WORDS * i + h) * SA + 32 * q + lane];
+#pragma unroll
+                        for (int c = 0; c < PT / 32; ++c) v[h][c] = xb[(WORDS * i + h) * SB + 32 * c + lane];
+                    }
                     if (!ptx::mbar_wait_all(&empty[s], par, abort_flag, L_WAIT_NS)) {
                         if (lane == 0) fail(4);
                         ok = false;
-                        continue;
+                        break;
                     }
                     ptx::tc_fence_after();
                     const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
 #pragma unroll
                     for (int h = 0; h < WORDS; ++h) {
-                        const int w = WORDS * i + h;
                         // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
-                        // word into all four columns; the other quarters' are never read)
-                        ptx::tmem_st4_rep(col + 16 * h, wa[w]);
-                        // column n of B: lane n mod 32 of every quarter, column + n / 32
-                        const uint32_t to = col + C::SF_B + 16 * h;
-                        uint32_t v[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = xb[w * NT + 32 * c + lane];
-                        ptx::tmem_st8(to, v);
+                        // word into all four columns; the other quarters' are never read); column n of B:
+                        // lane n mod 32 of every quarter, column + n / 32
+                        ptx::tmem_st4_rep(col + 16 * h, w[h]);
+                        ptx::tmem_st8(col + C::SF_B + 16 * h, v[h]);
                     }
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
@@ -933,7 +915,7 @@ Tiling tiling(const MxDims& d) {
     for (int nt = 64; nt <= 256; nt += 32) {
         const int64_t tiles = (int64_t)((d.N + 2 * LM - 1) / (2 * LM)) * ((d.T + nt - 1) / nt);
         const int64_t rounds = (tiles + L_CTAS / 2 - 1) / (L_CTAS / 2);
-        if (d.x_mx) take(6.6f + 0.45f * (rounds * nk), {2, nt, 1, false});
+        if (d.x_mx) take(6.3f + 0.41f * (rounds * nk), {2, nt, 1, false});
         else take(6.5f + (0.235f + 0.00182f * nt) * (rounds * (d.K / 128)), {2, nt, 1, false});
     }
     return best;
