@@ -90,7 +90,7 @@ extern "C" {
 #define MOE_ERR_BAD_IDS           -7  /* device: an expert id outside [0, E) */
 #define MOE_ERR_BAD_SCALE         -8  /* device: an e8m0 scale byte of 255 (NaN) */
 #define MOE_ERR_NO_DEVICE         -9  /* current device is not sm_103 (GB300), or has too few SMs (moe_tree_attention) */
-#define MOE_ERR_BAD_LENGTHS      -10  /* device: a request's length is negative or does not fit */
+#define MOE_ERR_BAD_LENGTHS      -10  /* device: a request's length is negative or does not fit; a position past its table */
 #define MOE_ERR_NO_PAGES         -11  /* device: the list of free pages is too short */
 #define MOE_ERR_BAD_PARENT       -12  /* device: a drafted token's parent is not an earlier one */
 #define MOE_ERR_BAD_PAGE         -13  /* device: a page id or slot outside the cache */
@@ -507,7 +507,8 @@ int moe_mx_quantize(int64_t rows, int32_t K, int dtype, const void* x, int64_t x
 
 /*
  * MXFP4 rows to y [rows, K] of type dtype, rows y_stride elements apart (as
- * above): code * scale, exact in fp32 and rounded to the type (to nearest even).
+ * above): code * scale, exact in fp32 (an infinity past its range, NaN under byte
+ * 255) and rounded to the type (to nearest even).
  */
 int moe_mx_dequantize(int64_t rows, int32_t K, int dtype, const uint8_t* codes, const uint8_t* scales, void* y,
                       int64_t y_stride, void* stream);
@@ -538,7 +539,8 @@ int moe_mx_workspace_bytes(const moe_mx_shape* shape, size_t* bytes);
  *   out [T, N] bf16
  * The products are exact in fp32 but for a bf16 x, whose elements enter as two
  * e4m3 terms under a power of two a block of 32 (see the top): exact down to
- * 2^-9 of the block's largest magnitude, below that within 2^-17 of it.  A row of x
+ * 2^-9 of the block's largest magnitude, below that within 2^-17 of it.  Sums whose
+ * magnitude is below 2^-126 may come out as 0.  A row of x
  * with a NaN or an infinity (MXFP4: a scale byte of 255) gives a row of NaN.
  * Device errors: MOE_ERR_BAD_SCALE (a scale byte of 255 in w: its column of out
  * is NaN), MOE_ERR_TIMEOUT (the workspace is then prepared again).

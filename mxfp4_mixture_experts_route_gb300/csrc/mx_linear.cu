@@ -10,21 +10,29 @@
 //
 // Few tokens: one CTA a tile of 128 weight rows x NT tokens; a token of a bf16 x takes
 // two columns of the MMA, added at the end.  Many: a pair of CTAs (cta_group::2) a tile of
-// 256 weight rows x 256 tokens, of which each holds half of either operand; the terms of
-// a bf16 x are two MMAs into one accumulator.
+// 256 weight rows x up to 256 tokens, of which each holds half of either operand (half the bytes a
+// product that two single CTAs would copy); the terms of a bf16 x are two MMAs into one accumulator.
 //
-// How the tiles' stages (KS elements of K) are shared out:
+// How the tiles' stages (KS elements of K) are shared out (tiling() chooses):
 //   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; the parts are
-//     added through the cluster's shared memory;
+//     added through the cluster's shared memory (T = 8, N = 7168, K = 4096, MXFP4 x: 6.7 us, by way of global
+//     memory 10.9);
 //   - else the persistent CTAs (pairs) take whole tiles in turn;
-//   - where a last round of them would leave much idle, the last tiles stand one after the other on a
-//     line of which every CTA (pair) takes an equal share.  A tile that a cut divides is
+//   - where a last round of single CTAs would leave much idle, the last tiles stand one after the other on a
+//     line of which every CTA takes an equal share.  A tile that a cut divides is
 //     joined without waiting: every CTA writes its part to the workspace and counts itself,
 //     and the one that comes last adds the parts in the order of the line (so the sum does
-//     not depend on who came last).
+//     not depend on who came last).  A pair's tile is too large for that (T = 1024, N = 6144, K = 4096: 32 us on the
+//     line): it takes fewer tokens instead, so that the tiles fill their rounds.
 //
-// Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> TMEM, 1024 K ahead in
-// registers), 6 on the accumulators' way out: four, or eight of a pair's CTA.
+// What bounds it: up to some dozen tokens the weights' bytes from HBM (N = 16384, K = 8192: 71 MB in 13.6 us) and, for small
+// products, the chain of a launch (0.5 us to the first copy, 1.5 to the first MMA, 1.5 for the sum over a
+// cluster); with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 95 us, 1719 TFLOP/s, 0.88 of the
+// measured bf16 rate); with both operands at 4 bits the copies, scales and stores beside MMAs that alone
+// take 197 of 273 us (8192 x 14336 x 7168: 6166 TFLOP/s).
+//
+// Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> shared memory or registers -> TMEM), from 6 on the accumulators' way
+// out (four, or eight of a pair's CTA), then a second set of scale warps.
 #include "mx.cuh"
 #include "quant.cuh"
 #include "tc_ptx.cuh"
@@ -719,59 +727,59 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 continue;
             }
             if constexpr (!PAIR) {
-            constexpr int64_t PART = (int64_t)NT * LM;
-            auto part_of = [&](int c, int slot) { return a.parts + ((int64_t)c * 2 + slot) * PART; };
-            float* part = part_of(me, g.k0 == 0) + r;
+                constexpr int64_t PART = (int64_t)NT * LM;
+                auto part_of = [&](int c, int slot) { return a.parts + ((int64_t)c * 2 + slot) * PART; };
+                float* part = part_of(me, g.k0 == 0) + r;
 #pragma unroll 1
-            for (int t = first; t < mine; t += G) {
-                float y[G];
-                read(ab, t, y);
+                for (int t = first; t < mine; t += G) {
+                    float y[G];
+                    read(ab, t, y);
 #pragma unroll
-                for (int j = 0; j < G; ++j)
-                    if (t + j < mine) part[(t + j) * LM] = y[j];
-            }
-            release(ab);
-            // the tile's parts: those of workers c0 .. c1
-            const int64_t p0 = (int64_t)(g.tile - a.waves * workers) * a.nk;
-            const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + a.nk - 1, a.total, workers);
-            __threadfence();
-            ptx::named_bar_sync(2, 32 * C::EW);
-            if (threadIdx.x == 6 * 32) {
-                uint32_t* count = a.count + c0;
-                const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
-                if (last) *count = 0;
-                __threadfence();
-                last_flag[0] = last;
-            }
-            ptx::named_bar_sync(2, 32 * C::EW);
-            if (!last_flag[0]) continue;
-            // four rows a lane, a token a warp at a time; J tokens' loads under way together
-            constexpr int J = NT / C::EW < 16 ? NT / C::EW : 16;
-            const int row4 = row0 + 4 * lane;
-#pragma unroll 1
-            for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
-                float4 y[J];
-#pragma unroll
-                for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-                for (int c = c0; c <= c1; ++c) {
-                    const float* from = part_of(c, c == c0) + 4 * lane;
-                    float4 v[J];
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        v[j] = tb + C::EW * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + C::EW * j) * LM))
-                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        y[j].x += v[j].x, y[j].y += v[j].y, y[j].z += v[j].z, y[j].w += v[j].w;
+                    for (int j = 0; j < G; ++j)
+                        if (t + j < mine) part[(t + j) * LM] = y[j];
                 }
+                release(ab);
+                // the tile's parts: those of workers c0 .. c1
+                const int64_t p0 = (int64_t)(g.tile - a.waves * workers) * a.nk;
+                const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + a.nk - 1, a.total, workers);
+                __threadfence();
+                ptx::named_bar_sync(2, 32 * C::EW);
+                if (threadIdx.x == 6 * 32) {
+                    uint32_t* count = a.count + c0;
+                    const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
+                    if (last) *count = 0;
+                    __threadfence();
+                    last_flag[0] = last;
+                }
+                ptx::named_bar_sync(2, 32 * C::EW);
+                if (!last_flag[0]) continue;
+                // four rows a lane, a token a warp at a time; J tokens' loads under way together
+                constexpr int J = NT / C::EW < 16 ? NT / C::EW : 16;
+                const int row4 = row0 + 4 * lane;
+#pragma unroll 1
+                for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
+                    float4 y[J];
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (tb + C::EW * j < n_tok && row4 < a.N)
-                        *reinterpret_cast<uint2*>(a.out + (t0 + tb + C::EW * j) * a.out_stride + row4) =
-                            make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
-            }
-            ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
+                    for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* from = part_of(c, c == c0) + 4 * lane;
+                        float4 v[J];
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            v[j] = tb + C::EW * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + C::EW * j) * LM))
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            y[j].x += v[j].x, y[j].y += v[j].y, y[j].z += v[j].z, y[j].w += v[j].w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (tb + C::EW * j < n_tok && row4 < a.N)
+                            *reinterpret_cast<uint2*>(a.out + (t0 + tb + C::EW * j) * a.out_stride + row4) =
+                                make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
+                }
+                ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
             }
         }
     }
@@ -886,9 +894,9 @@ constexpr int LINE = 10;
 // stages, and sharing K `join` (us).  The numbers were fitted to measurements over T = 1 .. 8192, which they
 // meet within 10%: with operands in L2 a single CTA's stage (256 K) takes about the same for 8 tokens as for 128
 // (its copies' latency), a pair's of MXFP4 x too, whatever its tokens; a pair's of a bf16 x (128 K) grows with
-// them.  For instance T = 512, N = 6144, K = 4096, MXFP4 x: tiles of 128 tokens 22.4 us, pairs with 192 13.8,
-// with 256 14.8; T = 128, N = 4096: 64 tokens and two CTAs a tile 8.7 us, 32 tokens and one 10.0; bf16
-// x, T = 4096: pairs with 224 tokens 127 us, with 256 140, with 128 158.
+// them.  For instance T = 512, N = 6144, K = 4096, MXFP4 x: tiles of 128 tokens 22.4 us, pairs with 192 12.6,
+// with 256 14; T = 128, N = 4096: 64 tokens and two CTAs a tile 8.7 us, 32 tokens and one 10.0; bf16
+// x, T = 4096: pairs with 224 tokens 121 us, with 256 134, with 128 152.
 Tiling tiling(const MxDims& d) {
     struct Single {
         int nt;
@@ -909,7 +917,8 @@ Tiling tiling(const MxDims& d) {
         for (int n = 2; n <= 8 && n <= nk; ++n)
             if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), {1, c.nt, n, false});
         take(c.start + c.stage * (rounds * nk), {1, c.nt, 1, false});
-        take(c.start + c.stage * ((float)(tiles * nk) / L_CTAS + LINE), {1, c.nt, 1, true});
+        // (with fewer tiles the parts of each would be many)
+        if (tiles > CLUSTERS[2]) take(c.start + c.stage * ((float)(tiles * nk) / L_CTAS + LINE), {1, c.nt, 1, true});
         if (c.nt >= d.T) break;
     }
     for (int nt = 64; nt <= 256; nt += 32) {
