@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         auto advance = [&](Segment<CG>& g, int& grp) {
             if (2 * ++grp >= g.k1) {
                 g.next();
-                grp = 0;
+                grp = g.k0 / 2;   // (the line may begin within a tile)
             }
         };
         // to the set's next group

@@ -229,6 +229,21 @@ def test_linear(T, N, K, kind):
     check(out, x64, off, values(w, ws))
 
 
+@pytest.mark.parametrize("T,N,K,kind", [
+    (1, 39680, 4096, "mxfp4"), (8, 40008, 3968, "mxfp4"), (30, 39680, 4096, "mxfp4"), (50, 39680, 4096, "mxfp4"),
+    (100, 39688, 4096, "mxfp4"), (4, 39680, 4096, "bf16"), (8, 39688, 4096, "bf16"), (12, 40008, 3968, "bf16"),
+    (30, 39680, 4096, "bf16"), (60, 39680, 4096, "bf16"), (40, 19848, 4224, "mxfp4")])
+def test_linear_line_behind_whole_tiles(T, N, K, kind):
+    # more than two rounds of tiles, the last ones cut anywhere: a worker goes from a whole tile into the middle of another
+    w, ws = weights(N + K, N, K)
+    x, xs, x64, off = tokens(T + K, T, K, kind)
+    first, work = product(x, xs, w, ws, T, N, K, kind)
+    again, _ = product(x, xs, w, ws, T, N, K, kind, work=work)
+    moe.check_device_status(work, "mx_linear")
+    assert torch.equal(first, again)
+    check(first, x64, off, values(w, ws))
+
+
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
 def test_linear_places_every_element(kind):
     # one element of x and of w at a time reaches the one place of out it belongs to
