@@ -487,6 +487,7 @@ int moe_qkv_append(const moe_kv_shape* shape, const moe_rope* rope, const void* 
 /* ------------------------------------------------------------------------
  * Dense MXFP4: a layer's projections in the experts' weight format.  Rows are
  * packed as w13 and w2 are (see the top): codes [rows, K/2] and scale bytes [rows, K/32].
+ * What a call writes stands apart from what it reads.
  */
 #define MOE_BF16 0
 #define MOE_F16  1

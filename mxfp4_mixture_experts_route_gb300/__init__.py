@@ -359,7 +359,7 @@ def _mx_rows(t, codes, scales):
         _mx_types.update({torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32})
     dt = _mx_types.get(t.dtype)
     n = t.numel()
-    if dt is None or not n:
+    if dt is None or not n or not t.dim():
         raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (bf16, fp16 or fp32)")
     K = t.shape[-1]
     stride = 0

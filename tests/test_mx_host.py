@@ -137,3 +137,12 @@ def test_binding_refuses_rows_it_cannot_describe():
         with pytest.raises(moe.MoEError) as e:
             moe.mx_dequantize(codes, scales, torch.empty(4, 64))
         assert e.value.code == INVALID
+
+
+def test_binding_refuses_what_has_no_rows():
+    torch = pytest.importorskip("torch")
+    c, s = torch.empty(4, 32, dtype=torch.uint8), torch.empty(4, 2, dtype=torch.uint8)
+    for x in (torch.tensor(1.0), torch.empty(0, 64)):
+        with pytest.raises(moe.MoEError) as e:
+            moe.mx_quantize(x, c, s)
+        assert e.value.code == INVALID
