@@ -14,7 +14,6 @@ namespace moe {
 namespace {
 
 constexpr int QKV_THREADS = 128;
-constexpr int QKV_WARPS = 16;                 // warps of an SM that still start at once
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -31,14 +30,18 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 }
 
 // LPH lanes a head; a warp takes CH heads of one kind (query, key or value) of one token, 32 / LPH side by side, U
-// of each group of lanes loaded at a time.
+// of each group of lanes loaded at a time.  With most heads a warp is a block of its own, a token's
+// next to one another: a block of all of them holds its place until the last one (often one of query heads beside
+// two of few key and value heads) is done, and 64 registers let 32 blocks run at once (16,411 rows of 56 + 2 x 8 heads:
+// to bf16 102 us, in blocks of four warps 112, with 71 registers 116; a token's warps far apart in the grid 117).
+constexpr bool lone(int heads) { return heads == 32; }
 template <int LPH, int CH, int U, bool E4M3, bool INTER>
-__global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, const QkvArgs a) {
+__global__ void __launch_bounds__(lone(CH) ? 32 : QKV_THREADS, lone(CH) ? 32 : 1) k_qkv_append(const KvDims d, const QkvArgs a) {
     constexpr int D = LPH * 8, SIDE = 32 / LPH;
     constexpr bool STAGED = CH == 8 || CH == 16;
     const int qc = (d.Hq + CH - 1) / CH, kc = (d.Hkv + CH - 1) / CH, chunks = qc + 2 * kc;
-    const int t = blockIdx.x;
-    int c = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
+    const int t = lone(CH) ? blockIdx.x / chunks : blockIdx.x;
+    int c = lone(CH) ? blockIdx.x - t * chunks : blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
     const int p = threadIdx.x % LPH;                 // the lane's piece of the head
     KT_MARK(K_QKV_APPEND, 0);
     pdl_wait();
@@ -85,8 +88,8 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
     if (live) load(h0);
 
     // the token's angles and the weights: by way of shared memory, once a block instead of once a warp, where a warp has
-    // some heads (500 rows of 56 + 2 x 8: 5.4 us, without 7.3; with fewer heads its latency counts, with more
-    // it gains nothing: 16,411 rows 122 us, without 116)
+    // some heads (500 rows of 56 + 2 x 8: 5.1 us, without 7.3; with fewer heads its latency counts, with more
+    // it gains nothing: 16,411 rows in blocks of four warps 122 us, without 116)
     const float *w = what == 0 ? a.q_norm : a.k_norm, *row = a.cos_sin + (int64_t)pos * a.R;
     if constexpr (STAGED) {
         __shared__ float4 stage[3][D / 4];
@@ -179,10 +182,10 @@ __global__ void __launch_bounds__(QKV_THREADS) k_qkv_append(const KvDims d, cons
 
 template <int LPH, int CH, int U>
 cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
-    // a token's warps in equal blocks
+    // a token's warps in equal blocks, or a block each
     const int chunks = (d.Hq + CH - 1) / CH + 2 * ((d.Hkv + CH - 1) / CH);
     const int ny = (chunks * 32 + QKV_THREADS - 1) / QKV_THREADS;
-    const dim3 grid(d.T, ny), block((chunks + ny - 1) / ny * 32);
+    const dim3 grid = lone(CH) ? dim3((unsigned)d.T * chunks) : dim3(d.T, ny), block(lone(CH) ? 32 : (chunks + ny - 1) / ny * 32);
     if (d.e4m3)
         return a.interleaved ? launch_pdl(k_qkv_append<LPH, CH, U, true, true>, grid, block, 0, st, d, a)
                              : launch_pdl(k_qkv_append<LPH, CH, U, true, false>, grid, block, 0, st, d, a);
@@ -190,16 +193,17 @@ cudaError_t launch_heads(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
                          : launch_pdl(k_qkv_append<LPH, CH, U, false, false>, grid, block, 0, st, d, a);
 }
 
-// The heads of a warp: two to four while the warps fit one round of the SMs (short chains), more where the angles and
-// weights that every warp needs come to count (rows of 56 + 2 x 8 heads to bf16: 32 rows 3.0 us with two, 3.9 with 16; 128
-// rows 3.5 with 8, 4.2 with 4 and with 16; 500 rows 5.4 with 16, 7.0 with 8 and with 32; 16,411 rows 116 with 32, 128 with 16).
+// The heads of a warp: two to four while an SM has few warps (short chains), more where the angles and
+// weights that every warp needs come to count (rows of 56 + 2 x 8 heads to bf16: 32 rows 2.8 us with two, 3.0 with 8; 64 rows 4.1 and
+// 3.3; 200 rows 3.6 with 8, 4.2 with 16; 500 rows 6.7 and 5.1; 1000 rows 9.7 with 16, 12.2 with 32; 3000 rows 25.0 and 24.6; of
+// 32 + 2 x 4 heads to e4m3: 3000 rows 21.7 and 19.0).
 template <int LPH>
 cudaError_t launch_lph(const KvDims& d, const QkvArgs& a, cudaStream_t st) {
     constexpr int SIDE = 32 / LPH;
-    const int64_t heads = (int64_t)d.T * (d.Hq + 2 * d.Hkv), most = (int64_t)num_sms() * QKV_WARPS;
-    if (heads <= most * SIDE) return launch_heads<LPH, SIDE, 1>(d, a, st);
-    if (heads <= most * 8) return launch_heads<LPH, 8, 2>(d, a, st);
-    if (heads <= most * 64) return launch_heads<LPH, 16, 2>(d, a, st);
+    const int64_t heads = (int64_t)d.T * (d.Hq + 2 * d.Hkv), sms = num_sms();
+    if (heads <= sms * 10 * SIDE) return launch_heads<LPH, SIDE, 1>(d, a, st);
+    if (heads <= sms * 128) return launch_heads<LPH, 8, 2>(d, a, st);
+    if (heads <= sms * 768) return launch_heads<LPH, 16, 2>(d, a, st);
     return launch_heads<LPH, 32, 2>(d, a, st);
 }
 

@@ -121,6 +121,20 @@ def test_qkv_append(kw, inter, e4m3):
     c.check()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(T=2000, Hq=56, Hkv=8, D=128, R=128), dict(T=2000, Hq=56, Hkv=8, D=128, R=128, e4m3=True),
+    dict(T=1300, Hq=99, Hkv=3, D=128, R=64, inter=True, in_place=True), dict(T=4001, Hq=33, Hkv=3, D=64, R=64, e4m3=True, odd_cache=True),
+    dict(T=1501, Hq=8, Hkv=8, D=128, R=0, norm=""), dict(T=12001, Hq=6, Hkv=2, D=64, R=48, inter=True, e4m3=True),
+    dict(T=2100, Hq=40, Hkv=40, D=64, R=64, fused=False)], ids=str)
+def test_many_heads(kw):
+    c = Case(**kw, seed=9)
+    c.pos[1] = c.pos[kw["T"] - 2] = -1
+    c.slots[2] = -1
+    c.run()
+    moe.check_device_status(c.ws)
+    c.check()
+
+
 @pytest.mark.parametrize("kw", [dict(norm=""), dict(norm="q"), dict(norm="k"), dict(in_place=True), dict(fused=False),
                                 dict(fused=False, in_place=True), dict(odd_cache=True), dict(odd_cache=True, e4m3=True),
                                 dict(page=1024, e4m3=True), dict(R=0, norm="")], ids=str)
