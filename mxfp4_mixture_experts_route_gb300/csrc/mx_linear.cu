@@ -92,6 +92,20 @@ struct LCfg {
     static_assert(CG == 1 || NT == 256, "a pair's tile is 256 x 256");
 };
 
+// n / d for 0 <= n < 2^31 as a product and a shift: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), n m 2^-(31 + s)
+// exceeds n / d by n e / (d 2^(31 + s)), 0 <= e < d <= 2^s, which is less than 1 / d.  (Divisions on the way
+// to the first MMA took 0.6 us of a launch's 6.7.)
+struct Div {
+    uint32_t mul;
+    int shift;
+    Div() = default;
+    explicit Div(uint32_t d) : shift(31) {
+        while (((uint32_t)1 << (shift - 31)) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
 struct LArgs {
     const uint8_t *w_scales, *xs;             // [N][K/32], [T][K/32]
     __nv_bfloat16* out;
@@ -104,14 +118,16 @@ struct LArgs {
     int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
     int split;                                // CTAs of a cluster that share a tile, or 1
     int tiles, waves;                         // whole tiles that every worker takes first, if there is a line
-    int64_t total;                            // stages on the line, which begins behind those tiles, or 0
+    int total;                                // stages on the line, which begins behind those tiles, or 0
     int vec;                                  // scale rows are 16-byte aligned
     int w_once;
+    Div workers, by_split, by_nk, by_total, by_band, by_last;   // (by_band: tiles of a band, by_last: weight tiles of the last one)
 };
 
 // the first stage of worker c's share of the line (of n), and the worker that holds stage p
-__device__ __forceinline__ int64_t share(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int holder_of(int64_t p, int64_t total, int n) { return (int)(((p + 1) * n - 1) / total); }
+// (total < 2 * 152 * 256 stages: the products are ordinary integers)
+__device__ __forceinline__ int share(const LArgs& a, int c) { return a.workers.of(a.total * c); }
+__device__ __forceinline__ int holder_of(const LArgs& a, int p, int n) { return a.by_total.of((p + 1) * n - 1); }
 
 // A worker's segments: stages [k0, k1) of tile (m, t), one after the other: `waves` whole tiles, then its share
 // of the line.  Tiles are numbered through bands of GM weight tiles, so that those that are worked on at one
@@ -119,45 +135,50 @@ __device__ __forceinline__ int holder_of(int64_t p, int64_t total, int n) { retu
 template <int CG>
 struct Segment {
     static constexpr int GM = 8;
-    int64_t left;                // stages of the share to go
+    int left;                    // stages of the share to go
     int tile, m, t, k0, k1, waves;
     const LArgs& a;
     __device__ __forceinline__ explicit Segment(const LArgs& args) : left(0), waves(args.waves), a(args) {
-        const int c = blockIdx.x / CG, n = gridDim.x / CG;
+        const int c = blockIdx.x / CG;
         tile = c;
         k0 = 0;
-        if (a.split > 1) {
-            const int part = c % a.split;
-            tile = c / a.split;
+        if (CG == 1 && a.split > 1) {
+            const int part = ptx::cluster_rank();
+            tile = ptx::cluster_id();
             waves = 0;
-            k0 = a.nk * part / a.split;
-            left = a.nk * (part + 1) / a.split - k0;
+            k0 = a.by_split.of(a.nk * part);
+            left = a.by_split.of(a.nk * (part + 1)) - k0;
         } else if (a.total == 0) {
-            waves = (a.tiles - c + n - 1) / n;
+            waves = a.workers.of(a.tiles - c + gridDim.x / CG - 1);
         } else {
-            const int64_t at = share(a.total, c, n);
-            left = share(a.total, c + 1, n) - at;
+            const int at = share(a, c);
+            left = share(a, c + 1) - at;
             if (waves == 0) to_line(at);
         }
         place();
     }
-    __device__ __forceinline__ void to_line(int64_t at) {
-        tile = (int)(at / a.nk);
-        k0 = (int)(at - (int64_t)tile * a.nk);
+    __device__ __forceinline__ void to_line(int at) {
+        tile = a.by_nk.of(at);
+        k0 = at - tile * a.nk;
         tile += a.waves * (gridDim.x / CG);
     }
     __device__ __forceinline__ void place() {
-        k1 = waves > 0 ? a.nk : (int)min((int64_t)a.nk, k0 + left);
-        const int band = tile / (GM * a.tt), in = tile - band * GM * a.tt, gm = min(GM, a.mt - band * GM);
-        t = in / gm;
-        m = band * GM + in - t * gm;
+        k1 = waves > 0 ? a.nk : min(a.nk, k0 + left);
+        m = tile;
+        t = 0;
+        if (a.tt > 1) {
+            const int band = a.by_band.of(tile), in = tile - band * GM * a.tt;
+            const bool whole = (band + 1) * GM <= a.mt;
+            t = whole ? in / GM : a.by_last.of(in);
+            m = band * GM + in - t * (whole ? GM : a.mt - band * GM);
+        }
     }
     __device__ __forceinline__ bool more() const { return waves > 0 || left > 0; }
     __device__ __forceinline__ void next() {
         const int n = gridDim.x / CG;
         if (waves > 0) {
             tile += n;
-            if (--waves == 0 && a.total > 0) to_line(share(a.total, blockIdx.x / CG, n));
+            if (--waves == 0 && a.total > 0) to_line(share(a, blockIdx.x / CG));
         } else {
             left -= k1 - k0;
             ++tile;
@@ -740,8 +761,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 }
                 release(ab);
                 // the tile's parts: those of workers c0 .. c1
-                const int64_t p0 = (int64_t)(g.tile - a.waves * workers) * a.nk;
-                const int c0 = holder_of(p0, a.total, workers), c1 = holder_of(p0 + a.nk - 1, a.total, workers);
+                const int p0 = (g.tile - a.waves * workers) * a.nk;
+                const int c0 = holder_of(a, p0, workers), c1 = holder_of(a, p0 + a.nk - 1, workers);
                 __threadfence();
                 ptx::named_bar_sync(2, 32 * C::EW);
                 if (threadIdx.x == 6 * 32) {
@@ -787,10 +808,10 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         if (a.split > 1) {
             // the cluster's parts, added in the order of K: CTA c of it takes the c-th share of the tokens
             ptx::cluster_sync_all();
-            const int c = blockIdx.x % a.split;
+            const int c = ptx::cluster_rank();
             const Segment<CG> g(a);
             const int row0 = g.m * LM, t0 = g.t * NT, n_tok = min(NT, a.T - t0);
-            const int u0 = n_tok * c / a.split, u1 = n_tok * (c + 1) / a.split;
+            const int u0 = a.by_split.of(n_tok * c), u1 = a.by_split.of(n_tok * (c + 1));
             // P parts of U pieces (four rows of a token) a thread, their loads under way together
             auto add = [&](auto parts, auto pieces) {
                 constexpr int P = decltype(parts)::value, U = decltype(pieces)::value;
@@ -1004,11 +1025,18 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
         // the line takes what whole rounds leave over and one round more, so that a cut tile has at most three parts
         const int64_t rounds = tiles / workers;
         a.waves = rounds >= 1 ? (int)rounds - 1 : 0;
-        a.total = (tiles - (int64_t)a.waves * workers) * a.nk;
-        ctas = (int)(a.total < workers ? a.total : workers);
+        a.total = (int)(tiles - (int64_t)a.waves * workers) * a.nk;
+        ctas = a.total < workers ? a.total : workers;
     }
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
+    const int gm = Segment<CG>::GM;
+    a.workers = Div(ctas);
+    a.by_split = Div(a.split);
+    a.by_nk = Div(a.nk);
+    a.by_total = Div(a.total > 0 ? a.total : 1);
+    a.by_band = Div(gm * a.tt);
+    a.by_last = Div(a.mt % gm ? a.mt % gm : gm);
     if (!C::FIRST) {
         timing_begin(K_MX_SPLIT, st);
         const bool many = (int64_t)d.T * (d.K / 8) > (int64_t)num_sms() * 2048;   // more than one round of the SMs' threads

@@ -384,6 +384,18 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// This CTA's number in its (one-dimensional) cluster, and the cluster's in the grid
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_id() {
+    int r;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 // The cluster address of `p`'s place in CTA `rank`, and an arrival there.  What the arrivals of a pair's
 // kernel announce are accesses to TMEM that have completed (tcgen05.wait) before it; a release at cluster
 // scope would wait for every load under way as well.
