@@ -50,6 +50,13 @@ constexpr uint64_t L_WAIT_NS = 2000000000ull;
 constexpr int L_SITE = 300;                   // detail of MOE_ERR_TIMEOUT: site of the wait
 
 // NT tokens a tile, CG CTAs a tile.
+// what a CTA of a cluster of up to 8 gets at most of n groups, each in as many parts
+constexpr int most_parts(int n) {
+    int most = 0;
+    for (int c = 2; c <= 8; ++c) most = (n + c - 1) / c * c > most ? (n + c - 1) / c * c : most;
+    return most;
+}
+
 template <bool XMX, int NT, int CG>
 struct LCfg {
     static constexpr bool FUSED = !XMX && CG == 1 && NT == 8;     // the terms of x are made here (K % 512 == 0)
@@ -86,8 +93,14 @@ struct LCfg {
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
     // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
     // (nor is a pair with a bf16 x faster with four stages than with three)
-    static constexpr int S = TERMS == 2 ? 3 : S_FIT < S_TMEM ? S_FIT : S_TMEM;
-    static constexpr int SMEM = 1024 + S * STAGE + XCH_BYTES + 512;
+    // (FUSED: five leave ROOM, see below: T = 1, N = 6144, K = 4096 7.05 us, with six 7.4)
+    static constexpr int S = TERMS == 2 ? 3 : FUSED ? 5 : S_FIT < S_TMEM ? S_FIT : S_TMEM;
+    // where a cluster's parts of a tile meet: a CTA's groups of four tokens, of each [part][LM] float4, behind the rest where
+    // there is room, so that they need not wait for this CTA's stages, else in those
+    static constexpr int MEET = most_parts(NT / 4) * LM * 16;
+    static constexpr bool ROOM = CG == 1 && 1024 + S * STAGE + XCH_BYTES + 512 + MEET <= 232448;
+    static constexpr int SMEM = 1024 + S * STAGE + XCH_BYTES + 512 + (ROOM ? MEET : 0);
+    static_assert(CG == 2 || ROOM || S * STAGE >= MEET, "a place for the parts");
     static_assert(S >= 2 && S <= S_FIT && SMEM <= 232448, "stages");
     static_assert(CG == 1 || NT == 256, "a pair's tile is 256 x 256");
 };
@@ -128,6 +141,16 @@ struct LArgs {
 // (total < 2 * 152 * 256 stages: the products are ordinary integers)
 __device__ __forceinline__ int share(const LArgs& a, int c) { return a.workers.of(a.total * c); }
 __device__ __forceinline__ int holder_of(const LArgs& a, int p, int n) { return a.by_total.of((p + 1) * n - 1); }
+
+// Token t's (low half) and t + 1's value of this lane's row of weights, to out[0] and out[stride] while below `end`: lanes 2i and
+// 2i + 1 exchange, so that each stores both rows of one of the tokens (2-byte stores: T = 8192, N = 14336,
+// K = 7168 in 311 us against 289; rows of 256 bytes through shared memory: 330, by TMA: 371).
+__device__ __forceinline__ void store_rows(__nv_bfloat16* out, int64_t stride, bool row, int t, int end, uint32_t v) {
+    const int odd = threadIdx.x & 1;
+    const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
+    if (row && t + odd < end)
+        *reinterpret_cast<uint32_t*>(out + (odd ? stride - 1 : 0)) = odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
+}
 
 // A worker's segments: stages [k0, k1) of tile (m, t), one after the other: `waves` whole tiles, then its share
 // of the line.  Tiles are numbered through bands of GM weight tiles, so that those that are worked on at one
@@ -234,6 +257,16 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     ptx::tc_fence_before();
     __syncthreads();
     if (PAIR) ptx::cluster_sync_all();   // both CTAs' barriers exist
+    // the cluster's CTAs run (and, without ROOM, are done with their stages): parts may be sent to them
+    bool met = PAIR || a.split == 1;
+    if (!PAIR && C::ROOM && a.split > 1) ptx::cluster_arrive_relaxed();
+    auto meet = [&] {
+        if (met) return;
+        met = true;
+        if (!C::ROOM) ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    };
+    float4* parts = reinterpret_cast<float4*>(C::ROOM ? sm + S * C::STAGE + C::XCH_BYTES + 512 : sm);
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
     if (C::FIRST) pdl_wait();
@@ -689,38 +722,37 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         int seg = 0;
         for (Segment<CG> g(a); g.more(); g.next(), ++seg) {
             const int ab = seg % ACC;
+            if (C::ROOM) meet();
             if (!ptx::mbar_wait_all(&acc_full[ab], (seg / ACC) & 1, abort_flag, L_WAIT_NS) && lane == 0) fail(5);
             // the warps decide together (they share barriers below)
             if (threadIdx.x == 6 * 32) last_flag[1 + (seg & 1)] = *abort_flag;
             ptx::named_bar_sync(2, 32 * C::EW);
+            meet();
             if (last_flag[1 + (seg & 1)]) break;
             ptx::tc_fence_after();
             const int row0 = (g.m * CG + rank) * LM, row = row0 + r, t0 = g.t * (PAIR ? a.nt : NT);
             const int n_tok = min(PAIR ? a.nt : NT, a.T - t0), mine = PAIR ? min(first + a.nt / 2, n_tok) : n_tok;
             if constexpr (!PAIR) {
                 if (a.split > 1) {
-                    // the CTA's part into its own shared memory, whose stages are done with
-                    float* part = reinterpret_cast<float*>(sm) + r;
+                    // the cluster's CTAs take four tokens in turn to add: their parts go there
+                    uint32_t at = ptx::smem_u32(parts + ptx::cluster_rank() * LM + r), to = 0;
 #pragma unroll 1
                     for (int t = 0; t < n_tok; t += G) {
                         float y[G];
                         read(ab, t, y);
 #pragma unroll
-                        for (int j = 0; j < G; ++j) part[(t + j) * LM] = y[j];
+                        for (int j = 0; j < G; j += 4) {
+                            if (t + j < n_tok)
+                                ptx::st_cluster(ptx::map_cluster(at, to), make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+                            if (++to == a.split) to = 0, at += a.split * LM * 16;
+                        }
                     }
                     break;
                 }
             }
             if (PAIR || (g.k0 == 0 && g.k1 == a.nk)) {
-                // lanes 2i and 2i + 1 exchange, so that each stores both rows of one of two tokens (2-byte
-                // stores: T = 8192, N = 14336, K = 7168 in 311 us against 289; rows of 256 bytes through shared
-                // memory: 330, by TMA: 371)
-                const int odd = lane & 1;
                 auto store = [&](int t, uint32_t v) {
-                    const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
-                    if (first + t + odd < mine && row < a.N)
-                        *reinterpret_cast<uint32_t*>(a.out + (t0 + first + t + odd) * a.out_stride + row - odd) =
-                            odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
+                    store_rows(a.out + (t0 + first + t) * a.out_stride + row, a.out_stride, row < a.N, first + t, mine, v);
                 };
                 if constexpr (PAIR) {
                     // its one accumulator is read out first, so that the next tile's MMAs may begin
@@ -806,43 +838,33 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     }
     if constexpr (!PAIR) {
         if (a.split > 1) {
-            // the cluster's parts, added in the order of K: CTA c of it takes the c-th share of the tokens
-            ptx::cluster_sync_all();
-            const int c = ptx::cluster_rank();
             const Segment<CG> g(a);
-            const int row0 = g.m * LM, t0 = g.t * NT, n_tok = min(NT, a.T - t0);
-            const int u0 = a.by_split.of(n_tok * c), u1 = a.by_split.of(n_tok * (c + 1));
-            // P parts of U pieces (four rows of a token) a thread, their loads under way together
-            auto add = [&](auto parts, auto pieces) {
-                constexpr int P = decltype(parts)::value, U = decltype(pieces)::value;
+            const int c = ptx::cluster_rank(), t0 = g.t * NT, n_tok = min(NT, a.T - t0);
+            const int groups = a.by_split.of((n_tok + 3) / 4 - c + a.split - 1);
+            __syncwarp();
+            meet();
+            ptx::cluster_sync_all();
+            // added in the order of K, four tokens of a row at a time
+            auto add = [&](auto most) {
+                constexpr int P = decltype(most)::value;
 #pragma unroll 1
-                for (int i = threadIdx.x; i < (u1 - u0) * 32; i += U * C::THREADS) {
-                    float4 v[U][P];
+                for (int i = warp; i < 4 * groups; i += C::THREADS / 32) {
+                    const int r = 32 * (i & 3) + lane, row = g.m * LM + r;
+                    const float4* from = parts + (i >> 2) * a.split * LM + r;
+                    float4 v[P];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int j = i + u * C::THREADS;
-                        const uint32_t at = ptx::smem_u32(sm) + (min(u0 + (j >> 5), u1 - 1) * LM + 4 * (j & 31)) * 4;
+                    for (int p = 0; p < P; ++p) v[p] = p < a.split ? from[p * LM] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    float4 y = v[0];
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            v[u][p] = p < a.split ? ptx::ld_cluster(ptx::map_cluster(at, p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int j = i + u * C::THREADS, t = u0 + (j >> 5), row = row0 + 4 * (j & 31);
-                        float4 y = v[u][0];
-#pragma unroll
-                        for (int p = 1; p < P; ++p)
-                            y.x += v[u][p].x, y.y += v[u][p].y, y.z += v[u][p].z, y.w += v[u][p].w;
-                        if (t < u1 && row < a.N)
-                            *reinterpret_cast<uint2*>(a.out + (t0 + t) * a.out_stride + row) =
-                                make_uint2(ptx::cvt_bf16x2(y.x, y.y), ptx::cvt_bf16x2(y.z, y.w));
-                    }
+                    for (int p = 1; p < P; ++p) y.x += v[p].x, y.y += v[p].y, y.z += v[p].z, y.w += v[p].w;
+                    const int t = 4 * ((i >> 2) * a.split + c);
+                    __nv_bfloat16* out = a.out + (t0 + t) * a.out_stride + row;
+                    store_rows(out, a.out_stride, row < a.N, t, n_tok, ptx::cvt_bf16x2(y.x, y.y));
+                    store_rows(out + 2 * a.out_stride, a.out_stride, row < a.N, t + 2, n_tok, ptx::cvt_bf16x2(y.z, y.w));
                 }
             };
-            if (a.split == 2) add(Int<2>(), Int<NT >= 64 ? 7 : 1>());
-            else if (a.split <= 4) add(Int<4>(), Int<NT >= 64 ? 4 : 1>());
-            else add(Int<8>(), Int<NT >= 64 ? 2 : 1>());
-            ptx::cluster_sync_relaxed();   // every CTA keeps its part until the others have read it
+            if (a.split == 2) add(Int<2>());
+            else add(Int<8>());
         }
     }
     __syncthreads();
