@@ -341,69 +341,69 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        if (rank == 0) {
+        // (one thread goes through the stages by itself, its waits without suspension: what it does between two stages'
+        // MMAs sets the pace)
+        if (rank == 0 && ptx::elect_one()) {
             int s = 0, seg = 0;
             uint32_t par = 0;
             bool ok = true;
+            // descriptors of stage 0; a stage further is STAGE / 16 more
+            const uint64_t a_desc = ptx::smem_desc_sw128(ptx::smem_u32(sm)), b_desc = a_desc + C::A_BYTES / 16;
+            const int n_mma = PAIR ? a.nt : NB;
             for (Segment<CG> g(a); ok && g.more(); g.next(), ++seg) {
                 const int ab = seg % ACC;
-                if (!ptx::mbar_wait_all(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
-                    if (lane == 0) fail(2);
-                    ok = false;
+                if (!ptx::mbar_wait_spin(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
+                    fail(2);
+                    break;
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem + ab * NB;
-                for (int k = g.k0; ok && k < g.k1; ++k) {
-                    if (!ptx::mbar_wait_all(&full[s], par, abort_flag, L_WAIT_NS)) {
-                        if (lane == 0) fail(3);
+                for (int k = g.k0; k < g.k1; ++k) {
+                    if (!ptx::mbar_wait_spin(&full[s], par, abort_flag, L_WAIT_NS)) {
+                        fail(3);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t a0 = ptx::smem_u32(sm + s * C::STAGE), b0 = a0 + C::A_BYTES;
+                    const uint64_t a0 = a_desc + (uint32_t)(s * (C::STAGE / 16)), b0 = b_desc + (uint32_t)(s * (C::STAGE / 16));
                     const uint32_t sfa = tmem + C::SF_COL0 + s * C::SF_SLOT, sfb = sfa + C::SF_B;
-                    if (ptx::elect_one()) {
-                        if constexpr (XMX) {
+                    if constexpr (XMX) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint64_t ad = ptx::smem_desc_sw128(a0 + 32 * j), bd = ptx::smem_desc_sw128(b0 + 32 * j);
-                                const uint32_t id = ptx::idesc_mxf4(LM * CG, PAIR ? a.nt : NB, 2 * (j & 1), 2 * (j & 1));
-                                const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * (j >> 1), fb = sfb + 16 * (j >> 1);
-                                if (PAIR) ptx::mma2_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
-                                else ptx::mma_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4 * WORDS * C::TERMS; ++j) {
-                                // 128-K slab, K step within it, term
-                                const int h = WORDS == 2 ? j >> 2 : 0, q = j & 3, e = C::TERMS == 2 ? j >> 2 : 0;
-                                const uint64_t ad = ptx::smem_desc_sw128(a0 + h * LM * 128 + 32 * q);
-                                const uint64_t bd = ptx::smem_desc_sw128(b0 + (h * C::B_ROWS + e * (a.nt / 2)) * 128 + 32 * q);
-                                const uint32_t id = ptx::idesc_mx_e2m1_e4m3(LM * CG, PAIR ? a.nt : NB, q, q);
-                                const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * h, fb = sfb + 16 * h;
-                                if (PAIR) ptx::mma2_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
-                                else ptx::mma_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t ad = a0 + 2 * j, bd = b0 + 2 * j;
+                            const uint32_t id = ptx::idesc_mxf4(LM * CG, n_mma, 2 * (j & 1), 2 * (j & 1));
+                            const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * (j >> 1), fb = sfb + 16 * (j >> 1);
+                            if (PAIR) ptx::mma2_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                            else ptx::mma_mxf4_ss(d_tmem, ad, bd, id, acc, fa, fb);
                         }
-                        if (PAIR) {
-                            ptx::mma2_commit(&empty[s]);
-                            if (k + 1 == g.k1) ptx::mma2_commit(&acc_full[ab]);
-                        } else {
-                            ptx::mma_commit(&empty[s]);
-                            if (k + 1 == g.k1) ptx::mma_commit(&acc_full[ab]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4 * WORDS * C::TERMS; ++j) {
+                            // 128-K slab, K step within it, term
+                            const int h = WORDS == 2 ? j >> 2 : 0, q = j & 3, e = C::TERMS == 2 ? j >> 2 : 0;
+                            const uint64_t ad = a0 + (h * LM * 8 + 2 * q);
+                            const uint64_t bd = b0 + (uint32_t)((h * C::B_ROWS + e * (a.nt / 2)) * 8 + 2 * q);
+                            const uint32_t id = ptx::idesc_mx_e2m1_e4m3(LM * CG, n_mma, q, q);
+                            const uint32_t acc = k > g.k0 || j > 0, fa = sfa + 16 * h, fb = sfb + 16 * h;
+                            if (PAIR) ptx::mma2_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
+                            else ptx::mma_mx_ss(d_tmem, ad, bd, id, acc, fa, fb);
                         }
                     }
-                    __syncwarp();
+                    if (PAIR) {
+                        ptx::mma2_commit(&empty[s]);
+                        if (k + 1 == g.k1) ptx::mma2_commit(&acc_full[ab]);
+                    } else {
+                        ptx::mma_commit(&empty[s]);
+                        if (k + 1 == g.k1) ptx::mma_commit(&acc_full[ab]);
+                    }
                     if (++s == S) s = 0, par ^= 1;
                 }
             }
             // every MMA issued above has completed before TMEM is released
-            if (ptx::elect_one()) {
-                if (PAIR) ptx::mma2_commit(fin);
-                else ptx::mma_commit(fin);
-            }
-            __syncwarp();
+            if (PAIR) ptx::mma2_commit(fin);
+            else ptx::mma_commit(fin);
         }
+        __syncwarp();
         ptx::mbar_wait_all(fin, 0, abort_flag, L_WAIT_NS);
     } else if (warp < 6 && PAIR) {
         // ------------------------------------------------------------ scales of a pair: groups of 1024 K, the next one ahead
