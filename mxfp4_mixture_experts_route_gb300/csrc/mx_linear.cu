@@ -14,22 +14,19 @@
 // product that two single CTAs would copy); the terms of a bf16 x are two MMAs into one accumulator.
 //
 // How the tiles' stages (KS elements of K) are shared out (tiling() chooses):
-//   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; the parts are
-//     added through the cluster's shared memory (T = 8, N = 7168, K = 4096, MXFP4 x: 6.7 us, by way of global
-//     memory 10.9);
-//   - else the persistent CTAs (pairs) take whole tiles in turn;
-//   - where a last round of single CTAs would leave much idle, the last tiles stand one after the other on a
-//     line of which every CTA takes an equal share.  A tile that a cut divides is
-//     joined without waiting: every CTA writes its part to the workspace and counts itself,
-//     and the one that comes last adds the parts in the order of the line (so the sum does
-//     not depend on who came last).  A pair's tile is too large for that (T = 1024, N = 6144, K = 4096: 32 us on the
-//     line): it takes fewer tokens instead, so that the tiles fill their rounds.
+//   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; every CTA sends its part by fours of tokens to
+//     the CTA that adds them, in the order of K (T = 8, N = 7168, K = 4096, MXFP4 x: 5.4 us; by way of global memory 4 us more;
+//     parts that the adding CTA reads: T = 64 8.1 us against 6.7);
+//   - else the persistent CTAs (pairs) take whole tiles in turn; pairs take fewer tokens where that fills their
+//     rounds.  (The last tiles cut anywhere and joined by way of global memory were slower for 50 of 52 products, by
+//     half for most; for the others, T = 16, N = 20480, K = 4096 and T = 40, N = 39680, bf16 x, 14.8 and 25.7 us against 15.5 and 28.7.)
 //
-// What bounds it: up to some dozen tokens the weights' bytes from HBM (N = 16384, K = 8192: 71 MB in 13.6 us) and, for small
-// products, the chain of a launch (0.5 us to the first copy, 1.5 to the first MMA, 1.5 for the sum over a
-// cluster); with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 95 us, 1719 TFLOP/s, 0.88 of the
+// What bounds it: up to some dozen tokens the weights' bytes from HBM (N = 16384, K = 8192: 71 MB in 13.3 us) and, for small
+// products, the chain of a launch (0.5 us to the first copy, 1.5 to the first MMA, 1.3 for the sum over a
+// cluster) and the stages' own pace (some 500 cycles: barrier, fences, four MMAs and their commit, whatever the tokens);
+// with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 94 us, 1740 TFLOP/s, 0.89 of the
 // measured bf16 rate); with both operands at 4 bits the copies, scales and stores beside MMAs that alone
-// take 197 of 273 us (8192 x 14336 x 7168: 6166 TFLOP/s).
+// take 197 of 265 us (8192 x 14336 x 7168: 6350 TFLOP/s).
 //
 // Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> shared memory or registers -> TMEM), from 6 on the accumulators' way
 // out (four, or eight of a pair's CTA), then a second set of scale warps.
@@ -74,7 +71,7 @@ struct LCfg {
     // sets of four scale warps (2-5, and behind the others), which take turns where a stage has little else: one alone
     // takes 0.4 us a stage (T = 8, N = 16384, K = 8192, MXFP4 x: 16.1 us, with two 13.8; with wider tiles the
     // registers of more warps cost more than they gain: T = 128, N = 9216, K = 7168 12.4, with two 13.1)
-    static constexpr int SETS = FUSED || (XMX && NT <= 64) ? 2 : 1;
+    static constexpr int SETS = CG == 1 && NT <= (XMX ? 64 : 32) ? 2 : 1;
     static constexpr int THREADS = 32 * (2 + 4 * SETS + EW);
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int TX = CG * (LM * KS / 2 + (FUSED ? 0 : B_BYTES));   // bytes of a stage that its barrier counts
@@ -122,25 +119,17 @@ struct Div {
 struct LArgs {
     const uint8_t *w_scales, *xs;             // [N][K/32], [T][K/32]
     __nv_bfloat16* out;
-    float* parts;                             // [CTA][2][NT][LM]
-    uint32_t* count;                          // [CTA]: parts of the tile that CTA began and did not finish
     StatusBlock* sb;
     int T, N, K;
     int64_t out_stride;
     int nt;                                   // tokens of a pair's tile: a multiple of 32 up to NT
     int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
     int split;                                // CTAs of a cluster that share a tile, or 1
-    int tiles, waves;                         // whole tiles that every worker takes first, if there is a line
-    int total;                                // stages on the line, which begins behind those tiles, or 0
+    int tiles;
     int vec;                                  // scale rows are 16-byte aligned
     int w_once;
-    Div workers, by_split, by_nk, by_total, by_band, by_last;   // (by_band: tiles of a band, by_last: weight tiles of the last one)
+    Div workers, by_split, by_band, by_last;   // (by_band: tiles of a band, by_last: weight tiles of the last one)
 };
-
-// the first stage of worker c's share of the line (of n), and the worker that holds stage p
-// (total < 2 * 152 * 256 stages: the products are ordinary integers)
-__device__ __forceinline__ int share(const LArgs& a, int c) { return a.workers.of(a.total * c); }
-__device__ __forceinline__ int holder_of(const LArgs& a, int p, int n) { return a.by_total.of((p + 1) * n - 1); }
 
 // Token t's (low half) and t + 1's value of this lane's row of weights, to out[0] and out[stride] while below `end`: lanes 2i and
 // 2i + 1 exchange, so that each stores both rows of one of the tokens (2-byte stores: T = 8192, N = 14336,
@@ -152,41 +141,29 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* out, int64_t stride, b
         *reinterpret_cast<uint32_t*>(out + (odd ? stride - 1 : 0)) = odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
 }
 
-// A worker's segments: stages [k0, k1) of tile (m, t), one after the other: `waves` whole tiles, then its share
-// of the line.  Tiles are numbered through bands of GM weight tiles, so that those that are worked on at one
+// A worker's segments: stages [k0, k1) of tile (m, t), one after the other: every n-th tile of n workers, or a cluster's CTA's
+// share of one.  Tiles are numbered through bands of GM weight tiles, so that those that are worked on at one
 // time share their rows of w and of x.
 template <int CG>
 struct Segment {
     static constexpr int GM = 8;
-    int left;                    // stages of the share to go
-    int tile, m, t, k0, k1, waves;
+    int left;                    // segments to go, this one too
+    int tile, m, t, k0, k1;
     const LArgs& a;
-    __device__ __forceinline__ explicit Segment(const LArgs& args) : left(0), waves(args.waves), a(args) {
-        const int c = blockIdx.x / CG;
-        tile = c;
-        k0 = 0;
+    __device__ __forceinline__ explicit Segment(const LArgs& args) : k0(0), k1(args.nk), a(args) {
         if (CG == 1 && a.split > 1) {
             const int part = ptx::cluster_rank();
             tile = ptx::cluster_id();
-            waves = 0;
+            left = 1;
             k0 = a.by_split.of(a.nk * part);
-            left = a.by_split.of(a.nk * (part + 1)) - k0;
-        } else if (a.total == 0) {
-            waves = a.workers.of(a.tiles - c + gridDim.x / CG - 1);
+            k1 = a.by_split.of(a.nk * (part + 1));
         } else {
-            const int at = share(a, c);
-            left = share(a, c + 1) - at;
-            if (waves == 0) to_line(at);
+            tile = blockIdx.x / CG;
+            left = a.workers.of(a.tiles - tile + gridDim.x / CG - 1);
         }
         place();
     }
-    __device__ __forceinline__ void to_line(int at) {
-        tile = a.by_nk.of(at);
-        k0 = at - tile * a.nk;
-        tile += a.waves * (gridDim.x / CG);
-    }
     __device__ __forceinline__ void place() {
-        k1 = waves > 0 ? a.nk : min(a.nk, k0 + left);
         m = tile;
         t = 0;
         if (a.tt > 1) {
@@ -196,18 +173,10 @@ struct Segment {
             m = band * GM + in - t * (whole ? GM : a.mt - band * GM);
         }
     }
-    __device__ __forceinline__ bool more() const { return waves > 0 || left > 0; }
+    __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next() {
-        const int n = gridDim.x / CG;
-        if (waves > 0) {
-            tile += n;
-            if (--waves == 0 && a.total > 0) to_line(share(a, blockIdx.x / CG));
-        } else {
-            left -= k1 - k0;
-            ++tile;
-            k0 = 0;
-        }
-        if (more()) place();
+        tile += gridDim.x / CG;
+        if (--left > 0) place();
     }
 };
 
@@ -421,13 +390,11 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         // bytes 32 grp + 4 word .. + 3 of rows 4 i + sub of this warp's part; past the tensor's ends 127 (its codes are zeros)
         auto load = [&](const uint8_t* from, int row0, int rows, int grp, auto& to) {
             const bool in = 32 * grp + 4 * word < kb;
+            const int n = rows - row0 - sub;     // rows from this lane's first one on
+            uint32_t at = (uint32_t)(row0 + sub) * kb + 32 * grp + 4 * word;   // (rows * kb <= 2^31)
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(to) / 4); ++i) {
-                const int row = row0 + 4 * i + sub;
-                to[i] = in && row < rows
-                            ? ld_dep(reinterpret_cast<const uint32_t*>(from + (int64_t)row * kb + 32 * grp + 4 * word))
-                            : 0x7F7F7F7Fu;
-            }
+            for (int i = 0; i < (int)(sizeof(to) / 4); ++i, at += 4 * kb)
+                to[i] = in && 4 * i < n ? ld_dep(reinterpret_cast<const uint32_t*>(from + at)) : 0x7F7F7F7Fu;
         };
         auto load_a = [&](const Segment<CG>& g, int grp) { load(a.w_scales, (g.m * CG + rank) * LM + q * (LM / 4), a.N, grp, na); };
         auto load_b = [&](const Segment<CG>& g, int grp) { load(a.xs, g.t * a.nt + q * (PT / 4), a.T, grp, nb); };
@@ -453,16 +420,12 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 for (int i = 0; i < NR; ++i) xb[word * SB + q * (PT / 4) + 4 * i + sub] = nb[i];
                 if (nan) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 // the next group's, under way while this one's stages go through
-                if (PG * (grp + 1) < g.k1) {
-                    load_a(g, grp + 1);
-                    load_b(g, grp + 1);
-                } else {
-                    Segment<CG> n = g;
-                    n.next();
-                    if (n.more()) {
-                        load_a(n, 0);
-                        load_b(n, 0);
-                    }
+                Segment<CG> n = g;
+                int ngrp = grp + 1;
+                if (PG * ngrp >= g.k1) n.next(), ngrp = 0;
+                if (n.more()) {
+                    load_a(n, ngrp);
+                    load_b(n, ngrp);
                 }
                 // (one barrier a group: a buffer is written again two groups later)
                 ptx::named_bar_sync(1, 128);
@@ -539,7 +502,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         auto advance = [&](Segment<CG>& g, int& grp) {
             if (2 * ++grp >= g.k1) {
                 g.next();
-                grp = g.k0 / 2;   // (the line may begin within a tile)
+                grp = g.k0 / 2;
             }
         };
         // to the set's next group
@@ -682,7 +645,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         const int q = warp & 3, r = 32 * q + lane;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const uint32_t acc_empty0 = PAIR ? ptx::map_cluster(acc_empty, 0) : 0;
-        if (!C::FIRST) pdl_wait();   // (the workspace's parts: an earlier call may still read its own)
+        if (!C::FIRST) pdl_wait();   // (what starts behind this call starts behind k_mx_split)
         pdl_trigger();
         // G tokens' sums, a token's columns added
         constexpr int G = C::EN < 32 ? C::EN : 32;
@@ -718,7 +681,6 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 else ptx::mbar_arrive(&acc_empty[ab]);
             }
         };
-        const int me = blockIdx.x / CG, workers = gridDim.x / CG;
         int seg = 0;
         for (Segment<CG> g(a); g.more(); g.next(), ++seg) {
             const int ab = seg % ACC;
@@ -750,89 +712,33 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                     break;
                 }
             }
-            if (PAIR || (g.k0 == 0 && g.k1 == a.nk)) {
-                auto store = [&](int t, uint32_t v) {
-                    store_rows(a.out + (t0 + first + t) * a.out_stride + row, a.out_stride, row < a.N, first + t, mine, v);
-                };
-                if constexpr (PAIR) {
-                    // its one accumulator is read out first, so that the next tile's MMAs may begin
-                    uint32_t y2[C::EN / 2];
+            auto store = [&](int t, uint32_t v) {
+                store_rows(a.out + (t0 + first + t) * a.out_stride + row, a.out_stride, row < a.N, first + t, mine, v);
+            };
+            if constexpr (PAIR) {
+                // its one accumulator is read out first, so that the next tile's MMAs may begin
+                uint32_t y2[C::EN / 2];
 #pragma unroll
-                    for (int t = 0; t < C::EN; t += G) {
-                        float y[G];
-                        read(ab, first + t, y);
+                for (int t = 0; t < C::EN; t += G) {
+                    float y[G];
+                    read(ab, first + t, y);
 #pragma unroll
-                        for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
-                    }
-                    release(ab);
-#pragma unroll
-                    for (int t = 0; t < C::EN; t += 2) store(t, y2[t / 2]);
-                } else {
-#pragma unroll 1
-                    for (int t = 0; t < n_tok; t += G) {
-                        float y[G];
-                        read(ab, t, y);
-#pragma unroll
-                        for (int j = 0; j < G; j += 2) store(t + j, ptx::cvt_bf16x2(y[j], y[j + 1]));
-                    }
-                    release(ab);
+                    for (int j = 0; j < G; j += 2) y2[(t + j) / 2] = ptx::cvt_bf16x2(y[j], y[j + 1]);
                 }
-                continue;
-            }
-            if constexpr (!PAIR) {
-                constexpr int64_t PART = (int64_t)NT * LM;
-                auto part_of = [&](int c, int slot) { return a.parts + ((int64_t)c * 2 + slot) * PART; };
-                float* part = part_of(me, g.k0 == 0) + r;
+                release(ab);
+                __nv_bfloat16* out = a.out + (t0 + first) * a.out_stride + row;
+#pragma unroll
+                for (int t = 0; t < C::EN; t += 2, out += 2 * a.out_stride)
+                    store_rows(out, a.out_stride, row < a.N, first + t, mine, y2[t / 2]);
+            } else {
 #pragma unroll 1
-                for (int t = first; t < mine; t += G) {
+                for (int t = 0; t < n_tok; t += G) {
                     float y[G];
                     read(ab, t, y);
 #pragma unroll
-                    for (int j = 0; j < G; ++j)
-                        if (t + j < mine) part[(t + j) * LM] = y[j];
+                    for (int j = 0; j < G; j += 2) store(t + j, ptx::cvt_bf16x2(y[j], y[j + 1]));
                 }
                 release(ab);
-                // the tile's parts: those of workers c0 .. c1
-                const int p0 = (g.tile - a.waves * workers) * a.nk;
-                const int c0 = holder_of(a, p0, workers), c1 = holder_of(a, p0 + a.nk - 1, workers);
-                __threadfence();
-                ptx::named_bar_sync(2, 32 * C::EW);
-                if (threadIdx.x == 6 * 32) {
-                    uint32_t* count = a.count + c0;
-                    const bool last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
-                    if (last) *count = 0;
-                    __threadfence();
-                    last_flag[0] = last;
-                }
-                ptx::named_bar_sync(2, 32 * C::EW);
-                if (!last_flag[0]) continue;
-                // four rows a lane, a token a warp at a time; J tokens' loads under way together
-                constexpr int J = NT / C::EW < 16 ? NT / C::EW : 16;
-                const int row4 = row0 + 4 * lane;
-#pragma unroll 1
-                for (int tb = warp - 6; tb < n_tok; tb += C::EW * J) {
-                    float4 y[J];
-#pragma unroll
-                    for (int j = 0; j < J; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* from = part_of(c, c == c0) + 4 * lane;
-                        float4 v[J];
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            v[j] = tb + C::EW * j < n_tok ? ld_dep(reinterpret_cast<const float4*>(from + (tb + C::EW * j) * LM))
-                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            y[j].x += v[j].x, y[j].y += v[j].y, y[j].z += v[j].z, y[j].w += v[j].w;
-                    }
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        if (tb + C::EW * j < n_tok && row4 < a.N)
-                            *reinterpret_cast<uint2*>(a.out + (t0 + tb + C::EW * j) * a.out_stride + row4) =
-                                make_uint2(ptx::cvt_bf16x2(y[j].x, y[j].y), ptx::cvt_bf16x2(y[j].z, y[j].w));
-                }
-                ptx::named_bar_sync(2, 32 * C::EW);   // the flag is written again
             }
         }
     }
@@ -921,33 +827,30 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16*
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// How a product is cut: CTAs and tokens a tile; CTAs of a cluster that share a tile's K; whether the last tiles go on a line.
+// How a product is cut: CTAs and tokens a tile; CTAs of a cluster that share a tile's K.
 struct Tiling {
     int cg, nt, split;
-    bool line;
 };
 
-constexpr int L_CTAS = 152;   // a GB300's SMs: at most as many CTAs as the workspace has parts for
+constexpr int L_CTAS = 152;   // a GB300's SMs
 // How many clusters of 0 .. 8 such CTAs (one an SM) a GB300 runs at once (cudaOccupancyMaxActiveClusters)
 constexpr int CLUSTERS[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-// The line's joins take as long as this many stages.
-constexpr int LINE = 10;
-
 // The cut with the least estimated time: a launch costs `start`, a round of tiles a stage's time for each of its
-// stages, and sharing K `join` (us).  The numbers were fitted to measurements over T = 1 .. 8192, which they
-// meet within 10%: with operands in L2 a single CTA's stage (256 K) takes about the same for 8 tokens as for 128
-// (its copies' latency), a pair's of MXFP4 x too, whatever its tokens; a pair's of a bf16 x (128 K) grows with
-// them.  For instance T = 512, N = 6144, K = 4096, MXFP4 x: tiles of 128 tokens 22.4 us, pairs with 192 12.6,
-// with 256 14; T = 128, N = 4096: 64 tokens and two CTAs a tile 8.7 us, 32 tokens and one 10.0; bf16
-// x, T = 4096: pairs with 224 tokens 121 us, with 256 134, with 128 152.
+// stages, every round behind the first `round` more, and sharing K `join` (us).  The numbers were fitted to 591 measured
+// cuts of 58 products, T = 1 .. 2048, operands in L2; what it takes there is 0.3% slower than the best cut on
+// average, 5% at most.  For instance T = 256, N = 6144, K = 4096, MXFP4 x: pairs with 128 tokens 10.7 us, tiles of 128 tokens
+// 12.1; T = 64: 64 tokens and two CTAs a tile 6.6; bf16 x, T = 8, N = 16384, K = 8192: tiles of 16 tokens 15.8, of 8
+// 19.1; T = 4096: pairs with 224 tokens 119, with 256 134.
 Tiling tiling(const MxDims& d) {
     struct Single {
         int nt;
-        float start, stage, join;
+        float start, stage, join, round;
     };
-    static const Single mx[4] = {{16, 3.7f, 0.31f, 0.5f}, {32, 3.7f, 0.35f, 0.6f}, {64, 4.3f, 0.40f, 1.2f}, {128, 5.0f, 0.465f, 1.6f}};
-    static const Single bf[4] = {{8, 4.4f, 0.47f, 0.3f}, {16, 4.8f, 0.44f, 0.4f}, {32, 5.6f, 0.42f, 0.6f}, {64, 7.0f, 0.49f, 1.f}};
-    Tiling best{0, 0, 1, false};
+    static const Single mx[4] = {{16, 3.05f, 0.273f, 0.22f, 0.57f}, {32, 3.48f, 0.287f, 0.05f, 0.13f}, {64, 4.45f, 0.307f, -0.28f, 0.21f},
+                                 {128, 5.23f, 0.431f, -0.13f, 0.96f}};
+    static const Single bf[4] = {{8, 3.11f, 0.485f, 0.46f, 0.1f}, {16, 4.48f, 0.339f, 0.71f, 0.25f}, {32, 5.34f, 0.364f, 0.32f, 0.f},
+                                 {64, 6.17f, 0.491f, -0.27f, 0.57f}};
+    Tiling best{0, 0, 1};
     float least = 0.f;
     auto take = [&](float t, const Tiling& c) {
         if (best.cg == 0 || t < least) best = c, least = t;
@@ -958,30 +861,25 @@ Tiling tiling(const MxDims& d) {
         const int64_t tiles = (int64_t)((d.N + LM - 1) / LM) * ((d.T + c.nt - 1) / c.nt);
         const int64_t rounds = (tiles + L_CTAS - 1) / L_CTAS;
         for (int n = 2; n <= 8 && n <= nk; ++n)
-            if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), {1, c.nt, n, false});
-        take(c.start + c.stage * (rounds * nk), {1, c.nt, 1, false});
-        // (with fewer tiles the parts of each would be many)
-        if (tiles > CLUSTERS[2]) take(c.start + c.stage * ((float)(tiles * nk) / L_CTAS + LINE), {1, c.nt, 1, true});
-        if (c.nt >= d.T) break;
+            if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), {1, c.nt, n});
+        take(c.start + c.round * (rounds - 1) + c.stage * (rounds * nk), {1, c.nt, 1});
     }
     for (int nt = 64; nt <= 256; nt += 32) {
         const int64_t tiles = (int64_t)((d.N + 2 * LM - 1) / (2 * LM)) * ((d.T + nt - 1) / nt);
         const int64_t rounds = (tiles + L_CTAS / 2 - 1) / (L_CTAS / 2);
-        if (d.x_mx) take(6.3f + 0.41f * (rounds * nk), {2, nt, 1, false});
-        else take(6.5f + (0.235f + 0.00182f * nt) * (rounds * (d.K / 128)), {2, nt, 1, false});
+        if (d.x_mx) take(4.72f + 0.0043f * nt + 0.69f * (rounds - 1) + (0.312f + 0.00022f * nt) * (rounds * nk), {2, nt, 1});
+        else take(7.11f + 0.0014f * nt + 0.37f * (rounds - 1) + (0.227f + 0.00138f * nt) * (rounds * (d.K / 128)), {2, nt, 1});
     }
     return best;
 }
 
 struct LLayout {
-    size_t count, parts, xq, xs, total;
+    size_t xq, xs, total;
 };
 LLayout layout(const MxDims& d) {
     const Tiling t = tiling(d);
     LLayout L;
-    L.count = sizeof(StatusBlock);            // in the zeroed prefix
-    L.parts = align256(WS_ZERO_PREFIX);
-    L.xq = L.parts + align256(t.line ? (size_t)L_CTAS * 2 * t.nt * LM * 4 : 0);
+    L.xq = align256(WS_ZERO_PREFIX);
     const bool split_x = !d.x_mx && !(t.cg == 1 && t.nt == 8);   // k_mx_split's terms
     L.xs = L.xq + (split_x ? align256((size_t)2 * d.T * d.K) : 0);
     L.total = L.xs + (split_x ? align256((size_t)d.T * (d.K / 32)) : 0);
@@ -1023,8 +921,6 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     a.w_scales = p.w_scales;
     a.xs = XMX ? p.xs : reinterpret_cast<const uint8_t*>(p.ws + L.xs);
     a.out = reinterpret_cast<__nv_bfloat16*>(p.out);
-    a.parts = reinterpret_cast<float*>(p.ws + L.parts);
-    a.count = reinterpret_cast<uint32_t*>(p.ws + L.count);
     a.sb = reinterpret_cast<StatusBlock*>(p.ws);
     a.T = d.T;
     a.N = d.N;
@@ -1038,25 +934,12 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
     a.tiles = (int)tiles;
     a.split = cut.split;
-    a.waves = 0;
-    a.total = 0;
-    int ctas = (int)(tiles < workers ? tiles : workers);
-    if (cut.split > 1) {
-        ctas = (int)tiles * cut.split;
-    } else if (cut.line) {
-        // the line takes what whole rounds leave over and one round more, so that a cut tile has at most three parts
-        const int64_t rounds = tiles / workers;
-        a.waves = rounds >= 1 ? (int)rounds - 1 : 0;
-        a.total = (int)(tiles - (int64_t)a.waves * workers) * a.nk;
-        ctas = a.total < workers ? a.total : workers;
-    }
+    const int ctas = cut.split > 1 ? (int)tiles * cut.split : (int)(tiles < workers ? tiles : workers);
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
     const int gm = Segment<CG>::GM;
     a.workers = Div(ctas);
     a.by_split = Div(a.split);
-    a.by_nk = Div(a.nk);
-    a.by_total = Div(a.total > 0 ? a.total : 1);
     a.by_band = Div(gm * a.tt);
     a.by_last = Div(a.mt % gm ? a.mt % gm : gm);
     if (!C::FIRST) {

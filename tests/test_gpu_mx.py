@@ -233,8 +233,7 @@ def test_linear(T, N, K, kind):
     (1, 39680, 4096, "mxfp4"), (8, 40008, 3968, "mxfp4"), (30, 39680, 4096, "mxfp4"), (50, 39680, 4096, "mxfp4"),
     (100, 39688, 4096, "mxfp4"), (4, 39680, 4096, "bf16"), (8, 39688, 4096, "bf16"), (12, 40008, 3968, "bf16"),
     (30, 39680, 4096, "bf16"), (60, 39680, 4096, "bf16"), (40, 19848, 4224, "mxfp4")])
-def test_linear_line_behind_whole_tiles(T, N, K, kind):
-    # more than two rounds of tiles, the last ones cut anywhere: a worker goes from a whole tile into the middle of another
+def test_linear_more_than_two_rounds_of_tiles(T, N, K, kind):
     w, ws = weights(N + K, N, K)
     x, xs, x64, off = tokens(T + K, T, K, kind)
     first, work = product(x, xs, w, ws, T, N, K, kind)
@@ -285,7 +284,7 @@ def test_linear_strides_and_what_is_around(kind, T):
 
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
 def test_linear_repeats_bitwise_and_shares_a_workspace(kind):
-    # shapes of different tilings through one workspace, back to back: counters are left as they were found
+    # shapes of different tilings through one workspace, back to back
     cases = [(T, N, K) for T, N, K in SHAPES if T <= 300]
     data = [(weights(i, N, K), tokens(i, T, K, kind)) for i, (T, N, K) in enumerate(cases)]
     most = max(moe.mx_workspace_bytes(moe.MXShape.of(*c, x_mxfp4=kind == "mxfp4")) for c in cases)
