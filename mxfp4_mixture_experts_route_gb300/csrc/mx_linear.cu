@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     float4* parts = reinterpret_cast<float4*>(C::ROOM ? sm + S * C::STAGE + C::XCH_BYTES + 512 : sm);
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
-    if (C::FIRST) pdl_wait();
+    // (with what needs no input done, each role waits for the kernels before)
 
     auto fail = [&](int site) {
         latch_status(a.sb, MOE_ERR_TIMEOUT, L_SITE + site);
@@ -293,10 +293,13 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             bool ok = true;
             int it = 0, s = 0;
             uint32_t par = 1;
-            for (Segment<CG> g(a); ok && g.more(); g.next()) {
+            Segment<CG> g(a);
+            if (C::FIRST) pdl_wait();
+            for (; ok && g.more(); g.next()) {
                 for (int k = g.k0; k < g.k1; ++k, ++it) {
                     if (it >= pre) {
-                        if (!ptx::mbar_wait(&empty[s], par, abort_flag, L_WAIT_NS)) {
+                        if (!(PAIR ? ptx::mbar_wait(&empty[s], par, abort_flag, L_WAIT_NS)
+                                   : ptx::mbar_wait_spin(&empty[s], par, abort_flag, L_WAIT_NS))) {
                             fail(1);
                             ok = false;
                             break;
@@ -399,8 +402,9 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         auto load_a = [&](const Segment<CG>& g, int grp) { load(a.w_scales, (g.m * CG + rank) * LM + q * (LM / 4), a.N, grp, na); };
         auto load_b = [&](const Segment<CG>& g, int grp) { load(a.xs, g.t * a.nt + q * (PT / 4), a.T, grp, nb); };
         Segment<CG> g(a);
+        if (C::FIRST) pdl_wait();
         if (g.more()) load_a(g, 0);
-        if (!XMX) pdl_wait();
+        if (!C::FIRST) pdl_wait();
         if (g.more()) load_b(g, 0);
         // a warp whose wait gave up goes on without waiting: the four share the barrier below
         int s = 0, buf = 0;
@@ -520,8 +524,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             int ngrp = agrp;
 #pragma unroll 1
             for (int i = 0; i < ring - 1 && n.more(); ++i, skip(n, ngrp)) fetch_a(n, ngrp, i);
-            pdl_wait();
         }
+        pdl_wait();
 #pragma unroll 1
         for (int i = 0; i < ring - 1; ++i) {
             if (ahead.more()) {
@@ -567,7 +571,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 const uint2 w = words(rows + bytes * r, g.m * LM + r, a.N, k);
                 if (__vcmpeq4(w.x, 0xFFFFFFFFu) | __vcmpeq4(w.y, 0xFFFFFFFFu)) latch_status(a.sb, MOE_ERR_BAD_SCALE, 255);
                 uint2 v[(NB + 31) / 32];
-                if (ok && !ptx::mbar_wait_all(C::FUSED ? &x_full[s] : &empty[s], par, abort_flag, L_WAIT_NS)) {
+                uint64_t* free = C::FUSED ? &x_full[s] : &empty[s];
+                if (ok && !__all_sync(0xffffffffu, ptx::mbar_test_wait(free, par)) && !ptx::mbar_wait_all(free, par, abort_flag, L_WAIT_NS)) {
                     if (lane == 0) fail(4);
                     ok = false;
                 }
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         const int q = warp & 3, r = 32 * q + lane;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         const uint32_t acc_empty0 = PAIR ? ptx::map_cluster(acc_empty, 0) : 0;
-        if (!C::FIRST) pdl_wait();   // (what starts behind this call starts behind k_mx_split)
+        pdl_wait();
         pdl_trigger();
         // G tokens' sums, a token's columns added
         constexpr int G = C::EN < 32 ? C::EN : 32;
