@@ -89,9 +89,8 @@ struct LCfg {
     static constexpr int S_FIT = (232448 - 1024 - 512 - XCH_BYTES) / STAGE;
     // (a ring of their own for the scales, which leaves a pair's MXFP4 tiles six stages of copies under way
     // instead of four, made T = 8192, N = 14336, K = 7168 slower: 335 us against 296)
-    // (nor is a pair with a bf16 x faster with four stages than with three)
     // (FUSED: five leave ROOM, see below: T = 1, N = 6144, K = 4096 7.05 us, with six 7.4)
-    static constexpr int S = TERMS == 2 ? 3 : FUSED ? 5 : S_FIT < S_TMEM ? S_FIT : S_TMEM;
+    static constexpr int S = TERMS == 2 ? 4 : FUSED ? 5 : S_FIT < S_TMEM ? S_FIT : S_TMEM;
     // where a cluster's parts of a tile meet: a CTA's groups of four tokens, of each [part][LM] float4, behind the rest where
     // there is room, so that they need not wait for this CTA's stages, else in those
     static constexpr int MEET = most_parts(NT / 4) * LM * 16;
@@ -124,6 +123,7 @@ struct LArgs {
     int64_t out_stride;
     int nt;                                   // tokens of a pair's tile: a multiple of 32 up to NT
     int nk, tt, mt;                           // stages a tile, token tiles, weight tiles
+    int under_way;                            // stages of a pair with a bf16 x that are used: S or fewer
     int split;                                // CTAs of a cluster that share a tile, or 1
     int tiles;
     int vec;                                  // scale rows are 16-byte aligned
@@ -188,9 +188,10 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     constexpr bool PAIR = CG == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* xch = sm + S * C::STAGE;    // scales: a pair's [2][8 words][NT] words, else [RING][LM + NT] rows
+    const int stages = C::TERMS == 2 ? a.under_way : S;
+    uint8_t* xch = sm + stages * C::STAGE;    // scales: a pair's [2][8 words][NT] words, else [RING][LM + NT] rows
     // a pair's stages are counted on the even CTA's `full`, and its MMAs' ends on both CTAs' barriers
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + S * C::STAGE + C::XCH_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(xch + C::XCH_BYTES);
     uint64_t* empty = full + S;          // the stage's MMAs are done
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + ACC;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
         if (!C::ROOM) ptx::cluster_arrive_relaxed();
         ptx::cluster_wait();
     };
-    float4* parts = reinterpret_cast<float4*>(C::ROOM ? sm + S * C::STAGE + C::XCH_BYTES + 512 : sm);
+    float4* parts = reinterpret_cast<float4*>(C::ROOM ? xch + C::XCH_BYTES + 512 : sm);
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
     // (with what needs no input done, each role waits for the kernels before)
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             if (!C::FIRST) {
                 // the first stages' weights, inputs of the call, before the wait for the tokens' terms
                 int i = 0;
-                for (Segment<CG> g(a); g.more() && i < S; g.next())
-                    for (int k = g.k0; k < g.k1 && i < S; ++k, ++i) weights(g, k, i);
+                for (Segment<CG> g(a); g.more() && i < stages; g.next())
+                    for (int k = g.k0; k < g.k1 && i < stages; ++k, ++i) weights(g, k, i);
                 pre = i;
                 pdl_wait();
             }
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                         weights(g, k, s);
                     }
                     tokens(g, k, s);
-                    if (++s == S) s = 0, par ^= 1;
+                    if (++s == stages) s = 0, par ^= 1;
                 }
             }
         }
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                         ptx::mma_commit(&empty[s]);
                         if (k + 1 == g.k1) ptx::mma_commit(&acc_full[ab]);
                     }
-                    if (++s == S) s = 0, par ^= 1;
+                    if (++s == stages) s = 0, par ^= 1;
                 }
             }
             // every MMA issued above has completed before TMEM is released
@@ -453,17 +454,16 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                     const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
 #pragma unroll
                     for (int h = 0; h < WORDS; ++h) {
-                        // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
-                        // word into all four columns; the other quarters' are never read); column n of B:
+                        // row r is read at lane r mod 32 of this quarter, column + q; column n of B:
                         // lane n mod 32 of every quarter, column + n / 32
-                        ptx::tmem_st4_rep(col + 16 * h, w[h]);
+                        ptx::tmem_st1(col + 16 * h + q, w[h]);
                         ptx::tmem_st8(col + C::SF_B + 16 * h, v[h]);
                     }
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(full0 + 8 * s);
-                    if (++s == S) s = 0, par ^= 1;
+                    if (++s == stages) s = 0, par ^= 1;
                 }
             }
         }
@@ -621,10 +621,9 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 }
                 if (!ok) continue;
                 const uint32_t col = tmem + lane_base + C::SF_COL0 + s * C::SF_SLOT;
-                // row r is read at lane r mod 32 of this quarter, column + q (a warp writes its
-                // word into all four columns; the other quarters' are never read)
-                ptx::tmem_st4_rep(col, w.x);
-                ptx::tmem_st4_rep(col + 16, w.y);
+                // row r is read at lane r mod 32 of this quarter, column + q
+                ptx::tmem_st1(col + q, w.x);
+                ptx::tmem_st1(col + 16 + q, w.y);
                 // column n of B: lane n mod 32 of every quarter, column + n / 32
                 const uint32_t to = col + C::SF_B;
                 if constexpr (NB <= 32) {
@@ -942,6 +941,9 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     const int ctas = cut.split > 1 ? (int)tiles * cut.split : (int)(tiles < workers ? tiles : workers);
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
+    // with most of a tile's tokens copies further ahead only get in the way of the others (T = 4096, N = 4864,
+    // K = 4096, 256 tokens: three 91.8 us, four 93.5; T = 512, N = 6144, 192 tokens: 23.4 and 22.2)
+    a.under_way = nt > 192 ? 3 : 4;
     const int gm = Segment<CG>::GM;
     a.workers = Div(ctas);
     a.by_split = Div(a.split);
@@ -960,7 +962,7 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * CG));
     cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.dynamicSmemBytes = C::SMEM - (C::TERMS == 2 ? (C::S - a.under_way) * C::STAGE : 0);   // (what is left is L1's)
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
