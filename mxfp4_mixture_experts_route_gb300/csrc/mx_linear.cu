@@ -15,18 +15,18 @@
 //
 // How the tiles' stages (KS elements of K) are shared out (tiling() chooses):
 //   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; every CTA sends its part by fours of tokens to
-//     the CTA that adds them, in the order of K (T = 8, N = 7168, K = 4096, MXFP4 x: 5.4 us; by way of global memory 4 us more;
+//     the CTA that adds them, in the order of K (T = 8, N = 7168, K = 4096, MXFP4 x: 4.7 us; by way of global memory 4 us more;
 //     parts that the adding CTA reads: T = 64 8.1 us against 6.7);
 //   - else the persistent CTAs (pairs) take whole tiles in turn; pairs take fewer tokens where that fills their
 //     rounds.  (The last tiles cut anywhere and joined by way of global memory were slower for 50 of 52 products, by
 //     half for most; for the others, T = 16, N = 20480, K = 4096 and T = 40, N = 39680, bf16 x, 14.8 and 25.7 us against 15.5 and 28.7.)
 //
-// What bounds it: up to some dozen tokens the weights' bytes from HBM (N = 16384, K = 8192: 71 MB in 13.3 us) and, for small
-// products, the chain of a launch (0.5 us to the first copy, 1.5 to the first MMA, 1.3 for the sum over a
+// What bounds it: up to some dozen tokens the weights' bytes from HBM (N = 16384, K = 8192: 71 MB in 12.7 us) and, for small
+// products, the chain of a launch (1.2 us from the wait for earlier kernels to the first MMA, 1.2 for the sum over a
 // cluster) and the stages' own pace (some 500 cycles: barrier, fences, four MMAs and their commit, whatever the tokens);
-// with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 94 us, 1740 TFLOP/s, 0.89 of the
+// with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 92 us, 1770 TFLOP/s, 0.91 of the
 // measured bf16 rate); with both operands at 4 bits the copies, scales and stores beside MMAs that alone
-// take 197 of 265 us (8192 x 14336 x 7168: 6350 TFLOP/s).
+// take 197 of 257 us (8192 x 14336 x 7168: 6550 TFLOP/s).
 //
 // Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> shared memory or registers -> TMEM), from 6 on the accumulators' way
 // out (four, or eight of a pair's CTA), then a second set of scale warps.
@@ -68,9 +68,9 @@ struct LCfg {
     static constexpr int B_BYTES = XMX ? B_ROWS * KS / 2 : TERMS * B_ROWS * KS;
     static constexpr int EW = CG == 2 ? 8 : 4;                    // warps of the way out, and tokens of each
     static constexpr int EN = NT / (EW / 4);
-    // sets of four scale warps (2-5, and behind the others), which take turns where a stage has little else: one alone
-    // takes 0.4 us a stage (T = 8, N = 16384, K = 8192, MXFP4 x: 16.1 us, with two 13.8; with wider tiles the
-    // registers of more warps cost more than they gain: T = 128, N = 9216, K = 7168 12.4, with two 13.1)
+    // sets of four scale warps (2-5, and behind the others), which take turns where a stage has little else (T = 16, N = 16384,
+    // K = 8192, bf16 x: 17.7 us with one, 16.0 with two; with wider tiles the registers of more warps cost more than they
+    // gain: T = 128, N = 9216, K = 7168, MXFP4 x 10.8 and 11.9)
     static constexpr int SETS = CG == 1 && NT <= (XMX ? 64 : 32) ? 2 : 1;
     static constexpr int THREADS = 32 * (2 + 4 * SETS + EW);
     static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -103,7 +103,7 @@ struct LCfg {
 
 // n / d for 0 <= n < 2^31 as a product and a shift: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), n m 2^-(31 + s)
 // exceeds n / d by n e / (d 2^(31 + s)), 0 <= e < d <= 2^s, which is less than 1 / d.  (Divisions on the way
-// to the first MMA took 0.6 us of a launch's 6.7.)
+// to the first MMA took 0.6 us of a launch's 6.7, with the code they needed 1.2.)
 struct Div {
     uint32_t mul;
     int shift;
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 // A bf16 x as two e4m3 terms a row (rows 2t and 2t + 1 of xq) and a scale byte a
 // block (quant.cuh); a block with a NaN or an infinity has byte 255 and codes 0.
 // PIECES of 16 bytes a thread, their loads under way together: with many rows four (bound by HBM; the product with
-// 4096 rows of 4096 takes 121 us, with one 128), with few one (latency; 128 rows of 7168 21.3 us, with four 22.9).
+// 4096 rows of 4096 took 121 us, with one 128), with few one (latency; 128 rows of 7168 21.3 us, with four 22.9).
 constexpr int SPLIT_THREADS = 128;
 template <int PIECES>
 __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16* x, int64_t stride, int K, uint8_t* xq, uint8_t* xs) {
@@ -841,10 +841,10 @@ constexpr int L_CTAS = 152;   // a GB300's SMs
 constexpr int CLUSTERS[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 // The cut with the least estimated time: a launch costs `start`, a round of tiles a stage's time for each of its
 // stages, every round behind the first `round` more, and sharing K `join` (us).  The numbers were fitted to 591 measured
-// cuts of 58 products, T = 1 .. 2048, operands in L2; what it takes there is 0.3% slower than the best cut on
-// average, 5% at most.  For instance T = 256, N = 6144, K = 4096, MXFP4 x: pairs with 128 tokens 10.7 us, tiles of 128 tokens
-// 12.1; T = 64: 64 tokens and two CTAs a tile 6.6; bf16 x, T = 8, N = 16384, K = 8192: tiles of 16 tokens 15.8, of 8
-// 19.1; T = 4096: pairs with 224 tokens 119, with 256 134.
+// cuts of 58 products, T = 1 .. 2048, operands in L2; of 70 products, T = 1 .. 8192, measured since, what it takes is 0.5% slower than
+// the best cut on average, 8% at most.  For instance T = 256, N = 6144, K = 4096, MXFP4 x: pairs with 128 tokens 9.1 us, tiles of
+// 128 tokens 11.6; bf16 x, T = 8, N = 16384, K = 8192: tiles of 16 tokens 15.3, of 8 18.5; T = 4096: pairs with 224
+// tokens 117, with 256 128.
 Tiling tiling(const MxDims& d) {
     struct Single {
         int nt;
