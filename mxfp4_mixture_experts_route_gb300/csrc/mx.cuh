@@ -10,12 +10,14 @@ cudaError_t launch_mx_quantize(int64_t rows, int K, int dtype, const void* x, in
 cudaError_t launch_mx_dequantize(int64_t rows, int K, int dtype, const uint8_t* codes, const uint8_t* scales, void* y,
                                  int64_t y_stride, cudaStream_t st);
 
-// The product's shape with its strides filled in (elements).
+// The product's shape with its strides filled in (elements), and how it is cut (mx_cut, of the rest).
 struct MxDims {
     int T, N, K;
     bool x_mx;
     int64_t x_stride, out_stride;
+    int cg, nt, split;   // CTAs and tokens a tile; CTAs of a cluster that share a tile's K
 };
+void mx_cut(MxDims& d);
 struct MxArgs {
     const void* x;
     const uint8_t *xs, *w, *w_scales;

@@ -26,12 +26,13 @@ int mx_dims(const moe_mx_shape* s, MxDims& d) {
     if (s->T < 1 || s->N < 1 || s->K < 1 || s->x_stride < 0 || s->out_stride < 0) return MOE_ERR_INVALID_ARG;
     if (s->T > (1 << 20) || s->N > (1 << 20) || s->N % 8 || s->K % 128 || s->K > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
     d = MxDims{s->T, s->N, s->K, (s->flags & MOE_MX_X_MXFP4) != 0, s->x_stride ? s->x_stride : s->K,
-               s->out_stride ? s->out_stride : s->N};
+               s->out_stride ? s->out_stride : s->N, 0, 0, 0};
     const int64_t most = (int64_t)1 << 38;
     if (d.x_stride < d.K || d.out_stride < d.N || d.x_stride >= most || d.out_stride >= most)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (d.x_mx && d.x_stride != d.K) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (d.x_stride % 8 || d.out_stride % 8) return MOE_ERR_ALIGNMENT;
+    mx_cut(d);
     return MOE_OK;
 }
 

@@ -13,7 +13,7 @@
 // 256 weight rows x up to 256 tokens, of which each holds half of either operand (half the bytes a
 // product that two single CTAs would copy); the terms of a bf16 x are two MMAs into one accumulator.
 //
-// How the tiles' stages (KS elements of K) are shared out (tiling() chooses):
+// How the tiles' stages (KS elements of K) are shared out (mx_cut chooses):
 //   - few tiles: a cluster of up to eight CTAs a tile, each a part of K; every CTA sends its part by fours of tokens to
 //     the CTA that adds them, in the order of K (T = 8, N = 7168, K = 4096, MXFP4 x: 4.7 us; by way of global memory 4 us more;
 //     parts that the adding CTA reads: T = 64 8.1 us against 6.7);
@@ -34,6 +34,7 @@
 #include "quant.cuh"
 #include "tc_ptx.cuh"
 
+#include <math.h>
 #include <type_traits>
 
 namespace moe {
@@ -831,21 +832,18 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16*
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// How a product is cut: CTAs and tokens a tile; CTAs of a cluster that share a tile's K.
-struct Tiling {
-    int cg, nt, split;
-};
-
 constexpr int L_CTAS = 152;   // a GB300's SMs
 // How many clusters of 0 .. 8 such CTAs (one an SM) a GB300 runs at once (cudaOccupancyMaxActiveClusters)
 constexpr int CLUSTERS[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+}  // namespace
+
 // The cut with the least estimated time: a launch costs `start`, a round of tiles a stage's time for each of its
 // stages, every round behind the first `round` more, and sharing K `join` (us).  The numbers were fitted to 591 measured
 // cuts of 58 products, T = 1 .. 2048, operands in L2; of 70 products, T = 1 .. 8192, measured since, what it takes is 0.5% slower than
 // the best cut on average, 8% at most.  For instance T = 256, N = 6144, K = 4096, MXFP4 x: pairs with 128 tokens 9.1 us, tiles of
 // 128 tokens 11.6; bf16 x, T = 8, N = 16384, K = 8192: tiles of 16 tokens 15.3, of 8 18.5; T = 4096: pairs with 224
 // tokens 117, with 256 128.
-Tiling tiling(const MxDims& d) {
+void mx_cut(MxDims& d) {
     struct Single {
         int nt;
         float start, stage, join, round;
@@ -854,10 +852,9 @@ Tiling tiling(const MxDims& d) {
                                  {128, 5.23f, 0.431f, -0.13f, 0.96f}};
     static const Single bf[4] = {{8, 3.11f, 0.485f, 0.46f, 0.1f}, {16, 4.48f, 0.339f, 0.71f, 0.25f}, {32, 5.34f, 0.364f, 0.32f, 0.f},
                                  {64, 6.17f, 0.491f, -0.27f, 0.57f}};
-    Tiling best{0, 0, 1};
-    float least = 0.f;
-    auto take = [&](float t, const Tiling& c) {
-        if (best.cg == 0 || t < least) best = c, least = t;
+    float least = INFINITY;
+    auto take = [&](float t, int cg, int nt, int split) {
+        if (t < least) least = t, d.cg = cg, d.nt = nt, d.split = split;
     };
     const int64_t nk = (d.K + 255) / 256;
     for (const Single& c : d.x_mx ? mx : bf) {
@@ -865,36 +862,36 @@ Tiling tiling(const MxDims& d) {
         const int64_t tiles = (int64_t)((d.N + LM - 1) / LM) * ((d.T + c.nt - 1) / c.nt);
         const int64_t rounds = (tiles + L_CTAS - 1) / L_CTAS;
         for (int n = 2; n <= 8 && n <= nk; ++n)
-            if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), {1, c.nt, n});
-        take(c.start + c.round * (rounds - 1) + c.stage * (rounds * nk), {1, c.nt, 1});
+            if (tiles <= CLUSTERS[n]) take(c.start + c.join + c.stage * ((nk + n - 1) / n), 1, c.nt, n);
+        take(c.start + c.round * (rounds - 1) + c.stage * (rounds * nk), 1, c.nt, 1);
     }
     for (int nt = 64; nt <= 256; nt += 32) {
         const int64_t tiles = (int64_t)((d.N + 2 * LM - 1) / (2 * LM)) * ((d.T + nt - 1) / nt);
         const int64_t rounds = (tiles + L_CTAS / 2 - 1) / (L_CTAS / 2);
-        if (d.x_mx) take(4.72f + 0.0043f * nt + 0.69f * (rounds - 1) + (0.312f + 0.00022f * nt) * (rounds * nk), {2, nt, 1});
-        else take(7.11f + 0.0014f * nt + 0.37f * (rounds - 1) + (0.227f + 0.00138f * nt) * (rounds * (d.K / 128)), {2, nt, 1});
+        if (d.x_mx) take(4.72f + 0.0043f * nt + 0.69f * (rounds - 1) + (0.312f + 0.00022f * nt) * (rounds * nk), 2, nt, 1);
+        else take(7.11f + 0.0014f * nt + 0.37f * (rounds - 1) + (0.227f + 0.00138f * nt) * (rounds * (d.K / 128)), 2, nt, 1);
     }
-    return best;
 }
+
+namespace {
 
 struct LLayout {
     size_t xq, xs, total;
 };
 LLayout layout(const MxDims& d) {
-    const Tiling t = tiling(d);
     LLayout L;
     L.xq = align256(WS_ZERO_PREFIX);
-    const bool split_x = !d.x_mx && !(t.cg == 1 && t.nt == 8);   // k_mx_split's terms
+    const bool split_x = !d.x_mx && !(d.cg == 1 && d.nt == 8);   // k_mx_split's terms
     L.xs = L.xq + (split_x ? align256((size_t)2 * d.T * d.K) : 0);
     L.total = L.xs + (split_x ? align256((size_t)d.T * (d.K / 32)) : 0);
     return L;
 }
 
 template <bool XMX, int NT, int CG>
-cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cudaStream_t st) {
+cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     using C = LCfg<XMX, NT, CG>;
     const LLayout L = layout(d);
-    const int nt = cut.nt;
+    const int nt = d.nt;
     CUtensorMap tm_w, tm_x;
     const uint64_t N = d.N, T = d.T, K = d.K;
     const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -937,8 +934,8 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, const Tiling& cut, cu
     const int64_t tiles = (int64_t)a.mt * a.tt;
     const int workers = (num_sms() < L_CTAS ? num_sms() : L_CTAS) / CG;
     a.tiles = (int)tiles;
-    a.split = cut.split;
-    const int ctas = cut.split > 1 ? (int)tiles * cut.split : (int)(tiles < workers ? tiles : workers);
+    a.split = d.split;
+    const int ctas = d.split > 1 ? (int)tiles * d.split : (int)(tiles < workers ? tiles : workers);
     a.vec = d.K % 512 == 0;
     a.w_once = a.tt == 1;
     // with most of a tile's tokens copies further ahead only get in the way of the others (T = 4096, N = 4864,
@@ -984,22 +981,21 @@ size_t mx_linear_ws_bytes(const MxDims& d) { return layout(d).total; }
 
 cudaError_t launch_mx_linear(const MxDims& d, const MxArgs& a, cudaStream_t st) {
     KT_BIND();
-    const Tiling t = tiling(d);
     if (d.x_mx) {
-        if (t.cg == 2) return launch_tiles<true, 256, 2>(d, a, t, st);
-        switch (t.nt) {
-            case 16: return launch_tiles<true, 16, 1>(d, a, t, st);
-            case 32: return launch_tiles<true, 32, 1>(d, a, t, st);
-            case 64: return launch_tiles<true, 64, 1>(d, a, t, st);
-            default: return launch_tiles<true, 128, 1>(d, a, t, st);
+        if (d.cg == 2) return launch_tiles<true, 256, 2>(d, a, st);
+        switch (d.nt) {
+            case 16: return launch_tiles<true, 16, 1>(d, a, st);
+            case 32: return launch_tiles<true, 32, 1>(d, a, st);
+            case 64: return launch_tiles<true, 64, 1>(d, a, st);
+            default: return launch_tiles<true, 128, 1>(d, a, st);
         }
     }
-    if (t.cg == 2) return launch_tiles<false, 256, 2>(d, a, t, st);
-    switch (t.nt) {
-        case 8: return launch_tiles<false, 8, 1>(d, a, t, st);
-        case 16: return launch_tiles<false, 16, 1>(d, a, t, st);
-        case 32: return launch_tiles<false, 32, 1>(d, a, t, st);
-        default: return launch_tiles<false, 64, 1>(d, a, t, st);
+    if (d.cg == 2) return launch_tiles<false, 256, 2>(d, a, st);
+    switch (d.nt) {
+        case 8: return launch_tiles<false, 8, 1>(d, a, st);
+        case 16: return launch_tiles<false, 16, 1>(d, a, st);
+        case 32: return launch_tiles<false, 32, 1>(d, a, st);
+        default: return launch_tiles<false, 64, 1>(d, a, st);
     }
 }
 
