@@ -796,12 +796,14 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
 
 // A bf16 x as two e4m3 terms a row (rows 2t and 2t + 1 of xq) and a scale byte a
 // block (quant.cuh); a block with a NaN or an infinity has byte 255 and codes 0.
-// PIECES of 16 bytes a thread, their loads under way together: with many rows four (bound by HBM; the product with
-// 4096 rows of 4096 took 121 us, with one 128), with few one (latency; 128 rows of 7168 21.3 us, with four 22.9).
-constexpr int SPLIT_THREADS = 128;
+// PIECES of 16 bytes a thread, their loads under way together: with many rows four in blocks of 128 (bound by HBM; the product
+// with 4096 rows of 4096 takes 118 us, in blocks of 256 119.5, with one piece 128), with few one in blocks of 256 (latency; 512 rows of
+// 4096 21.7 us, in blocks of 128 22.3; 128 rows of 7168 19.6, with four pieces 21).
+constexpr int split_threads(int pieces) { return pieces == 1 ? 256 : 128; }
 template <int PIECES>
-__global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16* x, int64_t stride, int K, uint8_t* xq, uint8_t* xs) {
-    const int t = blockIdx.x, first = blockIdx.y * SPLIT_THREADS * PIECES + threadIdx.x, n = K / 8;
+__global__ void __launch_bounds__(split_threads(PIECES)) k_mx_split(const __nv_bfloat16* x, int64_t stride, int K, uint8_t* xq, uint8_t* xs) {
+    constexpr int THREADS = split_threads(PIECES);
+    const int t = blockIdx.x, first = blockIdx.y * THREADS * PIECES + threadIdx.x, n = K / 8;
     const uint4* row = reinterpret_cast<const uint4*>(x + t * stride);
     KT_MARK(K_MX_SPLIT, 0);
     pdl_wait();
@@ -810,12 +812,12 @@ __global__ void __launch_bounds__(SPLIT_THREADS) k_mx_split(const __nv_bfloat16*
     uint4 v[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int c = first + i * SPLIT_THREADS;
+        const int c = first + i * THREADS;
         v[i] = c < n ? ld_dep(row + c) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int c = first + i * SPLIT_THREADS;
+        const int c = first + i * THREADS;
         QuantChunk q = quantize_vals(v[i]);
         if (q.amax >= 0x7F800000u) {
             q.hi = q.lo = make_uint2(0, 0);
@@ -948,9 +950,9 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
     a.by_last = Div(a.mt % gm ? a.mt % gm : gm);
     if (!C::FIRST) {
         timing_begin(K_MX_SPLIT, st);
-        const bool many = (int64_t)d.T * (d.K / 8) > (int64_t)num_sms() * 2048;   // more than one round of the SMs' threads
-        const int per = SPLIT_THREADS * (many ? 4 : 1);
-        e = launch_pdl(many ? k_mx_split<4> : k_mx_split<1>, dim3(d.T, (d.K / 8 + per - 1) / per), dim3(SPLIT_THREADS), 0, st,
+        const bool many = (int64_t)d.T * (d.K / 8) > (int64_t)num_sms() * 4096;   // more than two rounds of the SMs' threads
+        const int pieces = many ? 4 : 1, threads = split_threads(pieces), per = threads * pieces;
+        e = launch_pdl(many ? k_mx_split<4> : k_mx_split<1>, dim3(d.T, (d.K / 8 + per - 1) / per), dim3(threads), 0, st,
                        reinterpret_cast<const __nv_bfloat16*>(p.x), d.x_stride, d.K,
                        reinterpret_cast<uint8_t*>(p.ws + L.xq), reinterpret_cast<uint8_t*>(p.ws + L.xs));
         timing_end(st);
