@@ -243,6 +243,35 @@ def test_linear_more_than_two_rounds_of_tiles(T, N, K, kind):
     check(first, x64, off, values(w, ws))
 
 
+# the tilings and ways of sharing K that SHAPES does not reach, the pairs' in several rounds with ragged ends too
+CUTS = [(1, 8, 1792, "bf16"), (1, 152, 2560, "bf16"), (1, 3040, 1536, "bf16"), (1, 3704, 1152, "bf16"),
+        (1, 6128, 1408, "bf16"), (1, 9904, 512, "bf16"), (2, 8, 1920, "bf16"), (13, 3304, 2560, "bf16"),
+        (16, 8, 1536, "bf16"), (16, 1032, 4096, "bf16"), (17, 1480, 5248, "bf16"), (17, 1480, 5248, "mxfp4"),
+        (17, 6208, 1920, "bf16"), (29, 2056, 1024, "bf16"), (33, 1848, 3712, "bf16"), (33, 1912, 5248, "mxfp4"),
+        (33, 2344, 2560, "bf16"), (33, 3240, 2816, "mxfp4"), (33, 3320, 2176, "mxfp4"), (33, 3416, 1920, "bf16"),
+        (33, 6712, 1408, "bf16"), (33, 6712, 1408, "mxfp4"), (50, 4920, 1152, "mxfp4"), (50, 4952, 640, "bf16"),
+        (61, 904, 4096, "bf16"), (100, 4976, 1152, "mxfp4"), (100, 10208, 640, "mxfp4"), (129, 1936, 5888, "mxfp4"),
+        (129, 4032, 1920, "mxfp4"), (300, 8, 7936, "bf16"), (300, 8, 7936, "mxfp4"), (300, 280, 3456, "bf16"),
+        (600, 8, 5248, "mxfp4"), (600, 16, 2432, "bf16"), (600, 16, 2432, "mxfp4"), (600, 5224, 384, "bf16"),
+        (700, 9736, 1280, "bf16"), (700, 9736, 1280, "mxfp4"), (1000, 16, 3456, "bf16"), (1000, 16, 3456, "mxfp4"),
+        (1000, 280, 3840, "mxfp4"), (1000, 1808, 640, "bf16"), (1000, 2640, 384, "mxfp4"),
+        (1000, 3760, 128, "mxfp4"), (1000, 3904, 128, "mxfp4"), (1000, 4416, 128, "bf16"), (1000, 4912, 128, "bf16"),
+        (1000, 4912, 128, "mxfp4"), (1000, 5568, 128, "bf16"), (1025, 6152, 384, "bf16"), (1025, 6152, 384, "mxfp4"),
+        (1500, 4104, 640, "bf16"), (1500, 4104, 640, "mxfp4"), (2049, 2056, 1152, "bf16"),
+        (2049, 2056, 1152, "mxfp4"), (4001, 1000, 2176, "bf16"), (4001, 1000, 2176, "mxfp4")]
+
+
+@pytest.mark.parametrize("T,N,K,kind", CUTS)
+def test_linear_every_cut(T, N, K, kind):
+    w, ws = weights(N + K, N, K)
+    x, xs, x64, off = tokens(T + K, T, K, kind)
+    buf = torch.full((T + 2, N), -77.0, dtype=torch.bfloat16, device=DEV)
+    out, work = product(x, xs, w, ws, T, N, K, kind, out=buf[1:-1])
+    moe.check_device_status(work, "mx_linear")
+    check(out, x64, off, values(w, ws))
+    assert (buf[0] == -77.0).all() and (buf[-1] == -77.0).all()
+
+
 @pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
 def test_linear_places_every_element(kind):
     # one element of x and of w at a time reaches the one place of out it belongs to
