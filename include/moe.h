@@ -530,7 +530,11 @@ typedef struct moe_mx_shape {
     int64_t out_stride;  /* ... of out */
 } moe_mx_shape;
 
-/* Workspace size of moe_mx_linear in *bytes (pure host function); moe_workspace_init prepares it once. */
+/*
+ * Workspace size of moe_mx_linear in *bytes (pure host function); moe_workspace_init prepares it once.
+ * The same for every N, and never less for more rows or a larger K: the workspace of a program's
+ * largest T and K with a bf16 x serves all of its calls.
+ */
 int moe_mx_workspace_bytes(const moe_mx_shape* shape, size_t* bytes);
 
 /*

@@ -883,9 +883,10 @@ struct LLayout {
 LLayout layout(const MxDims& d) {
     LLayout L;
     L.xq = align256(WS_ZERO_PREFIX);
-    const bool split_x = !d.x_mx && !(d.cg == 1 && d.nt == 8);   // k_mx_split's terms
-    L.xs = L.xq + (split_x ? align256((size_t)2 * d.T * d.K) : 0);
-    L.total = L.xs + (split_x ? align256((size_t)d.T * (d.K / 32)) : 0);
+    // k_mx_split's terms of a bf16 x, room for them also where the cut makes them in the product's kernel: which cut that is
+    // does not follow T alone, and a workspace for many tokens has to serve fewer
+    L.xs = L.xq + (d.x_mx ? 0 : align256((size_t)2 * d.T * d.K));
+    L.total = L.xs + (d.x_mx ? 0 : align256((size_t)d.T * (d.K / 32)));
     return L;
 }
 

@@ -146,3 +146,17 @@ def test_binding_refuses_what_has_no_rows():
         with pytest.raises(moe.MoEError) as e:
             moe.mx_quantize(x, c, s)
         assert e.value.code == INVALID
+
+
+@pytest.mark.parametrize("x_mxfp4", [False, True])
+@pytest.mark.parametrize("N,K", [(6144, 2048), (6144, 4096), (512, 8192), (1024, 2560), (5120, 1536), (8, 128), (264, 640),
+                                 (9216, 7168), (14336, 65536)])
+def test_a_workspace_serves_fewer_rows(L, N, K, x_mxfp4):
+    # whatever tiles a row count takes, and for every N and smaller K too
+    sizes = [nbytes(L, moe.MXShape.of(T, N, K, x_mxfp4=x_mxfp4)) for T in [*range(1, 300), 511, 512, 1000, 4096, 1 << 20]]
+    assert all(rc == moe.MOE_OK for rc, _ in sizes) and sizes == sorted(sizes)
+    for T in (1, 8, 9, 24, 49, 300, 4096):
+        n = nbytes(L, moe.MXShape.of(T, N, K, x_mxfp4=x_mxfp4))[1]
+        assert all(nbytes(L, moe.MXShape.of(T, m, K, x_mxfp4=x_mxfp4))[1] == n for m in (8, 1000, 6144, 1 << 20))
+        assert nbytes(L, moe.MXShape.of(T, N, max(128, K // 256 * 128), x_mxfp4=x_mxfp4))[1] <= n
+        assert nbytes(L, moe.MXShape.of(T, N, K, x_mxfp4=True))[1] <= n
