@@ -44,7 +44,11 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 
 constexpr int LM = 128;                       // weight rows a CTA
+#ifndef MOE_WAIT_TEST
 constexpr uint64_t L_WAIT_NS = 2000000000ull;
+#else
+constexpr uint64_t L_WAIT_NS = 1000000ull;    // test-only build: waits give up after 1 ms
+#endif
 constexpr int L_SITE = 300;                   // detail of MOE_ERR_TIMEOUT: site of the wait
 
 // NT tokens a tile, CG CTAs a tile.
@@ -324,6 +328,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
             // descriptors of stage 0; a stage further is STAGE / 16 more
             const uint64_t a_desc = ptx::smem_desc_sw128(ptx::smem_u32(sm)), b_desc = a_desc + C::A_BYTES / 16;
             const int n_mma = PAIR ? a.nt : NB;
+            // (it reads nothing that they wrote, but its waits' limit must not count their time)
+            pdl_wait();
             for (Segment<CG> g(a); ok && g.more(); g.next(), ++seg) {
                 const int ab = seg % ACC;
                 if (!ptx::mbar_wait_spin(&acc_empty[ab], ((seg / ACC) & 1) ^ 1, abort_flag, L_WAIT_NS)) {
@@ -1003,3 +1009,19 @@ cudaError_t launch_mx_linear(const MxDims& d, const MxArgs& a, cudaStream_t st) 
 }
 
 }  // namespace moe
+
+#ifdef MOE_WAIT_TEST
+// Test-only export of the wait-test build: a kernel of one warp that lets its successor start at once and ends `us`
+// microseconds later, for calls whose waits have a shorter limit.
+__global__ void k_test_early(int us) {
+    moe::pdl_trigger();
+    const uint64_t t0 = moe::ptx::globaltimer();
+    while (moe::ptx::globaltimer() - t0 < 1000ull * us) {
+    }
+}
+extern "C" int moe_test_early_kernel(int us, void* stream) {
+    if (us < 0 || us > 100000) return MOE_ERR_INVALID_ARG;
+    k_test_early<<<1, 32, 0, (cudaStream_t)stream>>>(us);
+    return moe::cuda_rc(cudaGetLastError());
+}
+#endif
