@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libmoe.so")
@@ -406,10 +407,38 @@ def new_mx_workspace(shape: MXShape, device="cuda", stream=None):
     return _workspace(mx_workspace_bytes(shape), device, stream)
 
 
+_mx_fields = struct.Struct("iiiIqq").unpack_from      # of an MXShape, in one step
+
+
+def _rows_fit(t, rows, width, stride) -> bool:
+    """Whether `rows` rows of `width` 16-bit elements, `stride` elements apart (0: packed), are t's: a contiguous tensor that is
+    long enough, or one whose first dimension is the rows and whose rows are each in one piece."""
+    stride = stride or width
+    if t.element_size() != 2:
+        return False
+    if t.is_contiguous():
+        return t.numel() >= (rows - 1) * stride + width
+    sizes, strides, n = t.shape, t.stride(), 1
+    for i in range(len(sizes) - 1, 0, -1):
+        if sizes[i] != 1 and strides[i] != n:
+            return False
+        n *= sizes[i]
+    return n >= width and sizes[0] >= rows and (rows == 1 or strides[0] == stride)
+
+
 def mx_linear(shape, x, xs, w, w_scales, out, ws, stream=None) -> None:
-    """out = x . w^T with MXFP4 w; x bf16 (xs None) or MXFP4 codes with scales xs; out bf16."""
-    rc = (_lib or lib()).moe_mx_linear(ctypes.byref(shape), x.data_ptr(), _ptr(xs), w.data_ptr(), w_scales.data_ptr(),
-                                       out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    """out = x . w^T with MXFP4 w; x bf16 (xs None) or MXFP4 codes with scales xs; out bf16.  Tensors that do not hold
+    what the descriptor says are refused."""
+    # (a small product is as long as this call, so the checks of packed tensors are written out)
+    T, N, K, codes, x_stride, out_stride = _mx_fields(shape)
+    if not ((x.nbytes >= T * K // 2 and x.is_contiguous() if codes else _rows_fit(x, T, K, x_stride))
+            and (xs is None or xs.nbytes >= T * K // 32 and xs.is_contiguous())
+            and w.nbytes >= N * K // 2 and w.is_contiguous() and w_scales.nbytes >= N * K // 32 and w_scales.is_contiguous()
+            and (not out_stride and out.nbytes == 2 * T * N and out.is_contiguous() or _rows_fit(out, T, N, out_stride))):
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_mx_linear (tensors that the descriptor does not describe)")
+    rc = (_lib or lib()).moe_mx_linear(shape, x.data_ptr(), None if xs is None else xs.data_ptr(), w.data_ptr(),
+                                       w_scales.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                       _raw_stream() if stream is None and _raw_stream else _stream(stream))
     if rc:
         raise MoEError(rc, "moe_mx_linear")
 

@@ -34,6 +34,7 @@
 #include "quant.cuh"
 #include "tc_ptx.cuh"
 
+#include <atomic>
 #include <math.h>
 #include <type_traits>
 
@@ -925,7 +926,13 @@ cudaError_t launch_tiles(const MxDims& d, const MxArgs& p, cudaStream_t st) {
                         : make_map(&tm_x, U8, p.ws + L.xq, 3, x_d, x_s, x_b, CU_TENSOR_MAP_SWIZZLE_128B));
     }
     if (!ok) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(k_mx_linear<XMX, NT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<bool> attribute_set[64];   // (a device's kernel attribute: set once, 0.3 us of a call)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !attribute_set[dev])) {
+        e = cudaFuncSetAttribute(k_mx_linear<XMX, NT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e == cudaSuccess && dev < 64) attribute_set[dev] = true;
+    }
     if (e != cudaSuccess) return e;
     LArgs a;
     a.w_scales = p.w_scales;

@@ -160,3 +160,75 @@ def test_a_workspace_serves_fewer_rows(L, N, K, x_mxfp4):
         assert all(nbytes(L, moe.MXShape.of(T, m, K, x_mxfp4=x_mxfp4))[1] == n for m in (8, 1000, 6144, 1 << 20))
         assert nbytes(L, moe.MXShape.of(T, N, max(128, K // 256 * 128), x_mxfp4=x_mxfp4))[1] <= n
         assert nbytes(L, moe.MXShape.of(T, N, K, x_mxfp4=True))[1] <= n
+
+
+class Product:
+    """Tensors of a product on the host: calls that the binding lets through end at the workspace, of one byte."""
+
+    def __init__(self, T=5, N=72, K=256, x_mxfp4=False, **strides):
+        import torch
+
+        def u8(*size):
+            return torch.zeros(size, dtype=torch.uint8)
+
+        self.shape = moe.MXShape.of(T, N, K, x_mxfp4=x_mxfp4, **strides)
+        self.x, self.xs = (u8(T, K // 2), u8(T, K // 32)) if x_mxfp4 else (torch.zeros(T, K, dtype=torch.bfloat16), None)
+        self.w, self.w_scales, self.out = u8(N, K // 2), u8(N, K // 32), torch.zeros(T, N, dtype=torch.bfloat16)
+
+    def code(self):
+        import torch
+        ws = torch.empty(512, dtype=torch.uint8)
+        at = -ws.data_ptr() % 256
+        with pytest.raises(moe.MoEError) as e:
+            moe.mx_linear(self.shape, self.x, self.xs, self.w, self.w_scales, self.out, ws[at:at + 1], stream=NoStream)
+        return e.value.code
+
+
+class NoStream:
+    cuda_stream = None
+
+
+@pytest.mark.parametrize("x_mxfp4", [False, True])
+def test_product_binding_refuses_tensors_too_small(L, x_mxfp4):
+    assert Product(x_mxfp4=x_mxfp4).code() == WS
+    for name in ("x", "xs", "w", "w_scales", "out"):
+        p = Product(x_mxfp4=x_mxfp4)
+        t = getattr(p, name)
+        if t is None:
+            continue
+        setattr(p, name, t[:-1])                                # a row too few
+        assert p.code() == INVALID, name
+        setattr(p, name, t[:, :-8].contiguous())                # rows too short
+        assert p.code() == INVALID, name
+        setattr(p, name, t.t().contiguous().t())                # the other way round
+        assert p.code() == INVALID, name
+        setattr(p, name, t[:1].expand_as(t))                    # one row in the place of all
+        assert p.code() == INVALID, name
+        setattr(p, name, t.repeat(2, 1)[::2])                   # rows further apart than the descriptor says
+        assert p.code() == INVALID, name
+        setattr(p, name, t.repeat(2, 1))                        # more rows than are used
+        assert p.code() == WS, name
+        setattr(p, name, t.view(-1))                            # the same bytes
+        assert p.code() == WS, name
+
+
+def test_product_binding_takes_rows_apart(L):
+    import torch
+    p = Product(x_stride=264, out_stride=96)
+    assert p.code() == INVALID                                  # packed rows
+    wide, out = torch.zeros(5, 264, dtype=torch.bfloat16), torch.zeros(5, 96, dtype=torch.bfloat16)
+    for x in (wide, wide[:, :256], wide.view(-1)[:4 * 264 + 256], wide.view(5, 33, 8)[:, :32]):
+        for o in (out, out[:, :72], out.view(-1)[:4 * 96 + 72], out.view(5, 12, 8)[:, :9]):
+            p.x, p.out = x, o
+            assert p.code() == WS
+    p.x, p.out = wide[:, :256], out[:, :64]                     # rows too short
+    assert p.code() == INVALID
+    p.out = out.view(-1)[:4 * 96 + 64]                          # the last one too short
+    assert p.code() == INVALID
+    p.out = out.float()[:, :72]                                 # of another size
+    assert p.code() == INVALID
+    p.out, p.x = out, wide.view(5, 33, 8)[:, ::2][:, :16]       # rows with gaps
+    assert p.code() == INVALID
+    p = Product(T=1)                                            # a single row, whatever stands between rows
+    p.x, p.out = wide[:1, :256], out[:1, :72]
+    assert p.code() == WS
