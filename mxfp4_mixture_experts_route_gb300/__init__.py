@@ -366,7 +366,10 @@ def _mx_rows(t, codes, scales):
     stride = 0
     if not t.is_contiguous():
         if t.dim() != 2:
-            t = t.view(-1, K)          # (raises if the rows are not evenly apart)
+            try:
+                t = t.view(-1, K)
+            except RuntimeError:
+                raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (evenly apart)") from None
         stride = t.stride(0)
         if (K > 1 and t.stride(1) != 1) or (n > K and stride < K):
             raise MoEError(MOE_ERR_INVALID_ARG, "mx rows (elements of a row side by side, rows apart)")

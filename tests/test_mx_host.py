@@ -232,3 +232,14 @@ def test_product_binding_takes_rows_apart(L):
     p = Product(T=1)                                            # a single row, whatever stands between rows
     p.x, p.out = wide[:1, :256], out[:1, :72]
     assert p.code() == WS
+
+
+def test_binding_refuses_rows_that_are_not_evenly_apart():
+    torch = pytest.importorskip("torch")
+    c, s = torch.empty(4, 2, 32, dtype=torch.uint8), torch.empty(4, 2, 2, dtype=torch.uint8)
+    for x in (torch.empty(4, 3, 64)[:, :2], torch.empty(2, 4, 64).transpose(0, 1), torch.empty(4, 2, 64).expand(1, 4, 2, 64)[:, :, [1]]
+              .expand(1, 4, 2, 64)):
+        for call in (lambda: moe.mx_quantize(x, c, s), lambda: moe.mx_dequantize(c, s, x)):
+            with pytest.raises(moe.MoEError) as e:
+                call()
+            assert e.value.code == INVALID
