@@ -555,6 +555,12 @@ int moe_mx_linear(const moe_mx_shape* shape, const void* x, const uint8_t* xs, c
                   const uint8_t* w_scales, void* out, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * How moe_mx_linear cuts a shape's work (diagnostics, pure host function; each pointer may be NULL): the CTAs
+ * (1, or 2 for a pair) and the tokens of a tile, and how many CTAs of a cluster share a tile's K.
+ */
+int moe_mx_linear_cut(const moe_mx_shape* shape, int32_t* ctas, int32_t* tokens, int32_t* parts);
+
+/*
  * Synchronises `stream`, returns the status latched in the workspace by the
  * device since the last call (MOE_OK, MOE_ERR_BAD_IDS, MOE_ERR_BAD_SCALE,
  * MOE_ERR_TIMEOUT or what the cache calls name; MOE_ERR_CUDA if the synchronisation itself failed) and

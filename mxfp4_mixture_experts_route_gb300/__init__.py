@@ -43,7 +43,7 @@ EXPORTS = ("moe_abi_version", "moe_strerror", "moe_workspace_bytes", "moe_worksp
            "moe_timing_enable", "moe_timing_collect", "moe_kernel_name", "moe_forward_noalloc",
            "moe_workspace_region", "moe_latent_workspace_bytes", "moe_latent_forward",
            "moe_kv_workspace_bytes", "moe_kv_plan", "moe_kv_append", "moe_tree_attention", "moe_qkv_append",
-           "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_workspace_bytes", "moe_mx_linear")
+           "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_workspace_bytes", "moe_mx_linear", "moe_mx_linear_cut")
 
 # workspace regions (moe_workspace_region)
 MOE_WS_STATUS, MOE_WS_POS, MOE_WS_TILES, MOE_WS_XQ, MOE_WS_XS, MOE_WS_HQ, MOE_WS_HS, MOE_WS_Y, MOE_WS_LOGITS = range(9)
@@ -165,6 +165,7 @@ def load_library(path: str) -> ctypes.CDLL:
     _MSP = ctypes.POINTER(MXShape)
     L.moe_mx_workspace_bytes.argtypes = [_MSP, ctypes.POINTER(ctypes.c_size_t)]
     L.moe_mx_linear.argtypes = [_MSP] + [_P] * 6 + [ctypes.c_size_t, _P]
+    L.moe_mx_linear_cut.argtypes = [_MSP] + [ctypes.POINTER(ctypes.c_int32)] * 3
     L.moe_timing_enable.argtypes = [ctypes.c_int]
     L.moe_timing_collect.argtypes = [_P, _P, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     L.moe_kernel_name.argtypes = [ctypes.c_int]
@@ -403,6 +404,13 @@ def mx_workspace_bytes(shape: MXShape) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().moe_mx_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "moe_mx_workspace_bytes")
     return n.value
+
+
+def mx_linear_cut(shape: MXShape) -> tuple[int, int, int]:
+    """(CTAs of a tile, tokens of a tile, CTAs of a cluster that share a tile's K) of mx_linear (diagnostics)."""
+    cut = [ctypes.c_int32(0) for _ in range(3)]
+    _check(lib().moe_mx_linear_cut(ctypes.byref(shape), *map(ctypes.byref, cut)), "moe_mx_linear_cut")
+    return tuple(c.value for c in cut)
 
 
 def new_mx_workspace(shape: MXShape, device="cuda", stream=None):

@@ -68,6 +68,16 @@ int moe_mx_workspace_bytes(const moe_mx_shape* shape, size_t* bytes) {
     return MOE_OK;
 }
 
+int moe_mx_linear_cut(const moe_mx_shape* shape, int32_t* ctas, int32_t* tokens, int32_t* parts) {
+    MxDims d;
+    const int rc = mx_dims(shape, d);
+    if (rc) return rc;
+    if (ctas) *ctas = d.cg;
+    if (tokens) *tokens = d.nt;
+    if (parts) *parts = d.split;
+    return MOE_OK;
+}
+
 int moe_mx_linear(const moe_mx_shape* shape, const void* x, const uint8_t* xs, const uint8_t* w,
                   const uint8_t* w_scales, void* out, void* ws, size_t ws_bytes, void* stream) {
     MxDims d;
