@@ -52,7 +52,6 @@ constexpr uint64_t L_WAIT_NS = 1000000ull;    // test-only build: waits give up 
 #endif
 constexpr int L_SITE = 300;                   // detail of MOE_ERR_TIMEOUT: site of the wait
 
-// NT tokens a tile, CG CTAs a tile.
 // what a CTA of a cluster of up to 8 gets at most of n groups, each in as many parts
 constexpr int most_parts(int n) {
     int most = 0;
@@ -60,6 +59,7 @@ constexpr int most_parts(int n) {
     return most;
 }
 
+// NT tokens a tile, CG CTAs a tile.
 template <bool XMX, int NT, int CG>
 struct LCfg {
     static constexpr bool FUSED = !XMX && CG == 1 && NT == 8;     // the terms of x are made here (K % 512 == 0)
@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = C::TERMS == 2 ? a.under_way : S;
-    uint8_t* xch = sm + stages * C::STAGE;    // scales: a pair's [2][8 words][NT] words, else [RING][LM + NT] rows
+    // scales: a pair's two buffers of 8 x (LM + 4) words of the weights and 8 x (NT + 4) of the tokens, else [RING][LM + NT] rows
+    uint8_t* xch = sm + stages * C::STAGE;
     // a pair's stages are counted on the even CTA's `full`, and its MMAs' ends on both CTAs' barriers
     uint64_t* full = reinterpret_cast<uint64_t*>(xch + C::XCH_BYTES);
     uint64_t* empty = full + S;          // the stage's MMAs are done
@@ -499,7 +500,8 @@ __global__ void __launch_bounds__(LCfg<XMX, NT, CG>::THREADS, 1)
                 }
             }
         };
-        // its 8 bytes of stage k; a row's bytes past K (of the next row, or zeros) meet codes that are zeros
+        // its 8 bytes of stage k.  Where K ends in half a stage the second word is the next row's first scales: a 0 in
+        // its place, because the codes there are zeros, but a 255 (NaN) of that row times zero is NaN
         auto words = [&](const uint8_t* p, int n, int rows, int k) {
             if (a.vec) return *reinterpret_cast<const uint2*>(p + 8 * (k & 1));
             const uint32_t* w = reinterpret_cast<const uint32_t*>(p + ((int64_t)min(n, rows - 1) * kb & 15) + 8 * (k & 1));

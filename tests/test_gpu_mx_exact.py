@@ -82,3 +82,25 @@ def test_sums_leave_nothing_out(T, N, K, kind):
     out, work = product(x, xs, w, ws, T, N, K, kind)
     moe.check_device_status(work, "mx_linear")
     assert torch.equal(out, want.bfloat16())
+
+
+# K ends in half a stage: the scale bytes behind a row's are the next row's first, over codes that are zeros
+@pytest.mark.parametrize("kind", ["mxfp4", "bf16"])
+@pytest.mark.parametrize("T", [4, 20, 40, 100, 300])
+@pytest.mark.parametrize("N,K", [(136, 640), (264, 384), (392, 1152), (4104, 128)])
+def test_a_row_of_nan_leaves_the_row_before_it(T, N, K, kind):
+    x, xs, w, ws, want = signs(T, N, K, kind)
+    bad_t, bad_n = [2, T - 1], [1, 77, N - 1]
+    for i, t in enumerate(bad_t):
+        if kind == "mxfp4":
+            xs[t, i:i + 2] = 255                    # among the row's first four scale bytes
+        else:
+            x[t, 32 * i + 5] = x[t, 32 * i + 90] = float("inf")
+    for i, n in enumerate(bad_n):
+        ws[n, i] = 255
+    out, work = product(x, xs, w, ws, T, N, K, kind)
+    assert moe.device_status(work) == (moe.MOE_ERR_BAD_SCALE, 255)
+    nan = torch.zeros(T, N, dtype=torch.bool, device=DEV)
+    nan[bad_t], nan[:, bad_n] = True, True
+    assert torch.equal(out.isnan(), nan)
+    assert torch.equal(out[~nan], want.bfloat16()[~nan])
