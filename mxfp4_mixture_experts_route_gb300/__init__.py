@@ -1,6 +1,7 @@
 """Python binding of libmoe, the routed MXFP4 mixture-of-experts block on GB300.
 
-Argument marshalling only: every step of the block runs in the library's CUDA
+Argument marshalling only (and, for the dense MXFP4 calls, a check that the tensors
+hold what the call says of them): every step of the block runs in the library's CUDA
 kernels.  Tensors are PyTorch CUDA tensors (device memory and streams come from
 PyTorch); the calls are the C entry points of include/moe.h under the same
 names without the ``moe_`` prefix.  There is no CPU fallback: if libmoe.so is

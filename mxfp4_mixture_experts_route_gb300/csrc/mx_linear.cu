@@ -6,7 +6,9 @@
 // a power of two a block of 32, which the scale warps make in shared memory (up to 8 tokens) or a
 // small kernel (k_mx_split) writes first; the TMA
 // unpacks the weights' codes for kind::mxf8f6f4.  Either way the tensor core applies the
-// block scales.
+// block scales.  (Two terms are fewer bits than a bf16 has where a block's magnitudes are far apart: exact to 2^-9 of the
+// largest, within 2^-17 of it below.  It is the price of weights that go in as codes and scales: for a
+// product in bf16 they are decoded first, to twice the bytes in shared memory.)
 //
 // Few tokens: one CTA a tile of 128 weight rows x NT tokens; a token of a bf16 x takes
 // two columns of the MMA, added at the end.  Many: a pair of CTAs (cta_group::2) a tile of
@@ -25,8 +27,8 @@
 // products, the chain of a launch (1.2 us from the wait for earlier kernels to the first MMA, 1.2 for the sum over a
 // cluster) and the stages' own pace (some 500 cycles: barrier, fences, four MMAs and their commit, whatever the tokens);
 // with many tokens and a bf16 x the tensor cores (4096 x 4864 x 4096: 92 us, 1770 TFLOP/s, 0.91 of the
-// measured bf16 rate); with both operands at 4 bits the copies, scales and stores beside MMAs that alone
-// take 197 of 257 us (8192 x 14336 x 7168: 6550 TFLOP/s).
+// measured bf16 rate); with both operands at 4 bits the K = 64 MMAs, which alone take 197 of 257 us, and the copies,
+// scales and stores beside them (8192 x 14336 x 7168: 6550 TFLOP/s).
 //
 // Warps: 0 TMA, 1 MMA, 2-5 scales (global memory -> shared memory or registers -> TMEM), from 6 on the accumulators' way
 // out (four, or eight of a pair's CTA), then a second set of scale warps.
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(split_threads(PIECES)) k_mx_split(const __nv_b
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-constexpr int L_CTAS = 152;   // a GB300's SMs
+constexpr int L_CTAS = 152;   // a GB300's SMs (with fewer the cuts are right all the same, but chosen for these)
 // How many clusters of 0 .. 8 such CTAs (one an SM) a GB300 runs at once (cudaOccupancyMaxActiveClusters)
 constexpr int CLUSTERS[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 }  // namespace
