@@ -423,19 +423,24 @@ _mx_fields = struct.Struct("iiiIqq").unpack_from      # of an MXShape, in one st
 
 
 def _rows_fit(t, rows, width, stride) -> bool:
-    """Whether `rows` rows of `width` 16-bit elements, `stride` elements apart (0: packed), are t's: a contiguous tensor that is
-    long enough, or one whose first dimension is the rows and whose rows are each in one piece."""
+    """Whether `rows` rows of `width` 16-bit elements, `stride` elements apart (0: packed), are t's, in its elements' order."""
     stride = stride or width
     if t.element_size() != 2:
         return False
     if t.is_contiguous():
         return t.numel() >= (rows - 1) * stride + width
-    sizes, strides, n = t.shape, t.stride(), 1
-    for i in range(len(sizes) - 1, 0, -1):
-        if sizes[i] != 1 and strides[i] != n:
-            return False
-        n *= sizes[i]
-    return n >= width and sizes[0] >= rows and (rows == 1 or strides[0] == stride)
+    sizes, strides = t.shape, t.stride()
+    i, piece = len(sizes), 1                             # the last dimensions that are in one piece
+    while i and (sizes[i - 1] == 1 or strides[i - 1] == piece):
+        i -= 1
+        piece *= sizes[i]
+    if piece >= (rows - 1) * stride + width:
+        return True
+    count = 1                                            # those before them: rows evenly apart
+    while i and (sizes[i - 1] == 1 or strides[i - 1] == stride * count):
+        i -= 1
+        count *= sizes[i]
+    return piece >= width and count >= rows
 
 
 def mx_linear(shape, x, xs, w, w_scales, out, ws, stream=None) -> None:

@@ -243,3 +243,24 @@ def test_binding_refuses_rows_that_are_not_evenly_apart():
             with pytest.raises(moe.MoEError) as e:
                 call()
             assert e.value.code == INVALID
+
+
+def test_product_binding_takes_rows_of_more_dimensions(L):
+    import torch
+    p = Product(T=6, x_stride=264, out_stride=96)
+    wide, out = torch.zeros(2, 3, 264, dtype=torch.bfloat16), torch.zeros(2, 3, 96, dtype=torch.bfloat16)
+    p.x, p.out = wide[:, :, :256], out[:, :, :72]               # evenly apart through both dimensions
+    assert p.code() == WS
+    p.x, p.out = wide.view(6, 1, 33, 8)[:, :, :32], out.view(2, 3, 1, 12, 8)[..., :9, :]
+    assert p.code() == WS
+    p.x = torch.zeros(2, 4, 264, dtype=torch.bfloat16)[:, :3, :256]     # a gap behind every third row
+    assert p.code() == INVALID
+    p.x = torch.zeros(2, 8, 264, dtype=torch.bfloat16)[:, :6, :256]     # as above, but six before the gap
+    assert p.code() == WS
+    p.x = torch.zeros(3, 2, 264, dtype=torch.bfloat16).transpose(0, 1)[..., :256]
+    assert p.code() == INVALID
+    p = Product(T=6)
+    p.x = torch.zeros(2, 8, 256, dtype=torch.bfloat16)[:, :6]           # packed rows, six of them in one piece
+    assert p.code() == WS
+    p.x = torch.zeros(2, 8, 256, dtype=torch.bfloat16)[:, :5]
+    assert p.code() == INVALID
